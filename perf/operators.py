@@ -271,6 +271,7 @@ def prepare(case, seed):
         s["b_scales"] = b.abs().amax((1, 3)) / E4M3_MAX
         s["b"] = (b / s["b_scales"][:, None, :, None]).to(f8).view(nb * BLOCK, kb * BLOCK)[:n, :k].contiguous()
         s["out"] = torch.empty((m, n), device=DEV, dtype=dt)
+        s["status"] = torch.zeros(1, device=DEV, dtype=torch.int32)
     return s
 
 
@@ -401,7 +402,7 @@ def own_attention(awq, s, case):
 
 
 def own_gemm(awq, s, case):
-    awq.fp8_gemm(s["a"], s["a_scales"], s["b"], s["b_scales"], s["out"])
+    awq.fp8_gemm(s["a"], s["a_scales"], s["b"], s["b_scales"], s["out"], s["status"])
     return {"out": s["out"]}
 
 
