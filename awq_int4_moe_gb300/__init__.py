@@ -1,6 +1,8 @@
 """Python binding of the GB300 AWQ int4 MoE expert-stage library.
 
-Thin marshalling layer over the C ABI in ``include/awq_moe.h``: every
+Thin marshalling layer over the C ABI in ``include/awq_moe.h`` (the expert
+stage) and ``include/awq_decoder.h`` (the decoder layer around it: norm,
+8-bit quantisation and product, rotary cache append, paged attention): every
 function here has the same name as its C entry point (without the ``awq_``
 prefix), passes ``tensor.data_ptr()`` and the current CUDA stream through
 ctypes, and raises :class:`AwqError` on a non-zero status. All computation
@@ -24,6 +26,7 @@ STATIC_SCRATCH_BYTES = 2 << 20   # AWQ_STATIC_SCRATCH_BYTES
 # awq_status
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, ERR_MISALIGNED, ERR_CUDA = 0, 1, 2, 3, 4
 ERR_DEVICE_TIMEOUT, ERR_BAD_EXPERT_ID, ERR_WORKSPACE_TOO_SMALL, ERR_LAYOUT = 5, 6, 7, 8
+ERR_BAD_INDEX = 9
 
 # awq_layout
 LAYOUT_CANONICAL, LAYOUT_PREPARED = 0, 1
@@ -115,6 +118,7 @@ def lib() -> C.CDLL:
         L.awq_moe_layer_static.argtypes = [P, P, P, i32, SP, WP, P, P, P]
         L.awq_moe_latency_floor.restype = C.c_int
         L.awq_moe_latency_floor.argtypes = [P, i32, SP, WP, P, P, C.c_size_t, P, P]
+        decoder.declare(L)
         _lib = L
     return _lib
 
@@ -324,3 +328,8 @@ def moe_latency_floor(topk_ids, M: int, shape, weights: Weights, out, workspace,
                  workspace=(workspace, "bytes", int(ws_bytes)), dev_status=(dev_status, "i32", 1))
     _check(lib().awq_moe_latency_floor(a["topk_ids"], M, C.byref(s), C.byref(weights), a["out"], a["workspace"],
                                        int(ws_bytes), a["dev_status"], _stream(stream)), "awq_moe_latency_floor")
+
+
+from . import decoder  # noqa: E402
+from .decoder import (DTYPE_BF16, DTYPE_E4M3, DTYPE_F16, FP8_BLOCK, add_rmsnorm, fp8_gemm,  # noqa: E402,F401
+                      paged_attention, paged_attention_workspace_bytes, quantize_fp8, rope_append)

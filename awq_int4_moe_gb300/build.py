@@ -19,9 +19,11 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libawqmoe.so")
 SOURCES = ["awq_moe_api.cu", "awq_moe_route.cu", "awq_moe_gemm.cu", "awq_moe_fused.cu", "awq_moe_prepare.cu",
            "awq_moe_sliced.cu", "awq_moe_tc.cu",
-           "awq_moe_floor.cu"]
+           "awq_moe_floor.cu", "awq_decoder_api.cu", "awq_norm.cu", "awq_rope.cu", "awq_attn.cu",
+           "awq_fp8_gemm.cu"]
 HEADERS = ["awq_ptx.cuh", "awq_moe_kernels.cuh", "awq_launch.cuh", "awq_dequant.cuh", "awq_route.cuh",
-           "awq_router.cuh", "awq_split.cuh", "awq_tc.cuh", "awq_nvfp4.cuh"]
+           "awq_router.cuh", "awq_split.cuh", "awq_tc.cuh", "awq_nvfp4.cuh",
+           "awq_decoder_kernels.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -45,7 +47,8 @@ def _stale(target: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     deps_common = [os.path.join(CSRC, h) for h in HEADERS] + [
-        os.path.join(ROOT, "include", "awq_moe.h"), os.path.abspath(__file__)]
+        os.path.join(ROOT, "include", "awq_moe.h"), os.path.join(ROOT, "include", "awq_decoder.h"),
+        os.path.abspath(__file__)]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -1,0 +1,226 @@
+// Kernel-side declarations of the decoder-layer operators (awq_decoder.h):
+// argument blocks, launchers and the conversions they share.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/awq_decoder.h"
+#include "awq_ptx.cuh"
+
+namespace awq {
+
+// ------------------------------------------------------------ conversions
+
+// One 16-bit activation as fp32 and back (round to nearest even).
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v)
+{
+    return __float2half_rn(v);
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v)
+{
+    return __float2bfloat16_rn(v);
+}
+
+// Two fp32 values as a 16-bit pair, `lo` in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A 16-bit pair as two fp32 values.
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v)
+{
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+// Two fp32 values as an e4m3 pair, `lo` in the low byte (nearest even,
+// saturating at +-448; NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d)
+{
+    return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
+}
+
+// N (1, 4 or 8) consecutive 16-bit elements; 4 and 8 in one aligned access.
+template <typename T, int N>
+__device__ __forceinline__ void load_elems(const T *p, float (&f)[N])
+{
+    if constexpr (N == 8) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack2<T>(w[i]);
+            f[2 * i] = x.x;
+            f[2 * i + 1] = x.y;
+        }
+    } else if constexpr (N == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        const float2 x = unpack2<T>(v.x), y = unpack2<T>(v.y);
+        f[0] = x.x;
+        f[1] = x.y;
+        f[2] = y.x;
+        f[3] = y.y;
+    } else {
+        static_assert(N == 1, "1, 4 or 8 elements");
+        f[0] = to_f32(*p);
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_elems(T *p, const float (&f)[N])
+{
+    if constexpr (N == 8) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
+                                                   pack2<T>(f[6], f[7]));
+    } else if constexpr (N == 4) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+    } else {
+        static_assert(N == 1, "1, 4 or 8 elements");
+        *p = from_f32<T>(f[0]);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[N])
+{
+    if constexpr (N == 8) {
+        *reinterpret_cast<uint2 *>(p) =
+            make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
+    } else if constexpr (N == 4) {
+        *reinterpret_cast<uint32_t *>(p) = pack_e4m3x4(f[0], f[1], f[2], f[3]);
+    } else {
+        static_assert(N == 1, "1, 4 or 8 elements");
+        *p = static_cast<uint8_t>(pack_e4m3x2(f[0], 0.f));
+    }
+}
+
+// A group's scale and the factor its values are multiplied by.
+__device__ __forceinline__ float2 group_scale(float amax)
+{
+    const float a = fmaxf(amax, AWQ_FP8_MIN_AMAX);
+    return make_float2(a / 448.f, 448.f / a);
+}
+
+// ---------------------------------------------------------- argument blocks
+
+struct NormArgs {
+    const void *x, *residual, *weight;
+    void *residual_out, *out;
+    uint8_t *out_q;
+    float *out_scales;
+    int64_t ldx, ldr, ldro, ldo, ldq;
+    float eps;
+    int32_t rows, hidden;
+};
+
+struct QuantArgs {
+    const void *x;
+    uint8_t *q;
+    float *scales;
+    int64_t ldx, ldq;
+    int32_t rows, cols;
+};
+
+struct RopeArgs {
+    awq_heads q, q_out, k, v;
+    const int32_t *positions;
+    const float *cos_sin;
+    const int64_t *slots;
+    awq_kv_cache cache;
+    int32_t *status;
+    int32_t max_positions, rotary_dim, interleaved, tokens, q_heads;
+};
+
+struct AttnArgs {
+    awq_heads q, out;
+    awq_kv_cache cache;
+    const int32_t *page_table;
+    const int32_t *seq_lens;
+    float *lse;
+    int32_t *counters;     // [kAttnMaxCtas], zero between calls
+    float *parts;          // split pieces, see awq_attn.cu
+    int32_t *status;
+    int64_t table_stride;
+    int32_t max_pages, batch, q_heads, group, row_tiles;
+    float scale;
+};
+
+struct GemmArgs {
+    const float *a_scales, *b_scales;
+    void *out;
+    int64_t ldo;
+    int32_t *status;
+    int32_t M, N, K;
+    uint64_t timeout_ns;
+};
+
+// ---------------------------------------------------------------- launchers
+
+// Vectors of 16 bytes where `wide`, else any size and alignment.
+awq_status launch_norm(const NormArgs &a, int dtype, bool wide, int sms, cudaStream_t st);
+awq_status launch_quantize(const QuantArgs &a, int dtype, bool wide, int sms, cudaStream_t st);
+// vec: elements per access (8, 4 or 1).
+awq_status launch_rope(const RopeArgs &a, int dtype, int vec, cudaStream_t st);
+
+// The attention's grid never exceeds this many blocks (its workspace holds
+// two pieces and one counter for each).
+constexpr int kAttnMaxCtas = 320;
+constexpr int kAttnRows = 16;          // query heads of one tile
+constexpr size_t kAttnCounterBytes = (kAttnMaxCtas * sizeof(int32_t) + 255) / 256 * 256;
+// Padded head size of the kernel that takes `dim`.
+constexpr int attn_padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+constexpr size_t attn_workspace_bytes(int dim)
+{
+    return kAttnCounterBytes +
+           static_cast<size_t>(kAttnMaxCtas) * 2 * kAttnRows * (attn_padded_dim(dim) + 2) * sizeof(float);
+}
+awq_status launch_attention(const AttnArgs &a, int dtype, int sms, cudaStream_t st);
+
+awq_status launch_fp8_gemm(const GemmArgs &g, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int dtype,
+                           int sms, cudaStream_t st);
+
+// awq_moe_api.cu
+int current_sm_count();
+bool encode_tensor_map(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *base, const cuuint64_t *dims,
+                       const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swz,
+                       CUtensorMapL2promotion l2);
+
+}  // namespace awq

@@ -80,6 +80,8 @@ awq_status check_weights(const awq_moe_weights *w)
     return w->layout == AWQ_LAYOUT_PREPARED ? AWQ_OK : AWQ_ERR_LAYOUT;
 }
 
+}  // namespace
+
 // Multiprocessor count of the current device, looked up once per device
 // (atomic entries: host threads may call concurrently).
 int current_sm_count()
@@ -96,6 +98,8 @@ int current_sm_count()
     if (dev < 64) cache[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
+
+namespace {
 
 awq_status check_m(int32_t M)
 {
@@ -124,15 +128,26 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-bool encode(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *base,
-            const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
-            CUtensorMapSwizzle swz, CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+}  // namespace
+
+bool encode_tensor_map(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *base,
+                        const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                        CUtensorMapSwizzle swz, CUtensorMapL2promotion l2)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return fn(m, dt, rank, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, swz, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+bool encode(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *base,
+            const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+            CUtensorMapSwizzle swz, CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+{
+    return encode_tensor_map(m, dt, rank, base, dims, strides, box, swz, l2);
 }
 
 // Prepared W2 banks are viewed as 2D arrays of 128-byte q lines and 32-record
@@ -467,8 +482,9 @@ const char *awq_status_string(awq_status st)
     case AWQ_ERR_CUDA: return "CUDA runtime or driver call failed";
     case AWQ_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
     case AWQ_ERR_BAD_EXPERT_ID: return "expert id outside [0, num_experts)";
-    case AWQ_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than awq_moe_workspace_bytes()";
+    case AWQ_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than the call needs";
     case AWQ_ERR_LAYOUT: return "weight banks are not in the layout the call needs";
+    case AWQ_ERR_BAD_INDEX: return "position, cache slot, page or length outside its array";
     }
     return "unknown status";
 }

@@ -109,7 +109,9 @@ typedef enum {
     AWQ_ERR_DEVICE_TIMEOUT = 5,     /* a bounded device wait ran out (dev_status) */
     AWQ_ERR_BAD_EXPERT_ID = 6,      /* expert id outside [0, E) (dev_status)    */
     AWQ_ERR_WORKSPACE_TOO_SMALL = 7, /* ws_bytes below awq_moe_workspace_bytes  */
-    AWQ_ERR_LAYOUT = 8              /* weight banks in the wrong layout         */
+    AWQ_ERR_LAYOUT = 8,             /* weight banks in the wrong layout         */
+    AWQ_ERR_BAD_INDEX = 9           /* position, slot, page or length outside its array
+                                       (dev_status; the calls of awq_decoder.h) */
 } awq_status;
 
 /* Layout of a weight bank set. */
