@@ -1,38 +1,42 @@
 // awq_paged_attention: one new token per sequence over the paged cache.
 //
-// Work is counted in units of 16 cached tokens of one (sequence, KV head, tile
-// of query heads), a segment, numbered segment by segment; block c of G takes
-// units [c * per, (c + 1) * per), whatever segments they belong to, so every
-// block reads the same number of cache bytes however ragged the batch is. A
-// segment that lies inside one block is finished there; one that is cut leaves
-// a piece (running maximum, sum, unnormalised output, all fp32) per block in
-// the workspace, and the block that finishes last joins the pieces in block
-// order, so the result does not depend on which one that is.
+// Work is counted in units of KT cached tokens (8 KB of K and V where a row
+// is at most 256 bytes) of one segment: a (sequence, KV head, tile of query
+// heads). Units are numbered segment by segment, and every warp of the grid
+// takes the same number of consecutive ones, whatever segments they belong
+// to, so that all read the same number of cache bytes however ragged the
+// batch is. A segment that lies inside a warp's range is finished there; what
+// is cut leaves parts (running maximum, sum, unnormalised output, all fp32):
+// the block's four warps join theirs in shared memory at the end, and a
+// segment that is cut between blocks leaves a piece per block in the
+// workspace, joined in block order by the block that finishes last (so the
+// result does not depend on which one that is). No warp waits for another
+// before that.
 //
-// Within a block each warp works alone: units go to the warps round-robin,
-// each warp copies its unit's 16 K and 16 V rows (cp.async, 16 bytes a lane,
-// STAGES units deep, running on into the next segment) and keeps its own
-// maximum, sum and output; the warps' results are merged per segment.
-//
-// Per unit and warp, with up to 16 query heads as the rows of the tensor-core
-// tile (mma.m16n8k16, fp32 accumulators):
-//   S[16 x 16]  = Q K^T, K rows read with ldmatrix as the B operand
-//   m' = max(m, rowmax S), P = exp2(S - m'), l = l * 2^(m - m') + sum P
-//   O[16 x D]   = O * 2^(m - m') + P V, V rows read with ldmatrix.trans
-// S is scaled to base-2 logarithms in fp32. P enters the tensor core as two
-// 16-bit terms, P = hi + lo, so its rounding does not reach the output: with
-// at most 8 query heads the lo terms are rows 8-15 of the same tile (free),
-// else they are a second product.
+// A warp copies its units' rows with cp.async (16 bytes a lane, several units
+// deep, running on into the next segment). With up to 8 query heads as the
+// columns of the tensor-core tile (mma.m16n8k16, fp32 accumulators; 9 to 16
+// heads are two tiles):
+//   S'[16 tokens x 8] = K Q', K's rows read with ldmatrix as the A operand
+//   m' = max(m, S), P = exp2(S - m'), l = l * 2^(m - m') + sum P
+//   O'[16 of D x 8]   = O' * 2^(m - m') + V' P', V read with ldmatrix.trans
+// so no row of the tile is padding at 8 heads, a head's statistics and its
+// output are in the same lanes, and P moves from the accumulator's layout to
+// the B operand's with movmatrix. m is raised only where a score passes it by
+// more than 2^8 (P stays below 2^8, the sums are fp32), which drops both the
+// search for the maximum and the scaling of O' from nearly every unit. P
+// enters the tensor core as two 16-bit terms, P = hi + lo, so that its
+// rounding does not reach the output.
 //
 // e4m3 planes are expanded to fp16 in registers (exact): a 4-byte lane of an
 // ldmatrix row holds 4 neighbouring elements of the head, so Q's elements are
 // dealt to the fragments in the same order (the dot product does not care),
-// and V's columns come out in an order that the output's store undoes. bf16 Q
-// becomes fp16 with its row's power of two taken out (exact to 2^-24 of the
-// row's largest element).
+// and V's rows of O' come in an order that the store undoes. bf16 Q becomes
+// fp16 with its head's power of two taken out (exact to 2^-24 of the head's
+// largest element).
 //
 // Bound: 4 * group operations per cached element of 1 or 2 bytes, so the
-// bytes decide; mma.sync at 16 rows has a few times the rate that they need.
+// bytes decide; the tensor-core tiles have a few times the rate they need.
 #include <algorithm>
 #include <type_traits>
 
@@ -43,10 +47,10 @@ namespace awq {
 
 namespace {
 
-constexpr int kUnit = 16;              // cached tokens of a unit
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = kWarps * 32;
-constexpr int kLens = 128;             // sequence lengths kept in shared memory
+constexpr int kLens = 64;              // sequence lengths kept in shared memory
+constexpr float kLazy = 8.f;           // a score raises the maximum when it passes it by this (base 2)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -91,11 +95,20 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes as an fp16 pair (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
+// Four e4m3 codes as two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+
+// 8x8 16-bit matrix across the warp, transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v)
 {
     uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 
@@ -115,38 +128,43 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
     lo = pack2<C>(a - h.x, b - h.y);
 }
 
-__device__ __forceinline__ float quad_max(float v)
+// Reductions over the eight lanes that hold a head's column.
+__device__ __forceinline__ float col_max(float v)
 {
-    v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
-    return fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+    v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+    return fmaxf(v, __shfl_xor_sync(~0u, v, 16));
 }
-__device__ __forceinline__ float quad_sum(float v)
+__device__ __forceinline__ float col_sum(float v)
 {
-    v += __shfl_xor_sync(~0u, v, 1);
-    return v + __shfl_xor_sync(~0u, v, 2);
+    v += __shfl_xor_sync(~0u, v, 4);
+    v += __shfl_xor_sync(~0u, v, 8);
+    return v + __shfl_xor_sync(~0u, v, 16);
 }
 
 struct BatchView {
     const int32_t *seq_lens;
     const int32_t *s_len;     // lengths of sequences b0 .. b0 + kLens - 1
-    int b0, batch, max_len;
+    int b0, max_len;
     int per_seq;              // segments of a sequence: KV heads x head tiles
 
+    __device__ __forceinline__ int clamp(int n) const { return n < 0 ? 0 : n > max_len ? max_len : n; }
     __device__ __forceinline__ int len(int b) const
     {
         const int i = b - b0;
-        const int n = i < kLens ? s_len[i] : seq_lens[b];
-        return n < 0 ? 0 : n > max_len ? max_len : n;
+        return clamp(i < kLens ? s_len[i] : seq_lens[b]);
     }
 };
 
-// A position in the flat order of units: segment (b, s) of n tokens, unit u.
+// A position in the flat order of units: segment s of sequence b (n tokens),
+// unit u.
+template <int KT>
 struct Cursor {
     int b, s, n, u;
-    int64_t left;             // units from u to the end of the block's range
+    int64_t left;             // units from u to the end of the warp's range
 
-    __device__ __forceinline__ int units() const { return (n + kUnit - 1) / kUnit; }
-    // the segment's units that belong to the block: [u, end())
+    __device__ __forceinline__ int units() const { return (n + KT - 1) / KT; }
+    // the segment's units that belong to the warp: [u, end())
     __device__ __forceinline__ int end() const
     {
         const int e = units();
@@ -168,23 +186,25 @@ struct Cursor {
     }
 };
 
-template <bool FP8, int DP, bool GS8>
+// NT: tiles of 8 query heads.
+template <bool FP8, int DP, int NT>
 struct Geo {
     static constexpr int kElem = FP8 ? 1 : 2;
     static constexpr int kRow = DP * kElem;             // bytes of a token's row in shared memory
     static constexpr int kChunks = kRow / 16;
-    static constexpr int kPlane = kUnit * kRow;
+    static constexpr int KT = kRow >= 256 ? 16 : 4096 / kRow;    // tokens of a unit
+    static constexpr int kPlane = KT * kRow;
     static constexpr int kStage = 2 * kPlane;           // K rows, then V rows
-    static constexpr int kRows = GS8 ? 8 : 16;          // query heads of a tile
-    static constexpr int kBlocks = kStage >= 16384 ? 1 : 2;      // resident per multiprocessor
-    static constexpr int kMergeRow = DP + 2;            // output, maximum, sum
-    static constexpr int kMerge = 2 * kRows * kMergeRow * 4;
-    // as many units in flight as a block's share of shared memory holds
-    static constexpr int kShare = (kBlocks == 1 ? 227 : 112) * 1024 + (kBlocks == 1 ? 0 : 640);
-    static constexpr int kFit = (kShare - kMerge) / (kWarps * kStage);
-    static constexpr int kStages = kFit > 8 ? 8 : kFit;
-    static constexpr int kSmem = kWarps * kStages * kStage + kMerge;
-    static_assert(kStages >= 2, "a unit in flight beside the one in use");
+    static constexpr int kPitch = attn_part_pitch(DP);  // floats of a part's row: output, maximum, sum
+    static constexpr int kPart = 8 * NT * kPitch * 4;   // bytes
+    // as many units in flight as a block's share of shared memory holds: two
+    // blocks per multiprocessor where each has two units per warp
+    static constexpr int kFit2 = (115200 - kWarps * kPart) / (kWarps * kStage);
+    static constexpr int kBlocks = kFit2 >= 2 ? 2 : 1;
+    static constexpr int kFit = kBlocks == 2 ? kFit2 : (231424 - kWarps * kPart) / (kWarps * kStage);
+    static constexpr int kStages = kFit > 4 ? 4 : kFit;
+    static constexpr int kSmem = kWarps * (kStages * kStage + kPart);
+    static_assert(kStages >= 2 && kStages * kStage >= kPart, "a unit in flight beside the one in use");
 
     // 16-byte chunk c of row r, placed so that 8 rows of one chunk fall into
     // different banks
@@ -195,37 +215,45 @@ struct Geo {
     }
 };
 
-template <typename T, bool FP8, int DP, bool GS8>
-__global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, GS8>::kBlocks) attn_kernel(const AttnArgs a)
+// A part of a segment, left by a warp.
+struct PartMeta {
+    int64_t seg_begin;        // flat number of the segment's first unit; -1: none
+    int32_t b, s;
+};
+
+template <typename T, bool FP8, int DP, int NT>
+__global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, NT>::kBlocks) attn_kernel(const AttnArgs a)
 {
-    using G = Geo<FP8, DP, GS8>;
+    using G = Geo<FP8, DP, NT>;
     using C = typename std::conditional<FP8, __half, T>::type;   // the tensor core's type
-    constexpr int KS = DP / 16;                                   // 16-element steps of a head
+    constexpr int KS = DP / 16, KT = G::KT, SUB = KT / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int32_t s_len[kLens];
-    __shared__ int64_t s_scan[kWarps + 1];
+    __shared__ int64_t s_scan[kWarps];
     __shared__ int64_t s_first[2];                                // first sequence of the block, units before it
+    __shared__ PartMeta s_meta[2 * kWarps];
     __shared__ int32_t s_ticket;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     const awq_kv_cache &c = a.cache;
     const int D = c.head_dim;
-    float *const merge = reinterpret_cast<float *>(smem + kWarps * G::kStages * G::kStage);
     uint8_t *const ring = smem + warp * G::kStages * G::kStage;
     const uint32_t ring_addr = smem_u32(ring);
+    float *const own_part = reinterpret_cast<float *>(smem + kWarps * G::kStages * G::kStage + warp * G::kPart);
 
     // chunks past the head's end are never copied: they stay zero
-    for (int i = lane; i < G::kStages * G::kStage / 16; i += 32)
-        reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
+    if (D != DP)
+        for (int i = lane; i < G::kStages * G::kStage / 16; i += 32)
+            reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
 
     BatchView view;
     view.seq_lens = a.seq_lens;
     view.s_len = s_len;
-    view.batch = a.batch;
+    view.b0 = 0;
     {
         const int64_t most = static_cast<int64_t>(a.max_pages) * c.page_size;
-        view.max_len = most > 0x7fffffe0 ? 0x7fffffe0 : static_cast<int>(most);
+        view.max_len = most > 0x7fffffc0 ? 0x7fffffc0 : static_cast<int>(most);
     }
     view.per_seq = c.num_heads * a.row_tiles;
 
@@ -237,12 +265,10 @@ __global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, GS8>::kBlocks) attn
     const int b_lo = tid * per_thread, b_hi = min(a.batch, b_lo + per_thread);
     int64_t mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
-        int n = a.seq_lens[b];
-        if (n < 0 || n > view.max_len) {
-            if (blockIdx.x == 0) set_status(a.status, AWQ_ERR_BAD_INDEX);
-            n = n < 0 ? 0 : view.max_len;
-        }
-        mine += (n + kUnit - 1) / kUnit;
+        const int raw = a.seq_lens[b], n = view.clamp(raw);
+        if (n != raw && blockIdx.x == 0) set_status(a.status, AWQ_ERR_BAD_INDEX);
+        if (b < kLens) s_len[b] = n;
+        mine += (n + KT - 1) / KT;
         // a sequence without tokens: zeros, spread over the blocks
         if (n == 0 && b % gridDim.x == blockIdx.x) {
             for (int h = 0; h < a.q_heads; ++h) {
@@ -260,6 +286,7 @@ __global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, GS8>::kBlocks) attn
         if (lane >= o) incl += y;
     }
     if (lane == 31) s_scan[warp] = incl;
+    if (tid < 2 * kWarps) s_meta[tid].seg_begin = -1;
     __syncthreads();
     int64_t total = 0, before = incl - mine;
 #pragma unroll
@@ -267,86 +294,102 @@ __global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, GS8>::kBlocks) attn
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
-    // at least a unit per warp, and whole rounds of the warps
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    per = (per + kWarps - 1) / kWarps * kWarps;
-    const int64_t begin = blockIdx.x * per;
+    const int64_t per_warp = (total + static_cast<int64_t>(gridDim.x) * kWarps - 1) / (static_cast<int64_t>(gridDim.x) * kWarps);
+    const int64_t per = per_warp * kWarps;
+    const int64_t begin = blockIdx.x * per, block_end = min(total, begin + per);
     if (begin >= total) return;
     if (begin >= before && begin < before + mine) {
         int b = b_lo;
         int64_t at = before;
-        while (true) {
-            int n = a.seq_lens[b];
-            n = n < 0 ? 0 : n > view.max_len ? view.max_len : n;
-            const int64_t u = static_cast<int64_t>((n + kUnit - 1) / kUnit) * view.per_seq;
+        for (; b < b_hi - 1; ++b) {
+            const int64_t u = static_cast<int64_t>((view.clamp(a.seq_lens[b]) + KT - 1) / KT) * view.per_seq;
             if (begin < at + u) break;
             at += u;
-            ++b;
         }
         s_first[0] = b;
         s_first[1] = at;
     }
     __syncthreads();
-    view.b0 = static_cast<int>(s_first[0]);
-    for (int i = tid; i < kLens; i += kAttnThreads) s_len[i] = view.b0 + i < a.batch ? a.seq_lens[view.b0 + i] : 0;
-    __syncthreads();
-
-    Cursor seg;                          // the segment being computed
-    seg.b = view.b0;
+    int64_t local = begin + warp * per_warp - s_first[1];
+    Cursor<KT> seg;                      // the segment being computed
+    seg.b = static_cast<int>(s_first[0]);
+    if (a.batch > kLens) {
+        view.b0 = seg.b;
+        if (tid < kLens) s_len[tid] = view.b0 + tid < a.batch ? a.seq_lens[view.b0 + tid] : 0;
+        __syncthreads();
+    }
+    seg.left = max(static_cast<int64_t>(0), min(per_warp, total - begin - warp * per_warp));
     seg.n = view.len(seg.b);
-    {
-        const int64_t local = begin - s_first[1];
+    seg.s = seg.u = 0;
+    if (seg.left > 0) {
+        while (true) {
+            const int64_t u = static_cast<int64_t>(seg.units()) * view.per_seq;
+            if (local < u) break;
+            local -= u;
+            ++seg.b;
+            seg.n = view.len(seg.b);
+        }
         seg.s = static_cast<int>(local / seg.units());
         seg.u = static_cast<int>(local - static_cast<int64_t>(seg.s) * seg.units());
-        seg.left = min(per, total - begin);
     }
 
     // ---- the copies run ahead of the computation
-    Cursor pre = seg;                    // u: the segment's first unit of the block
-    int pre_u = pre.u + warp;            // the warp's next unit to copy
-    int pre_end = pre.end();
-    int32_t pre_page = 0;                // page of this lane's token of that unit
-    const bool lane_v = lane >= 16;
-    const int lane_tok = lane & 15;
-    const awq_kv_plane &plane = lane_v ? c.v : c.k;
+    Cursor<KT> pre = seg;
+    int pre_u = pre.u;                   // the next unit to copy
+    int pre_end = pre.left > 0 ? pre.end() : 0;
+    // this lane's tokens of that unit: page, and place in it
+    constexpr int TL = KT > 32 ? KT / 32 : 1;
+    int32_t pre_page[TL], pre_place[TL];
 
-    auto find = [&]() {                  // skip segments without units for this warp
-        while (pre.left > 0 && pre_u >= pre_end) {
+    auto find = [&]() {
+        if (pre.left > 0 && pre_u >= pre_end) {
             pre.next_segment(view);
-            pre_u = pre.u + warp;
+            pre_u = pre.u;
             pre_end = pre.left > 0 ? pre.end() : 0;
         }
         if (pre.left > 0) {
-            const int tok = min(pre_u * kUnit + lane_tok, pre.n - 1);
-            pre_page = __ldg(a.page_table + pre.b * a.table_stride + tok / c.page_size);
+#pragma unroll
+            for (int i = 0; i < TL; ++i) {
+                const int tok = min(pre_u * KT + (KT < 32 ? lane % KT : lane + 32 * i), pre.n - 1);
+                const int page = a.page_shift ? static_cast<int>(__umulhi(tok, a.page_magic) >> (a.page_shift - 1)) : tok;
+                pre_place[i] = tok - page * c.page_size;
+                pre_page[i] = __ldg(a.page_table + pre.b * a.table_stride + page);
+            }
         }
     };
     int put = 0;                         // ring slot of the next copy
     auto copy = [&]() {
         if (pre.left > 0) {
-            const int tok = pre_u * kUnit + lane_tok;
-            const bool in_seq = tok < pre.n;
-            const bool ok = pre_page >= 0 && pre_page < c.num_pages;
-            if (in_seq && !ok) set_status(a.status, AWQ_ERR_BAD_INDEX);
-            const int place = tok % c.page_size;
             const int head = pre.s / a.row_tiles;
-            const char *src = static_cast<const char *>(plane.data);
-            if (in_seq && ok)
-                src += (pre_page * plane.page_stride + place * plane.token_stride + head * plane.head_stride) * G::kElem;
-            const uint32_t bytes = in_seq && ok ? 16u : 0u;
-            const uint32_t dst = ring_addr + put * G::kStage;
-            const uint64_t packed = reinterpret_cast<uint64_t>(src);
+            int64_t k_at[TL], v_at[TL];  // bytes from the plane's start; -1: nothing to copy
 #pragma unroll
-            for (int i = 0; i < 2 * kUnit * G::kChunks / 32; ++i) {
-                const int idx = i * 32 + lane;
-                const int row = idx / G::kChunks, ch = idx % G::kChunks;   // rows 16-31: V
-                const uint64_t base = __shfl_sync(~0u, packed, row);
-                const uint32_t size = __shfl_sync(~0u, bytes, row);
-                if (ch * 16 < D * G::kElem)
-                    cp_async_16_zfill(dst + (row >= kUnit ? G::kPlane : 0) + G::at(row & 15, ch),
-                                      reinterpret_cast<const char *>(base) + (size ? ch * 16 : 0), size);
+            for (int i = 0; i < TL; ++i) {
+                const bool in_seq = pre_u * KT + (KT < 32 ? lane % KT : lane + 32 * i) < pre.n;
+                const bool ok = pre_page[i] >= 0 && pre_page[i] < c.num_pages;
+                if (in_seq && !ok) set_status(a.status, AWQ_ERR_BAD_INDEX);
+                k_at[i] = v_at[i] = -1;
+                if (in_seq && ok) {
+                    k_at[i] = (pre_page[i] * c.k.page_stride + pre_place[i] * c.k.token_stride + head * c.k.head_stride) * G::kElem;
+                    v_at[i] = (pre_page[i] * c.v.page_stride + pre_place[i] * c.v.token_stride + head * c.v.head_stride) * G::kElem;
+                }
             }
-            pre_u += kWarps;
+            const uint32_t dst = ring_addr + put * G::kStage;
+            constexpr int kRowsPer = 32 / G::kChunks;                // rows of one instruction of the warp
+            const int ch = lane % G::kChunks;
+            const char *kb = static_cast<const char *>(c.k.data) + ch * 16, *vb = static_cast<const char *>(c.v.data) + ch * 16;
+            const bool in_row = ch * 16 < D * G::kElem;
+#pragma unroll
+            for (int i = 0; i < KT / kRowsPer; ++i) {
+                const int row = i * kRowsPer + lane / G::kChunks;
+                const int64_t ka = __shfl_sync(~0u, k_at[i * kRowsPer / 32], row % 32);
+                const int64_t va = a.same_strides ? ka : __shfl_sync(~0u, v_at[i * kRowsPer / 32], row % 32);
+                const uint32_t size = ka < 0 ? 0 : 16;
+                if (in_row) {
+                    cp_async_16_zfill(dst + G::at(row, ch), kb + (ka < 0 ? -ch * 16 : ka), size);
+                    cp_async_16_zfill(dst + G::kPlane + G::at(row, ch), vb + (ka < 0 ? -ch * 16 : va), size);
+                }
+            }
+            ++pre_u;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         put = put + 1 == G::kStages ? 0 : put + 1;
@@ -356,186 +399,202 @@ __global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, GS8>::kBlocks) attn
 #pragma unroll
     for (int i = 0; i < G::kStages - 1; ++i) copy();
 
+    // element of the head that row `hi` (0: g, 1: g + 8) of output tile i is
+    auto column = [&](int i, int hi) { return FP8 ? 16 * i + 2 * g + hi : 16 * i + g + 8 * hi; };
+
     int get = 0;                         // ring slot of the next unit
-    int64_t unit0 = begin;               // flat number of the segment's first unit of the block
+    int64_t unit0 = begin + warp * per_warp;     // flat number of the segment's first unit of the warp
     while (seg.left > 0) {
         const int end = seg.end();
         const int kv_head = seg.s / a.row_tiles, tile = seg.s % a.row_tiles;
         const int rows_here = min(kAttnRows, a.group - tile * kAttnRows);
         const int head0 = kv_head * a.group + tile * kAttnRows;
-        const int rg[2] = {g, g + 8};
 
-        // ---- Q fragments: rows g and g + 8
-        uint32_t qf[KS][4];
-        float fac[2];                    // score to base-2 logarithm
-        const T *qb = static_cast<const T *>(a.q.data) + seg.b * a.q.token_stride;
+        // ---- Q fragments: head 8 nt + g; the heads of this lane's columns are 8 nt + 2 t4 + j
+        uint32_t qf[NT][KS][2];
+        float fac[NT][2];                // score to base-2 logarithm
+        const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int r = 0; r < (GS8 ? 1 : 2); ++r) {
-            const bool ok = rg[r] < rows_here;
-            const T *q = qb + (head0 + (ok ? rg[r] : 0)) * a.q.head_stride;
-            uint32_t raw[KS][2];
+        for (int nt = 0; nt < NT; ++nt) {
+            const bool ok = 8 * nt + g < rows_here;
+            const T *q = static_cast<const T *>(a.q.data) + seg.b * a.q.token_stride +
+                         (head0 + (ok ? 8 * nt + g : 0)) * a.q.head_stride;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const int d0 = ks * 16 + (FP8 ? 4 * t4 : 2 * t4), d1 = ks * 16 + (FP8 ? 4 * t4 + 2 : 2 * t4 + 8);
-                raw[ks][0] = ok && d0 < D ? *reinterpret_cast<const uint32_t *>(q + d0) : 0u;
-                raw[ks][1] = ok && d1 < D ? *reinterpret_cast<const uint32_t *>(q + d1) : 0u;
+                qf[nt][ks][0] = ok && d0 < D ? *reinterpret_cast<const uint32_t *>(q + d0) ^ sign : 0u;
+                qf[nt][ks][1] = ok && d1 < D ? *reinterpret_cast<const uint32_t *>(q + d1) ^ sign : 0u;
             }
-            fac[r] = a.scale * c.k.scale * kLog2e;
+            float f = fabsf(a.scale) * c.k.scale * kLog2e;
             if constexpr (FP8 && !std::is_same<T, __half>::value) {
                 float top = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 x = unpack2<T>(raw[ks][i]);
+                        const float2 x = unpack2<T>(qf[nt][ks][i]);
                         top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
                     }
-                top = quad_max(top);
-                // 2^-e and 2^e of the row's largest element, e kept where both are normal
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                // 2^-e and 2^e of the head's largest element, e kept where both are normal
                 const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 2), 252);
                 const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-                fac[r] *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+                f *= __uint_as_float(static_cast<uint32_t>(e) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 x = unpack2<T>(raw[ks][i]);
-                        raw[ks][i] = pack2<C>(x.x * down, x.y * down);
+                        const float2 x = unpack2<T>(qf[nt][ks][i]);
+                        qf[nt][ks][i] = pack2<C>(x.x * down, x.y * down);
                     }
             }
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                qf[ks][r] = raw[ks][0];
-                qf[ks][2 + r] = raw[ks][1];
-            }
-        }
-        if constexpr (GS8) {
-            fac[1] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) qf[ks][1] = qf[ks][3] = 0u;
+            fac[nt][0] = __shfl_sync(~0u, f, 8 * t4);
+            fac[nt][1] = __shfl_sync(~0u, f, 8 * t4 + 4);
         }
 
-        float o[DP / 8][4];
+        float o[KS][NT][4];
+        float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+        }
 
-        for (int u = seg.u + warp; u < end; u += kWarps) {
+        for (int u = seg.u; u < end; ++u) {
             asm volatile("cp.async.wait_group %0;" ::"n"(G::kStages - 2) : "memory");
             __syncwarp();
             const uint32_t kst = ring_addr + get * G::kStage, vst = kst + G::kPlane;
             get = get + 1 == G::kStages ? 0 : get + 1;
 
-            // ---- S = Q K^T
-            float s[2][4] = {};
-            if constexpr (FP8) {
+            // ---- S' = K Q'
+            float s[SUB][NT][4];
 #pragma unroll
-                for (int ks = 0; ks < KS; ks += 2) {
-                    uint32_t k4[4];
+            for (int sub = 0; sub < SUB; ++sub) {
+                float x[2][NT][4] = {};          // two chains of products
+                const int row = 16 * sub + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+                for (int ks = 0; ks < KS; ks += FP8 ? 2 : 1) {
                     if (ks * 16 < D) {
-                        ldmatrix_x4(k4, kst + G::at((lane & 7) + ((lane >> 3) & 1) * 8, ks + (lane >> 4)));
+                        uint32_t k4[4];
+                        ldmatrix_x4(k4, kst + G::at(row, (FP8 ? ks : 2 * ks) + (lane >> 4)));
+                        if constexpr (FP8) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
+                            for (int j = 0; j < 2; ++j) {
+                                uint32_t a0, a1, a2, a3;
+                                e4m3x4_to_f16x4(k4[2 * j], a0, a2);
+                                e4m3x4_to_f16x4(k4[2 * j + 1], a1, a3);
 #pragma unroll
-                            for (int n = 0; n < 2; ++n)
-                                mma16816<C>(s[n], qf[ks + j][0], qf[ks + j][1], qf[ks + j][2], qf[ks + j][3],
-                                            e4m3x2_to_f16x2(k4[2 * j + n]), e4m3x2_to_f16x2(k4[2 * j + n] >> 16));
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816<C>(x[j][nt], a0, a1, a2, a3, qf[nt][ks + j][0], qf[nt][ks + j][1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<C>(x[ks & 1][nt], k4[0], k4[1], k4[2], k4[3], qf[nt][ks][0], qf[nt][ks][1]);
+                        }
                     }
                 }
-            } else {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t k4[4];
-                    if (ks * 16 < D) {
-                        ldmatrix_x4(k4, kst + G::at((lane & 7) + (lane >> 4) * 8, 2 * ks + ((lane >> 3) & 1)));
-                        mma16816<C>(s[0], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], k4[0], k4[1]);
-                        mma16816<C>(s[1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], k4[2], k4[3]);
-                    }
-                }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[sub][nt][j] = x[0][nt][j] + x[1][nt][j];
             }
 
             // ---- softmax over the unit
-            const int left = seg.n - u * kUnit;          // tokens of the unit that exist, if below 16
-            constexpr int R = GS8 ? 1 : 2;
-            float top[2] = {-INFINITY, -INFINITY};
+            const int left = seg.n - u * KT;
+            if (left < KT) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+                for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float &x = s[n][2 * r + j];
-                        x *= fac[r];
-                        if (8 * n + 2 * t4 + j >= left) x = -INFINITY;
-                        top[r] = fmaxf(top[r], x);
-                    }
-                top[r] = quad_max(top[r]);
+                        for (int j = 0; j < 4; ++j)
+                            if (16 * sub + g + 8 * (j >> 1) >= left) s[sub][nt][j] = -INFINITY;
             }
+            float top[NT][2];
             bool grew = false;
 #pragma unroll
-            for (int r = 0; r < R; ++r) grew |= top[r] > m[r];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    top[nt][j] = -INFINITY;
+#pragma unroll
+                    for (int sub = 0; sub < SUB; ++sub)
+                        top[nt][j] = fmaxf(top[nt][j], fmaxf(s[sub][nt][j], s[sub][nt][2 + j]));
+                    top[nt][j] *= fac[nt][j];
+                    grew |= top[nt][j] - kLazy > m[nt][j];
+                }
             if (__any_sync(~0u, grew)) {
-                float corr[2] = {1.f, 1.f};
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float mn = fmaxf(m[r], top[r]);
-                    corr[r] = m[r] == mn ? 1.f : fast_exp2(m[r] - mn);
-                    m[r] = mn;
-                    l[r] *= corr[r];
-                }
-#pragma unroll
-                for (int i = 0; i < DP / 8; ++i) {
-                    o[i][0] *= corr[0];
-                    o[i][1] *= corr[0];
-                    o[i][2] *= GS8 ? corr[0] : corr[1];
-                    o[i][3] *= GS8 ? corr[0] : corr[1];
-                }
-            }
-            uint32_t p[4], pl[4];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float base = m[r] == -INFINITY ? 0.f : m[r];
-                float e[4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        e[2 * n + j] = fast_exp2(s[n][2 * r + j] - base);
-                        l[r] += e[2 * n + j];
+                        const float mn = fmaxf(m[nt][j], col_max(top[nt][j]));
+                        const float corr = m[nt][j] == mn ? 1.f : fast_exp2(m[nt][j] - mn);
+                        m[nt][j] = mn;
+                        l[nt][j] *= corr;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            o[i][nt][j] *= corr;
+                            o[i][nt][2 + j] *= corr;
+                        }
                     }
-                split2<C>(e[0], e[1], p[r], pl[r]);
-                split2<C>(e[2], e[3], p[2 + r], pl[2 + r]);
             }
-            if constexpr (GS8) {                        // rows 8-15: the lo terms
-                p[1] = pl[0];
-                p[3] = pl[2];
-            }
-
-            // ---- O += P V
 #pragma unroll
-            for (int ks = 0; ks < (FP8 ? KS / 2 : KS); ++ks) {
-                uint32_t v4[4];
-                if (ks * (FP8 ? 32 : 16) < D) {
-                    ldmatrix_x4_trans(v4, vst + G::at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * ks + (lane >> 4)));
-                    if constexpr (FP8) {
+            for (int sub = 0; sub < SUB; ++sub) {
+                uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {   // 16 columns: the even ones, the odd ones
-                            const uint32_t x = __byte_perm(v4[2 * j], 0, 0x3120), y = __byte_perm(v4[2 * j + 1], 0, 0x3120);
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t b0 = e4m3x2_to_f16x2(h ? x >> 16 : x), b1 = e4m3x2_to_f16x2(h ? y >> 16 : y);
-                                float (&acc)[4] = o[4 * ks + 2 * j + h];
-                                mma16816<C>(acc, p[0], p[1], p[2], p[3], b0, b1);
-                                if constexpr (!GS8) mma16816<C>(acc, pl[0], pl[1], pl[2], pl[3], b0, b1);
+                    for (int j = 0; j < 4; ++j) {
+                        const float base = m[nt][j & 1] == -INFINITY ? 0.f : m[nt][j & 1];
+                        p[j] = fast_exp2(fmaf(s[sub][nt][j], fac[nt][j & 1], -base));
+                        l[nt][j & 1] += p[j];
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        split2<C>(p[2 * h], p[2 * h + 1], ph[nt][h], pl[nt][h]);
+                        ph[nt][h] = movmatrix_trans(ph[nt][h]);
+                        pl[nt][h] = movmatrix_trans(pl[nt][h]);
+                    }
+                }
+                // ---- O' += V' P'
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int i = 0; i < KS; i += 2) {
+                        if (i * 16 < D) {
+                            uint32_t v4[4];
+                            ldmatrix_x4_trans(v4, vst + G::at(16 * sub + (lane & 7) + ((lane >> 3) & 1) * 8, i + (lane >> 4)));
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {        // 16 elements: the even ones are rows 0-7, the odd ones 8-15
+                                uint32_t a0, a1, a2, a3;
+                                e4m3x4_to_f16x4(__byte_perm(v4[2 * j], 0, 0x3120), a0, a1);
+                                e4m3x4_to_f16x4(__byte_perm(v4[2 * j + 1], 0, 0x3120), a2, a3);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma16816<C>(o[i + j][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                                    mma16816<C>(o[i + j][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                                }
                             }
                         }
-                    } else {
+                    }
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            mma16816<C>(o[2 * ks + j], p[0], p[1], p[2], p[3], v4[2 * j], v4[2 * j + 1]);
-                            if constexpr (!GS8) mma16816<C>(o[2 * ks + j], pl[0], pl[1], pl[2], pl[3], v4[2 * j], v4[2 * j + 1]);
+                    for (int i = 0; i < KS; ++i) {
+                        if (i * 16 < D) {
+                            uint32_t v4[4];
+                            ldmatrix_x4_trans(v4, vst + G::at(16 * sub + (lane & 7) + (lane >> 4) * 8, 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816<C>(o[i][nt], v4[0], v4[1], v4[2], v4[3], ph[nt][0], ph[nt][1]);
+                                mma16816<C>(o[i][nt], v4[0], v4[1], v4[2], v4[3], pl[nt][0], pl[nt][1]);
+                            }
                         }
                     }
                 }
@@ -544,166 +603,172 @@ __global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, GS8>::kBlocks) attn
             copy();
         }
 
-        // ---- the warps' results become one (in warp 0)
-        constexpr int R = GS8 ? 1 : 2;
-        if constexpr (GS8) {
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) {
-                o[i][0] += o[i][2];
-                o[i][1] += o[i][3];
-            }
-        }
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < R; ++r) l[r] = quad_sum(l[r]);
+            for (int j = 0; j < 2; ++j) l[nt][j] = col_sum(l[nt][j]);
+        const bool starts = seg.u == 0, ends = end == seg.units();
+        if (starts && ends) {
+            // ---- the warp has the whole segment: the output
 #pragma unroll
-        for (int step = kWarps / 2; step > 0; step >>= 1) {
-            __syncthreads();
-            if (warp >= step && warp < 2 * step) {
-                float *buf = merge + (warp - step) * G::kRows * G::kMergeRow;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float *row = buf + rg[r] * G::kMergeRow;
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 8 * nt + 2 * t4 + j;
+                    if (r >= rows_here) continue;
+                    const float inv = l[nt][j] > 0.f ? c.v.scale / l[nt][j] : l[nt][j];   // l is 0 (no weight) or NaN otherwise
+                    T *out = static_cast<T *>(a.out.data) + seg.b * a.out.token_stride + (head0 + r) * a.out.head_stride;
 #pragma unroll
-                    for (int i = 0; i < DP / 8; ++i)
-                        *reinterpret_cast<float2 *>(row + 8 * i + 2 * t4) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-                    if (t4 == 0) {
-                        row[DP] = m[r];
-                        row[DP + 1] = l[r];
-                    }
-                }
-            }
-            __syncthreads();
-            if (warp < step) {
-                const float *buf = merge + warp * G::kRows * G::kMergeRow;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float *row = buf + rg[r] * G::kMergeRow;
-                    const float m2 = row[DP], mn = fmaxf(m[r], m2);
-                    const float w1 = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - mn);
-                    const float w2 = m2 == -INFINITY ? 0.f : fast_exp2(m2 - mn);
-                    m[r] = mn;
-                    l[r] = l[r] * w1 + row[DP + 1] * w2;
-#pragma unroll
-                    for (int i = 0; i < DP / 8; ++i) {
-                        const float2 x = *reinterpret_cast<const float2 *>(row + 8 * i + 2 * t4);
-                        o[i][2 * r] = o[i][2 * r] * w1 + x.x * w2;
-                        o[i][2 * r + 1] = o[i][2 * r + 1] * w1 + x.y * w2;
-                    }
-                }
-            }
-        }
-
-        // ---- whole segment: the output; else a piece
-        // element of the head that o[i][2r + j] is
-        auto column = [&](int i, int j) {
-            return FP8 ? (i >> 1) * 16 + 4 * t4 + 2 * j + (i & 1) : 8 * i + 2 * t4 + j;
-        };
-        const bool whole = seg.u == 0 && end == seg.units();
-        if (whole) {
-            if (warp == 0) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (rg[r] >= rows_here) continue;
-                    const int h = head0 + rg[r];
-                    const float inv = l[r] > 0.f ? c.v.scale / l[r] : l[r];       // l is 0 (no output) or NaN otherwise
-                    T *out = static_cast<T *>(a.out.data) + seg.b * a.out.token_stride + h * a.out.head_stride;
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int i = 0; i < DP / 8; i += 2) {
-                            const int d = column(i, 0);                            // four neighbours: d .. d + 3
-                            if (d < D)
-                                *reinterpret_cast<uint2 *>(out + d) =
-                                    make_uint2(pack2<T>(o[i][2 * r] * inv, o[i + 1][2 * r] * inv),
-                                               pack2<T>(o[i][2 * r + 1] * inv, o[i + 1][2 * r + 1] * inv));
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < DP / 8; ++i) {
-                            const int d = column(i, 0);
-                            if (d < D)
-                                *reinterpret_cast<uint32_t *>(out + d) = pack2<T>(o[i][2 * r] * inv, o[i][2 * r + 1] * inv);
+                    for (int i = 0; i < KS; ++i) {
+                        if constexpr (FP8) {
+                            if (column(i, 0) < D)
+                                *reinterpret_cast<uint32_t *>(out + column(i, 0)) = pack2<T>(o[i][nt][j] * inv, o[i][nt][2 + j] * inv);
+                        } else {
+                            if (column(i, 0) < D) out[column(i, 0)] = from_f32<T>(o[i][nt][j] * inv);
+                            if (column(i, 1) < D) out[column(i, 1)] = from_f32<T>(o[i][nt][2 + j] * inv);
                         }
                     }
-                    if (a.lse && t4 == 0)
-                        a.lse[static_cast<int64_t>(seg.b) * a.q_heads + h] = (m[r] + log2f(l[r])) * kLn2;
+                    if (a.lse && g == 0)
+                        a.lse[static_cast<int64_t>(seg.b) * a.q_heads + head0 + r] = (m[nt][j] + log2f(l[nt][j])) * kLn2;
                 }
-            }
         } else {
-            // blocks of the segment, and this one's piece (a block's first
-            // segment has its slot 0, a later one slot 1)
-            const int64_t seg_begin = unit0 - seg.u, seg_end = seg_begin + seg.units();
-            const int first = static_cast<int>(seg_begin / per), last = static_cast<int>((seg_end - 1) / per);
-            constexpr int kPiece = kAttnRows * G::kMergeRow;
-            float *piece = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (unit0 == begin ? 0 : 1)) * kPiece;
-            if (warp == 0) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (rg[r] >= rows_here) continue;
-                    float *row = piece + rg[r] * G::kMergeRow;
-#pragma unroll
-                    for (int i = 0; i < DP / 8; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) row[column(i, j)] = o[i][2 * r + j];
-                    if (t4 == 0) {
-                        row[DP] = m[r];
-                        row[DP + 1] = l[r];
-                    }
-                }
-                __threadfence();
+            // ---- a part: the warp's first segment in its own space, its last
+            // one over the ring, whose units have all been used
+            const bool last = seg.left == end - seg.u;
+            float *buf = own_part;
+            if (last) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) s_ticket = atomicAdd(a.counters + first, 1);
+                buf = reinterpret_cast<float *>(ring);
             }
-            __syncthreads();
-            if (s_ticket == last - first) {
-                __threadfence();
-                if (tid == 0) a.counters[first] = 0;
-                const float *first_piece =
-                    a.parts + (2 * static_cast<int64_t>(first) + (seg_begin == first * per ? 0 : 1)) * kPiece;
-                const int cols = D / 2;
-                for (int i = tid; i < rows_here * cols; i += kAttnThreads) {
-                    const int r = i / cols, d = 2 * (i - r * cols);
-                    const int64_t at = static_cast<int64_t>(r) * G::kMergeRow;
-                    float mx = __ldcg(first_piece + at + DP);
-                    for (int p = first + 1; p <= last; ++p)
-                        mx = fmaxf(mx, __ldcg(a.parts + 2 * static_cast<int64_t>(p) * kPiece + at + DP));
-                    const float base = mx == -INFINITY ? 0.f : mx;
-                    float sum = 0.f, x = 0.f, y = 0.f;
-                    for (int p = first; p <= last; ++p) {
-                        const float *src = (p == first ? first_piece : a.parts + 2 * static_cast<int64_t>(p) * kPiece) + at;
-                        const float w = fast_exp2(__ldcg(src + DP) - base);
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + d));
-                        sum += w * __ldcg(src + DP + 1);
-                        x += w * v.x;
-                        y += w * v.y;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float *row = buf + (8 * nt + 2 * t4 + j) * G::kPitch;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        row[column(i, 0)] = o[i][nt][j];
+                        row[column(i, 1)] = o[i][nt][2 + j];
                     }
-                    const float inv = sum > 0.f ? c.v.scale / sum : sum;
-                    const int h = head0 + r;
-                    *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out.data) + seg.b * a.out.token_stride +
-                                                  h * a.out.head_stride + d) = pack2<T>(x * inv, y * inv);
-                    if (a.lse && d == 0) a.lse[static_cast<int64_t>(seg.b) * a.q_heads + h] = (mx + log2f(sum)) * kLn2;
+                    if (g == 0) *reinterpret_cast<float2 *>(row + DP) = make_float2(m[nt][j], l[nt][j]);
                 }
-            }
+            if (lane == 0) s_meta[2 * warp + last] = PartMeta{unit0 - seg.u, seg.b, seg.s};
         }
         unit0 += end - seg.u;
         seg.next_segment(view);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+
+    // ---- the warps' parts, in order; those of one segment are neighbours
+    for (int e0 = 0; e0 < 2 * kWarps;) {
+        const PartMeta meta = s_meta[e0];
+        int e1 = e0 + 1;
+        if (meta.seg_begin < 0) {
+            e0 = e1;
+            continue;
+        }
+        while (e1 < 2 * kWarps && (s_meta[e1].seg_begin < 0 || s_meta[e1].seg_begin == meta.seg_begin)) ++e1;
+        const int n = view.len(meta.b);
+        const int64_t seg_end = meta.seg_begin + (n + KT - 1) / KT;
+        const int kv_head = meta.s / a.row_tiles, tile = meta.s % a.row_tiles;
+        const int rows_here = min(kAttnRows, a.group - tile * kAttnRows);
+        const int head0 = kv_head * a.group + tile * kAttnRows;
+        T *const out = static_cast<T *>(a.out.data) + meta.b * a.out.token_stride + head0 * a.out.head_stride;
+        float *const lse = a.lse ? a.lse + static_cast<int64_t>(meta.b) * a.q_heads + head0 : nullptr;
+        auto finish = [&](int r, int d, float mx, float sum, float4 v) {
+            const float inv = sum > 0.f ? c.v.scale / sum : sum;
+            *reinterpret_cast<uint2 *>(out + r * a.out.head_stride + d) =
+                make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+            if (lse && d == 0) lse[r] = (mx + log2f(sum)) * kLn2;
+        };
+        const bool whole = meta.seg_begin >= begin && seg_end <= block_end;
+        constexpr int kPiece = kAttnRows * G::kPitch;
+        float *const piece = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (meta.seg_begin <= begin ? 0 : 1)) * kPiece;
+        const int cols = D / 4;
+        for (int i = tid; i < rows_here * cols; i += kAttnThreads) {
+            const int r = i / cols, d = 4 * (i - r * cols);
+            float mx = -INFINITY, sum = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int e = e0; e < e1; ++e) {
+                if (s_meta[e].seg_begin < 0) continue;
+                const float *row = (e & 1 ? reinterpret_cast<const float *>(smem + (e >> 1) * G::kStages * G::kStage)
+                                          : reinterpret_cast<const float *>(smem + kWarps * G::kStages * G::kStage +
+                                                                            (e >> 1) * G::kPart)) +
+                                   r * G::kPitch;
+                const float2 ml = *reinterpret_cast<const float2 *>(row + DP);
+                const float4 x = *reinterpret_cast<const float4 *>(row + d);
+                const float mn = fmaxf(mx, ml.x);
+                const float w0 = mx == -INFINITY ? 0.f : fast_exp2(mx - mn), w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mn);
+                mx = mn;
+                sum = sum * w0 + ml.y * w1;
+                v.x = v.x * w0 + x.x * w1;
+                v.y = v.y * w0 + x.y * w1;
+                v.z = v.z * w0 + x.z * w1;
+                v.w = v.w * w0 + x.w * w1;
+            }
+            if (whole) {
+                finish(r, d, mx, sum, v);
+            } else {
+                float *row = piece + r * G::kPitch;
+                *reinterpret_cast<float4 *>(row + d) = v;
+                if (d == 0) *reinterpret_cast<float2 *>(row + DP) = make_float2(mx, sum);
+            }
+        }
+        e0 = e1;
+        if (whole) continue;
+        const int first = static_cast<int>(meta.seg_begin / per), last = static_cast<int>((seg_end - 1) / per);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) s_ticket = atomicAdd(a.counters + first, 1);
+        __syncthreads();
+        if (s_ticket != last - first) continue;
+        __threadfence();
+        if (tid == 0) a.counters[first] = 0;
+        const float *const first_piece =
+            a.parts + (2 * static_cast<int64_t>(first) + (meta.seg_begin == first * per ? 0 : 1)) * kPiece;
+        for (int i = tid; i < rows_here * cols; i += kAttnThreads) {
+            const int r = i / cols, d = 4 * (i - r * cols);
+            const int64_t at = static_cast<int64_t>(r) * G::kPitch;
+            auto row_of = [&](int p) { return (p == first ? first_piece : a.parts + 2 * static_cast<int64_t>(p) * kPiece) + at; };
+            float mx = -INFINITY;
+#pragma unroll 8
+            for (int p = first; p <= last; ++p) mx = fmaxf(mx, __ldcg(row_of(p) + DP));
+            const float base = mx == -INFINITY ? 0.f : mx;
+            float sum = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int p = first; p <= last; ++p) {
+                const float *src = row_of(p);
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + DP));
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + d));
+                const float w = fast_exp2(ml.x - base);
+                sum += w * ml.y;
+                v.x += w * x.x;
+                v.y += w * x.y;
+                v.z += w * x.z;
+                v.w += w * x.w;
+            }
+            finish(r, d, mx, sum, v);
+        }
+    }
 }
 
-template <typename T, bool FP8, int DP, bool GS8>
+template <typename T, bool FP8, int DP, int NT>
 awq_status launch_attn_g(const AttnArgs &a, int sms, cudaStream_t st)
 {
-    using G = Geo<FP8, DP, GS8>;
-    const awq_status r = set_smem(attn_kernel<T, FP8, DP, GS8>, G::kSmem);
+    using G = Geo<FP8, DP, NT>;
+    const awq_status r = set_smem(attn_kernel<T, FP8, DP, NT>, G::kSmem);
     if (r) return r;
-    return launch(attn_kernel<T, FP8, DP, GS8>, dim3(std::min(sms * G::kBlocks, kAttnMaxCtas)), dim3(kAttnThreads), G::kSmem,
+    return launch(attn_kernel<T, FP8, DP, NT>, dim3(std::min(sms * G::kBlocks, kAttnMaxCtas)), dim3(kAttnThreads), G::kSmem,
                   1, st, a);
 }
 
 template <typename T, bool FP8, int DP>
 awq_status launch_attn_dp(const AttnArgs &a, int sms, cudaStream_t st)
 {
-    return a.group <= 8 ? launch_attn_g<T, FP8, DP, true>(a, sms, st) : launch_attn_g<T, FP8, DP, false>(a, sms, st);
+    return a.group <= 8 ? launch_attn_g<T, FP8, DP, 1>(a, sms, st) : launch_attn_g<T, FP8, DP, 2>(a, sms, st);
 }
 
 template <typename T, bool FP8>

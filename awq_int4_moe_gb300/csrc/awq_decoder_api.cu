@@ -184,6 +184,12 @@ awq_status awq_paged_attention(const awq_heads *q, const awq_kv_cache *cache, co
     a.q_heads = q_heads;
     a.group = q_heads / cache->num_heads;
     a.row_tiles = (a.group + kAttnRows - 1) / kAttnRows;
+    // exact for every token below 2^31: with 2^shift >= page_size, magic =
+    // floor(2^(31 + shift) / page_size) + 1 exceeds the quotient by at most 1
+    while ((1ll << a.page_shift) < cache->page_size) ++a.page_shift;
+    a.page_magic = static_cast<uint32_t>((1ull << (31 + a.page_shift)) / cache->page_size + 1);
+    a.same_strides = cache->k.page_stride == cache->v.page_stride && cache->k.token_stride == cache->v.token_stride &&
+                     cache->k.head_stride == cache->v.head_stride;
     a.scale = scale;
     const int sms = current_sm_count();
     if (sms <= 0) return AWQ_ERR_CUDA;

@@ -180,6 +180,9 @@ struct AttnArgs {
     int32_t *status;
     int64_t table_stride;
     int32_t max_pages, batch, q_heads, group, row_tiles;
+    uint32_t page_magic;   // token / page_size = umulhi(token, magic) >> (shift - 1); shift 0: page size 1
+    int32_t page_shift;
+    int32_t same_strides;  // K and V have the same strides
     float scale;
 };
 
@@ -207,10 +210,13 @@ constexpr int kAttnRows = 16;          // query heads of one tile
 constexpr size_t kAttnCounterBytes = (kAttnMaxCtas * sizeof(int32_t) + 255) / 256 * 256;
 // Padded head size of the kernel that takes `dim`.
 constexpr int attn_padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+// Floats of a row of a part or piece: output, maximum, sum; 16-byte rows, and
+// heads two apart fall eight banks apart.
+constexpr int attn_part_pitch(int padded_dim) { return padded_dim + 4; }
 constexpr size_t attn_workspace_bytes(int dim)
 {
     return kAttnCounterBytes +
-           static_cast<size_t>(kAttnMaxCtas) * 2 * kAttnRows * (attn_padded_dim(dim) + 2) * sizeof(float);
+           static_cast<size_t>(kAttnMaxCtas) * 2 * kAttnRows * attn_part_pitch(attn_padded_dim(dim)) * sizeof(float);
 }
 awq_status launch_attention(const AttnArgs &a, int dtype, int sms, cudaStream_t st);
 
