@@ -7,7 +7,7 @@
 // to, so that all read the same number of cache bytes however ragged the
 // batch is. A segment that lies inside a warp's range is finished there; what
 // is cut leaves parts (running maximum, sum, unnormalised output, all fp32):
-// the block's four warps join theirs in shared memory at the end, and a
+// the block's warps join theirs in shared memory at the end, and a
 // segment that is cut between blocks leaves a piece per block in the
 // workspace, joined in block order by the block that finishes last (so the
 // result does not depend on which one that is). No warp waits for another
@@ -47,8 +47,6 @@ namespace awq {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kAttnThreads = kWarps * 32;
 constexpr int kLens = 64;              // sequence lengths kept in shared memory
 constexpr float kLazy = 8.f;           // a score raises the maximum when it passes it by this (base 2)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -197,11 +195,11 @@ struct Geo {
     static constexpr int kStage = 2 * kPlane;           // K rows, then V rows
     static constexpr int kPitch = attn_part_pitch(DP);  // floats of a part's row: output, maximum, sum
     static constexpr int kPart = 8 * NT * kPitch * 4;   // bytes
-    // as many units in flight as a block's share of shared memory holds: two
-    // blocks per multiprocessor where each has two units per warp
-    static constexpr int kFit2 = (115200 - kWarps * kPart) / (kWarps * kStage);
-    static constexpr int kBlocks = kFit2 >= 2 ? 2 : 1;
-    static constexpr int kFit = kBlocks == 2 ? kFit2 : (231424 - kWarps * kPart) / (kWarps * kStage);
+    // eight warps a block, four where they could not have two units each
+    static constexpr int kWarps = 8 * (2 * kStage + kPart) <= 231424 ? 8 : 4;
+    static constexpr int kThreads = 32 * kWarps;
+    // as many units in flight as shared memory holds beside the parts
+    static constexpr int kFit = (231424 - kWarps * kPart) / (kWarps * kStage);
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static constexpr int kSmem = kWarps * (kStages * kStage + kPart);
     static_assert(kStages >= 2 && kStages * kStage >= kPart, "a unit in flight beside the one in use");
@@ -222,16 +220,18 @@ struct PartMeta {
 };
 
 template <typename T, bool FP8, int DP, int NT>
-__global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, NT>::kBlocks) attn_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(const AttnArgs a)
 {
     using G = Geo<FP8, DP, NT>;
     using C = typename std::conditional<FP8, __half, T>::type;   // the tensor core's type
     constexpr int KS = DP / 16, KT = G::KT, SUB = KT / 16;
+    constexpr int kWarps = G::kWarps, kAttnThreads = G::kThreads;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int32_t s_len[kLens];
     __shared__ int64_t s_scan[kWarps];
     __shared__ int64_t s_first[2];                                // first sequence of the block, units before it
     __shared__ PartMeta s_meta[2 * kWarps];
+    __shared__ float2 s_join[kAttnRows];                          // a segment's maximum and sum by head
     __shared__ int32_t s_ticket;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -728,29 +728,57 @@ __global__ void __launch_bounds__(kAttnThreads, Geo<FP8, DP, NT>::kBlocks) attn_
         if (tid == 0) a.counters[first] = 0;
         const float *const first_piece =
             a.parts + (2 * static_cast<int64_t>(first) + (meta.seg_begin == first * per ? 0 : 1)) * kPiece;
+        auto row_of = [&](int p, int r) {
+            return (p == first ? first_piece : a.parts + 2 * static_cast<int64_t>(p) * kPiece) + r * G::kPitch;
+        };
+        // a warp per head: the pieces' maxima and sums, a lane per piece
+        for (int r = warp; r < rows_here; r += kWarps) {
+            constexpr int kMost = (kAttnMaxCtas + 31) / 32;
+            float2 ml[kMost];
+            float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+                const int p = first + lane + 32 * i;
+                ml[i] = p <= last ? __ldcg(reinterpret_cast<const float2 *>(row_of(p, r) + DP)) : make_float2(-INFINITY, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) mx = fmaxf(mx, ml[i].x);
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
+            const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) sum += fast_exp2(ml[i].x - base) * ml[i].y;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
+            if (lane == 0) s_join[r] = make_float2(mx, sum);
+        }
+        __syncthreads();
         for (int i = tid; i < rows_here * cols; i += kAttnThreads) {
             const int r = i / cols, d = 4 * (i - r * cols);
-            const int64_t at = static_cast<int64_t>(r) * G::kPitch;
-            auto row_of = [&](int p) { return (p == first ? first_piece : a.parts + 2 * static_cast<int64_t>(p) * kPiece) + at; };
-            float mx = -INFINITY;
-#pragma unroll 8
-            for (int p = first; p <= last; ++p) mx = fmaxf(mx, __ldcg(row_of(p) + DP));
-            const float base = mx == -INFINITY ? 0.f : mx;
-            float sum = 0.f;
+            const float2 j = s_join[r];
+            const float base = j.x == -INFINITY ? 0.f : j.x;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int p = first; p <= last; ++p) {
-                const float *src = row_of(p);
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + DP));
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + d));
-                const float w = fast_exp2(ml.x - base);
-                sum += w * ml.y;
-                v.x += w * x.x;
-                v.y += w * x.y;
-                v.z += w * x.z;
-                v.w += w * x.w;
+            constexpr int kAhead = 16;               // pieces in flight
+            for (int p0 = first; p0 <= last; p0 += kAhead) {
+                float4 x[kAhead];
+                float w[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const float *src = row_of(min(p0 + k, last), r);
+                    w[k] = __ldcg(src + DP);
+                    x[k] = __ldcg(reinterpret_cast<const float4 *>(src + d));
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (p0 + k > last) break;
+                    const float f = fast_exp2(w[k] - base);
+                    v.x += f * x[k].x;
+                    v.y += f * x[k].y;
+                    v.z += f * x[k].z;
+                    v.w += f * x[k].w;
+                }
             }
-            finish(r, d, mx, sum, v);
+            finish(r, d, j.x, j.y, v);
         }
     }
 }
@@ -761,7 +789,7 @@ awq_status launch_attn_g(const AttnArgs &a, int sms, cudaStream_t st)
     using G = Geo<FP8, DP, NT>;
     const awq_status r = set_smem(attn_kernel<T, FP8, DP, NT>, G::kSmem);
     if (r) return r;
-    return launch(attn_kernel<T, FP8, DP, NT>, dim3(std::min(sms * G::kBlocks, kAttnMaxCtas)), dim3(kAttnThreads), G::kSmem,
+    return launch(attn_kernel<T, FP8, DP, NT>, dim3(std::min(sms, kAttnMaxCtas)), dim3(G::kThreads), G::kSmem,
                   1, st, a);
 }
 

@@ -205,7 +205,7 @@ awq_status launch_rope(const RopeArgs &a, int dtype, int vec, cudaStream_t st);
 
 // The attention's grid never exceeds this many blocks (its workspace holds
 // two pieces and one counter for each).
-constexpr int kAttnMaxCtas = 320;
+constexpr int kAttnMaxCtas = 160;
 constexpr int kAttnRows = 16;          // query heads of one tile
 constexpr size_t kAttnCounterBytes = (kAttnMaxCtas * sizeof(int32_t) + 255) / 256 * 256;
 // Padded head size of the kernel that takes `dim`.
