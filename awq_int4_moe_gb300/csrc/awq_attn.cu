@@ -47,7 +47,7 @@ namespace awq {
 
 namespace {
 
-constexpr int kLens = 64;              // sequence lengths kept in shared memory
+constexpr int kLens = 128;              // sequence lengths kept in shared memory
 constexpr float kLazy = 8.f;           // a score raises the maximum when it passes it by this (base 2)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -61,16 +61,14 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
 
 template <typename T>
@@ -196,16 +194,17 @@ struct Geo {
     static constexpr int kPitch = attn_part_pitch(DP);  // floats of a part's row: output, maximum, sum
     static constexpr int kPart = 8 * NT * kPitch * 4;   // bytes
     // eight warps a block, four where they could not have two units each
-    static constexpr int kWarps = 8 * (2 * kStage + kPart) <= 231424 ? 8 : 4;
+    static constexpr int kWarps = 8 * (2 * kStage + kPart) <= 230400 ? 8 : 4;
     static constexpr int kThreads = 32 * kWarps;
     // as many units in flight as shared memory holds beside the parts
-    static constexpr int kFit = (231424 - kWarps * kPart) / (kWarps * kStage);
+    static constexpr int kFit = (230400 - kWarps * kPart) / (kWarps * kStage);
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static constexpr int kSmem = kWarps * (kStages * kStage + kPart);
     static_assert(kStages >= 2 && kStages * kStage >= kPart, "a unit in flight beside the one in use");
 
     // 16-byte chunk c of row r, placed so that 8 rows of one chunk fall into
-    // different banks
+    // different banks. Planes are aligned to a row, so chunk c ^ x of the row
+    // is at(r, c) ^ (x << 4).
     static __device__ __forceinline__ uint32_t at(int r, int c)
     {
         const int sw = kRow >= 128 ? (r & 7) : ((r >> 1) & 3);
@@ -219,6 +218,14 @@ struct PartMeta {
     int32_t b, s;
 };
 
+// Neighbouring parts of one segment in a block.
+struct Group {
+    int64_t seg_begin, seg_end;   // flat units
+    uint32_t parts;               // which of the block's parts
+    int32_t b, head0, rows;       // sequence, first query head, query heads
+    int32_t whole;                // the segment lies inside the block
+};
+
 template <typename T, bool FP8, int DP, int NT>
 __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(const AttnArgs a)
 {
@@ -226,13 +233,14 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     using C = typename std::conditional<FP8, __half, T>::type;   // the tensor core's type
     constexpr int KS = DP / 16, KT = G::KT, SUB = KT / 16;
     constexpr int kWarps = G::kWarps, kAttnThreads = G::kThreads;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int32_t s_len[kLens];
     __shared__ int64_t s_scan[kWarps];
     __shared__ int64_t s_first[2];                                // first sequence of the block, units before it
     __shared__ PartMeta s_meta[2 * kWarps];
-    __shared__ float2 s_join[kAttnRows];                          // a segment's maximum and sum by head
-    __shared__ int32_t s_ticket;
+    __shared__ Group s_group[2 * G::kWarps];
+    __shared__ int32_t s_groups;
+    __shared__ int32_t s_joins[2];                                // whether this block joins the first, the last group
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -337,20 +345,36 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     Cursor<KT> pre = seg;
     int pre_u = pre.u;                   // the next unit to copy
     int pre_end = pre.left > 0 ? pre.end() : 0;
-    // this lane's tokens of that unit: page, and place in it
+    constexpr int kRowsPer = 32 / G::kChunks;        // rows of one copy instruction of the warp
+    const int ch = lane % G::kChunks, sub_row = lane / G::kChunks;
+    const bool in_row = ch * 16 < D * G::kElem;
+    const uint32_t dst0 = ring_addr + G::at(sub_row, ch);
+    const char *const k_data = static_cast<const char *>(c.k.data), *const v_data = static_cast<const char *>(c.v.data);
+    int64_t k_head = 0, v_head = 0;      // bytes to the segment's KV head
+    // Pages of whole multiples of 16 tokens (paged16): every 16 rows of a unit
+    // are neighbours in one page, found by lane i for rows 16 i ..; else every
+    // row is looked up, by lane i for row i (and i + 32).
     constexpr int TL = KT > 32 ? KT / 32 : 1;
+    const bool paged16 = c.page_size % 16 == 0;
     int32_t pre_page[TL], pre_place[TL];
 
+    auto set_head = [&]() {
+        const int head = pre.s / a.row_tiles;
+        k_head = head * c.k.head_stride * G::kElem;
+        v_head = head * c.v.head_stride * G::kElem;
+    };
     auto find = [&]() {
         if (pre.left > 0 && pre_u >= pre_end) {
             pre.next_segment(view);
             pre_u = pre.u;
             pre_end = pre.left > 0 ? pre.end() : 0;
+            set_head();
         }
         if (pre.left > 0) {
 #pragma unroll
             for (int i = 0; i < TL; ++i) {
-                const int tok = min(pre_u * KT + (KT < 32 ? lane % KT : lane + 32 * i), pre.n - 1);
+                const int row = paged16 ? 16 * (lane % SUB) : KT < 32 ? lane % KT : lane + 32 * i;
+                const int tok = min(pre_u * KT + row, paged16 ? (pre.n - 1) & ~15 : pre.n - 1);
                 const int page = a.page_shift ? static_cast<int>(__umulhi(tok, a.page_magic) >> (a.page_shift - 1)) : tok;
                 pre_place[i] = tok - page * c.page_size;
                 pre_page[i] = __ldg(a.page_table + pre.b * a.table_stride + page);
@@ -360,33 +384,64 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     int put = 0;                         // ring slot of the next copy
     auto copy = [&]() {
         if (pre.left > 0) {
-            const int head = pre.s / a.row_tiles;
-            int64_t k_at[TL], v_at[TL];  // bytes from the plane's start; -1: nothing to copy
+            const uint32_t dst = dst0 + put * G::kStage;
+            const int rows = min(KT, pre.n - pre_u * KT);
+            bool ok[TL];
+            int64_t k_at[TL], v_at[TL];  // bytes from the plane's start
 #pragma unroll
             for (int i = 0; i < TL; ++i) {
-                const bool in_seq = pre_u * KT + (KT < 32 ? lane % KT : lane + 32 * i) < pre.n;
-                const bool ok = pre_page[i] >= 0 && pre_page[i] < c.num_pages;
-                if (in_seq && !ok) set_status(a.status, AWQ_ERR_BAD_INDEX);
-                k_at[i] = v_at[i] = -1;
-                if (in_seq && ok) {
-                    k_at[i] = (pre_page[i] * c.k.page_stride + pre_place[i] * c.k.token_stride + head * c.k.head_stride) * G::kElem;
-                    v_at[i] = (pre_page[i] * c.v.page_stride + pre_place[i] * c.v.token_stride + head * c.v.head_stride) * G::kElem;
+                ok[i] = pre_page[i] >= 0 && pre_page[i] < c.num_pages;
+                if (!ok[i]) {            // nothing of this page is read
+                    set_status(a.status, AWQ_ERR_BAD_INDEX);
+                    pre_page[i] = 0;
                 }
+                k_at[i] = (pre_page[i] * c.k.page_stride + pre_place[i] * c.k.token_stride) * G::kElem + k_head;
+                v_at[i] = a.same_strides ? k_at[i]
+                                         : (pre_page[i] * c.v.page_stride + pre_place[i] * c.v.token_stride) * G::kElem + v_head;
             }
-            const uint32_t dst = ring_addr + put * G::kStage;
-            constexpr int kRowsPer = 32 / G::kChunks;                // rows of one instruction of the warp
-            const int ch = lane % G::kChunks;
-            const char *kb = static_cast<const char *>(c.k.data) + ch * 16, *vb = static_cast<const char *>(c.v.data) + ch * 16;
-            const bool in_row = ch * 16 < D * G::kElem;
+            if (paged16) {
+                const int64_t k_step = kRowsPer * c.k.token_stride * G::kElem, v_step = kRowsPer * c.v.token_stride * G::kElem;
 #pragma unroll
-            for (int i = 0; i < KT / kRowsPer; ++i) {
-                const int row = i * kRowsPer + lane / G::kChunks;
-                const int64_t ka = __shfl_sync(~0u, k_at[i * kRowsPer / 32], row % 32);
-                const int64_t va = a.same_strides ? ka : __shfl_sync(~0u, v_at[i * kRowsPer / 32], row % 32);
-                const uint32_t size = ka < 0 ? 0 : 16;
-                if (in_row) {
-                    cp_async_16_zfill(dst + G::at(row, ch), kb + (ka < 0 ? -ch * 16 : ka), size);
-                    cp_async_16_zfill(dst + G::kPlane + G::at(row, ch), vb + (ka < 0 ? -ch * 16 : va), size);
+                for (int sub = 0; sub < SUB; ++sub) {
+                    const int good = __shfl_sync(~0u, static_cast<int>(ok[0]), sub);
+                    const int64_t k0 = __shfl_sync(~0u, k_at[0], sub), v0 = __shfl_sync(~0u, v_at[0], sub);
+                    const char *kp = k_data + k0 + sub_row * c.k.token_stride * G::kElem + ch * 16;
+                    const char *vp = v_data + v0 + sub_row * c.v.token_stride * G::kElem + ch * 16;
+                    const int have = good ? rows - 16 * sub - sub_row : 0;       // rows from this lane's first on
+                    if (in_row) {
+#pragma unroll
+                        for (int i = 0; i < 16 / kRowsPer; ++i) {
+                            const int r = 16 * sub + i * kRowsPer;               // + sub_row, which is below kRowsPer
+                            const uint32_t at = (dst + r * G::kRow) ^ ((G::kRow >= 128 ? r & 7 : (r >> 1) & 3) << 4);
+                            const uint32_t size = i * kRowsPer < have ? 16 : 0;
+                            cp_async_16_zfill(at, kp, size);
+                            cp_async_16_zfill(at + G::kPlane, vp, size);
+                            kp += k_step;
+                            vp += v_step;
+                        }
+                    }
+                }
+            } else {
+#pragma unroll 4
+                for (int i = 0; i < KT / kRowsPer; ++i) {
+                    const int r = i * kRowsPer;
+                    const int row = r + sub_row;
+                    int64_t k0 = k_at[0], v0 = v_at[0];
+                    int good = ok[0];
+                    if (TL > 1 && r >= 32) {
+                        k0 = k_at[TL - 1];
+                        v0 = v_at[TL - 1];
+                        good = ok[TL - 1];
+                    }
+                    k0 = __shfl_sync(~0u, k0, row % 32);
+                    v0 = __shfl_sync(~0u, v0, row % 32);
+                    good = __shfl_sync(~0u, good, row % 32);
+                    const uint32_t at = (dst + r * G::kRow) ^ ((G::kRow >= 128 ? r & 7 : (r >> 1) & 3) << 4);
+                    const uint32_t size = good && row < rows ? 16 : 0;
+                    if (in_row) {
+                        cp_async_16_zfill(at, k_data + k0 + ch * 16, size);
+                        cp_async_16_zfill(at + G::kPlane, v_data + v0 + ch * 16, size);
+                    }
                 }
             }
             ++pre_u;
@@ -395,6 +450,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         put = put + 1 == G::kStages ? 0 : put + 1;
         find();
     };
+    set_head();
     find();
 #pragma unroll
     for (int i = 0; i < G::kStages - 1; ++i) copy();
@@ -402,6 +458,11 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     // element of the head that row `hi` (0: g, 1: g + 8) of output tile i is
     auto column = [&](int i, int hi) { return FP8 ? 16 * i + 2 * g + hi : 16 * i + g + 8 * hi; };
 
+    // ldmatrix rows of this lane: 16 tokens x 2 chunks, tokens first for K and
+    // for e4m3 V, chunks first for 16-bit V
+    const uint32_t k_lane = ring_addr + G::at((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+    const uint32_t v_lane = ring_addr + G::kPlane + (FP8 ? G::at((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4)
+                                                         : G::at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1));
     int get = 0;                         // ring slot of the next unit
     int64_t unit0 = begin + warp * per_warp;     // flat number of the segment's first unit of the warp
     while (seg.left > 0) {
@@ -468,7 +529,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         for (int u = seg.u; u < end; ++u) {
             asm volatile("cp.async.wait_group %0;" ::"n"(G::kStages - 2) : "memory");
             __syncwarp();
-            const uint32_t kst = ring_addr + get * G::kStage, vst = kst + G::kPlane;
+            const uint32_t kst = k_lane + get * G::kStage, vst = v_lane + get * G::kStage;
             get = get + 1 == G::kStages ? 0 : get + 1;
 
             // ---- S' = K Q'
@@ -476,12 +537,11 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
             for (int sub = 0; sub < SUB; ++sub) {
                 float x[2][NT][4] = {};          // two chains of products
-                const int row = 16 * sub + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
                 for (int ks = 0; ks < KS; ks += FP8 ? 2 : 1) {
                     if (ks * 16 < D) {
                         uint32_t k4[4];
-                        ldmatrix_x4(k4, kst + G::at(row, (FP8 ? ks : 2 * ks) + (lane >> 4)));
+                        ldmatrix_x4(k4, (kst + 16 * sub * G::kRow) ^ ((FP8 ? ks : 2 * ks) << 4));
                         if constexpr (FP8) {
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
@@ -570,7 +630,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                     for (int i = 0; i < KS; i += 2) {
                         if (i * 16 < D) {
                             uint32_t v4[4];
-                            ldmatrix_x4_trans(v4, vst + G::at(16 * sub + (lane & 7) + ((lane >> 3) & 1) * 8, i + (lane >> 4)));
+                            ldmatrix_x4_trans(v4, (vst + 16 * sub * G::kRow) ^ (i << 4));
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {        // 16 elements: the even ones are rows 0-7, the odd ones 8-15
                                 uint32_t a0, a1, a2, a3;
@@ -589,7 +649,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                     for (int i = 0; i < KS; ++i) {
                         if (i * 16 < D) {
                             uint32_t v4[4];
-                            ldmatrix_x4_trans(v4, vst + G::at(16 * sub + (lane & 7) + (lane >> 4) * 8, 2 * i + ((lane >> 3) & 1)));
+                            ldmatrix_x4_trans(v4, (vst + 16 * sub * G::kRow) ^ (i << 5));
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 mma16816<C>(o[i][nt], v4[0], v4[1], v4[2], v4[3], ph[nt][0], ph[nt][1]);
@@ -661,124 +721,154 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
 
-    // ---- the warps' parts, in order; those of one segment are neighbours
-    for (int e0 = 0; e0 < 2 * kWarps;) {
-        const PartMeta meta = s_meta[e0];
-        int e1 = e0 + 1;
-        if (meta.seg_begin < 0) {
-            e0 = e1;
-            continue;
+    // ---- the warps' parts, in order; those of one segment are neighbours: a
+    // group. Lane e of the first warp looks at part e.
+    if (warp == 0) {
+        const PartMeta mt = s_meta[lane < 2 * kWarps ? lane : 0];
+        const uint32_t valid = __ballot_sync(~0u, lane < 2 * kWarps && mt.seg_begin >= 0);
+        const uint32_t below = valid & ((1u << lane) - 1);
+        const int64_t prev = __shfl_sync(~0u, mt.seg_begin, below ? 31 - __clz(below) : 0);
+        const bool head = ((valid >> lane) & 1) && (!below || prev != mt.seg_begin);
+        const uint32_t heads = __ballot_sync(~0u, head);
+        if (head) {
+            const uint32_t after = heads & ~((2u << lane) - 1);
+            Group gr;
+            gr.seg_begin = mt.seg_begin;
+            gr.seg_end = mt.seg_begin + (view.len(mt.b) + KT - 1) / KT;
+            gr.parts = valid & ~((1u << lane) - 1) & (after ? (after & (0u - after)) - 1 : ~0u);
+            const int kv_head = mt.s / a.row_tiles, tile = mt.s % a.row_tiles;
+            gr.b = mt.b;
+            gr.rows = min(kAttnRows, a.group - tile * kAttnRows);
+            gr.head0 = kv_head * a.group + tile * kAttnRows;
+            gr.whole = gr.seg_begin >= begin && gr.seg_end <= block_end;
+            s_group[__popc(heads & ((1u << lane) - 1))] = gr;
         }
-        while (e1 < 2 * kWarps && (s_meta[e1].seg_begin < 0 || s_meta[e1].seg_begin == meta.seg_begin)) ++e1;
-        const int n = view.len(meta.b);
-        const int64_t seg_end = meta.seg_begin + (n + KT - 1) / KT;
-        const int kv_head = meta.s / a.row_tiles, tile = meta.s % a.row_tiles;
-        const int rows_here = min(kAttnRows, a.group - tile * kAttnRows);
-        const int head0 = kv_head * a.group + tile * kAttnRows;
-        T *const out = static_cast<T *>(a.out.data) + meta.b * a.out.token_stride + head0 * a.out.head_stride;
-        float *const lse = a.lse ? a.lse + static_cast<int64_t>(meta.b) * a.q_heads + head0 : nullptr;
-        auto finish = [&](int r, int d, float mx, float sum, float4 v) {
-            const float inv = sum > 0.f ? c.v.scale / sum : sum;
-            *reinterpret_cast<uint2 *>(out + r * a.out.head_stride + d) =
-                make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
-            if (lse && d == 0) lse[r] = (mx + log2f(sum)) * kLn2;
-        };
-        const bool whole = meta.seg_begin >= begin && seg_end <= block_end;
-        constexpr int kPiece = kAttnRows * G::kPitch;
-        float *const piece = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (meta.seg_begin <= begin ? 0 : 1)) * kPiece;
-        const int cols = D / 4;
-        for (int i = tid; i < rows_here * cols; i += kAttnThreads) {
-            const int r = i / cols, d = 4 * (i - r * cols);
-            float mx = -INFINITY, sum = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int e = e0; e < e1; ++e) {
-                if (s_meta[e].seg_begin < 0) continue;
-                const float *row = (e & 1 ? reinterpret_cast<const float *>(smem + (e >> 1) * G::kStages * G::kStage)
-                                          : reinterpret_cast<const float *>(smem + kWarps * G::kStages * G::kStage +
-                                                                            (e >> 1) * G::kPart)) +
-                                   r * G::kPitch;
-                const float2 ml = *reinterpret_cast<const float2 *>(row + DP);
-                const float4 x = *reinterpret_cast<const float4 *>(row + d);
-                const float mn = fmaxf(mx, ml.x);
-                const float w0 = mx == -INFINITY ? 0.f : fast_exp2(mx - mn), w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mn);
-                mx = mn;
-                sum = sum * w0 + ml.y * w1;
-                v.x = v.x * w0 + x.x * w1;
-                v.y = v.y * w0 + x.y * w1;
-                v.z = v.z * w0 + x.z * w1;
-                v.w = v.w * w0 + x.w * w1;
-            }
-            if (whole) {
-                finish(r, d, mx, sum, v);
-            } else {
-                float *row = piece + r * G::kPitch;
-                *reinterpret_cast<float4 *>(row + d) = v;
-                if (d == 0) *reinterpret_cast<float2 *>(row + DP) = make_float2(mx, sum);
-            }
+        if (lane == 0) s_groups = __popc(heads);
+    }
+    __syncthreads();
+    const int groups = s_groups;
+    constexpr int kPiece = kAttnRows * G::kPitch;
+    // a row of 4 columns per lane: output, or piece
+    auto finish = [&](const Group &gr, int r, int d, float mx, float sum, float4 v) {
+        const float inv = sum > 0.f ? c.v.scale / sum : sum;     // the sum is 0 (no weight) or NaN otherwise
+        *reinterpret_cast<uint2 *>(static_cast<T *>(a.out.data) + gr.b * a.out.token_stride + (gr.head0 + r) * a.out.head_stride + d) =
+            make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+        if (a.lse && d == 0) a.lse[static_cast<int64_t>(gr.b) * a.q_heads + gr.head0 + r] = (mx + log2f(sum)) * kLn2;
+    };
+    auto piece_of = [&](int64_t seg_begin, int64_t block) {      // slot 0: the segment that holds the block's first unit
+        return a.parts + (2 * block + (seg_begin <= block * per ? 0 : 1)) * kPiece;
+    };
+    bool pieces = false;
+    for (int i = warp; i < groups * 8 * NT; i += kWarps) {
+        const Group &gr = s_group[i / (8 * NT)];
+        const int r = i % (8 * NT);
+        if (r >= gr.rows) continue;
+        float mx = -INFINITY, sum = 0.f;
+        float4 v[(DP + 127) / 128];
+#pragma unroll
+        for (int k = 0; k < (DP + 127) / 128; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t rest = gr.parts; rest; rest &= rest - 1) {
+            const int e = __ffs(rest) - 1;
+            const float *row = reinterpret_cast<const float *>(
+                                   smem + (e & 1 ? (e >> 1) * G::kStages * G::kStage
+                                                 : kWarps * G::kStages * G::kStage + (e >> 1) * G::kPart)) +
+                               r * G::kPitch;
+            const float2 ml = *reinterpret_cast<const float2 *>(row + DP);
+            const float mn = fmaxf(mx, ml.x);
+            const float w0 = mx == -INFINITY ? 0.f : fast_exp2(mx - mn), w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mn);
+            mx = mn;
+            sum = sum * w0 + ml.y * w1;
+#pragma unroll
+            for (int k = 0; k < (DP + 127) / 128; ++k)
+                if (4 * lane + 128 * k < DP) {
+                    const float4 x = *reinterpret_cast<const float4 *>(row + 4 * lane + 128 * k);
+                    v[k].x = v[k].x * w0 + x.x * w1;
+                    v[k].y = v[k].y * w0 + x.y * w1;
+                    v[k].z = v[k].z * w0 + x.z * w1;
+                    v[k].w = v[k].w * w0 + x.w * w1;
+                }
         }
-        e0 = e1;
-        if (whole) continue;
-        const int first = static_cast<int>(meta.seg_begin / per), last = static_cast<int>((seg_end - 1) / per);
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) s_ticket = atomicAdd(a.counters + first, 1);
-        __syncthreads();
-        if (s_ticket != last - first) continue;
-        __threadfence();
-        if (tid == 0) a.counters[first] = 0;
-        const float *const first_piece =
-            a.parts + (2 * static_cast<int64_t>(first) + (meta.seg_begin == first * per ? 0 : 1)) * kPiece;
-        auto row_of = [&](int p, int r) {
-            return (p == first ? first_piece : a.parts + 2 * static_cast<int64_t>(p) * kPiece) + r * G::kPitch;
-        };
-        // a warp per head: the pieces' maxima and sums, a lane per piece
-        for (int r = warp; r < rows_here; r += kWarps) {
+        float *const row = piece_of(gr.seg_begin, blockIdx.x) + r * G::kPitch;
+#pragma unroll
+        for (int k = 0; k < (DP + 127) / 128; ++k)
+            if (const int d = 4 * lane + 128 * k; d < D) {
+                if (gr.whole)
+                    finish(gr, r, d, mx, sum, v[k]);
+                else
+                    *reinterpret_cast<float4 *>(row + d) = v[k];
+            }
+        if (!gr.whole && lane == 0) *reinterpret_cast<float2 *>(row + DP) = make_float2(mx, sum);
+        pieces |= !gr.whole;
+    }
+    if (pieces) __threadfence();
+    __syncthreads();
+
+    // ---- segments cut between blocks: only the first and the last group can be
+    if (tid < groups && !s_group[tid].whole) {
+        const int64_t first = s_group[tid].seg_begin / per, last = (s_group[tid].seg_end - 1) / per;
+        const bool joins = atomicAdd(a.counters + first, 1) == static_cast<int>(last - first);
+        if (joins) {
+            __threadfence();
+            a.counters[first] = 0;
+        }
+        s_joins[tid ? 1 : 0] = joins;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const int gi = k ? groups - 1 : 0;
+        if ((k && groups == 1) || groups == 0 || s_group[gi].whole || !s_joins[k]) continue;
+        const Group gr = s_group[gi];
+        const int first = static_cast<int>(gr.seg_begin / per), last = static_cast<int>((gr.seg_end - 1) / per);
+        // a warp per head; a lane per piece for the maxima and sums, then one per 4 columns
+        for (int r = warp; r < gr.rows; r += kWarps) {
+            const float *const row0 = piece_of(gr.seg_begin, first) + r * G::kPitch;
+            const float *const rows = a.parts + r * G::kPitch;       // + 2 p kPiece for a later block p
             constexpr int kMost = (kAttnMaxCtas + 31) / 32;
-            float2 ml[kMost];
+            float w[kMost], l[kMost];
             float mx = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < kMost; ++i) {
                 const int p = first + lane + 32 * i;
-                ml[i] = p <= last ? __ldcg(reinterpret_cast<const float2 *>(row_of(p, r) + DP)) : make_float2(-INFINITY, 0.f);
+                const float2 ml = p > last ? make_float2(-INFINITY, 0.f)
+                                           : __ldcg(reinterpret_cast<const float2 *>(
+                                                 (p == first ? row0 : rows + 2 * static_cast<int64_t>(p) * kPiece) + DP));
+                w[i] = ml.x;
+                l[i] = ml.y;
+                mx = fmaxf(mx, ml.x);
             }
-#pragma unroll
-            for (int i = 0; i < kMost; ++i) mx = fmaxf(mx, ml[i].x);
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
             const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-            for (int i = 0; i < kMost; ++i) sum += fast_exp2(ml[i].x - base) * ml[i].y;
+            for (int i = 0; i < kMost; ++i) {
+                w[i] = fast_exp2(w[i] - base);
+                sum += w[i] * l[i];
+            }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
-            if (lane == 0) s_join[r] = make_float2(mx, sum);
-        }
-        __syncthreads();
-        for (int i = tid; i < rows_here * cols; i += kAttnThreads) {
-            const int r = i / cols, d = 4 * (i - r * cols);
-            const float2 j = s_join[r];
-            const float base = j.x == -INFINITY ? 0.f : j.x;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kAhead = 16;               // pieces in flight
-            for (int p0 = first; p0 <= last; p0 += kAhead) {
-                float4 x[kAhead];
-                float w[kAhead];
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 128) {
+                const int d = min(d0 + 4 * lane, D - 4);
+                float4 v = __ldcg(reinterpret_cast<const float4 *>(row0 + d));
+                const float w0 = __shfl_sync(~0u, w[0], 0);
+                v = make_float4(v.x * w0, v.y * w0, v.z * w0, v.w * w0);
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const float *src = row_of(min(p0 + k, last), r);
-                    w[k] = __ldcg(src + DP);
-                    x[k] = __ldcg(reinterpret_cast<const float4 *>(src + d));
+                for (int i = 0; i < kMost; ++i) {
+                    const int top = min(31, last - first - 32 * i);
+#pragma unroll 8
+                    for (int k = i ? 0 : 1; k <= top; ++k) {
+                        const float4 x = __ldcg(
+                            reinterpret_cast<const float4 *>(rows + 2 * static_cast<int64_t>(first + 32 * i + k) * kPiece + d));
+                        const float f = __shfl_sync(~0u, w[i], k);
+                        v.x += f * x.x;
+                        v.y += f * x.y;
+                        v.z += f * x.z;
+                        v.w += f * x.w;
+                    }
                 }
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    if (p0 + k > last) break;
-                    const float f = fast_exp2(w[k] - base);
-                    v.x += f * x[k].x;
-                    v.y += f * x[k].y;
-                    v.z += f * x[k].z;
-                    v.w += f * x[k].w;
-                }
+                if (d0 + 4 * lane < D) finish(gr, r, d, mx, sum, v);
             }
-            finish(r, d, j.x, j.y, v);
         }
     }
 }
