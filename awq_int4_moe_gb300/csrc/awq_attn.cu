@@ -277,14 +277,6 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         if (n != raw && blockIdx.x == 0) set_status(a.status, AWQ_ERR_BAD_INDEX);
         if (b < kLens) s_len[b] = n;
         mine += (n + KT - 1) / KT;
-        // a sequence without tokens: zeros, spread over the blocks
-        if (n == 0 && b % gridDim.x == blockIdx.x) {
-            for (int h = 0; h < a.q_heads; ++h) {
-                T *o = static_cast<T *>(a.out.data) + b * a.out.token_stride + h * a.out.head_stride;
-                for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4 *>(o + d) = make_uint4(0, 0, 0, 0);
-                if (a.lse) a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
-            }
-        }
     }
     mine *= view.per_seq;
     int64_t incl = mine;
@@ -301,6 +293,18 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
+    }
+    // sequences without tokens: zeros, sequence b by block b mod the grid
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+        if (view.clamp(b < kLens ? s_len[b] : a.seq_lens[b]) > 0) continue;
+        const int chunks = D / 8;
+        for (int i = tid; i < a.q_heads * chunks; i += kAttnThreads) {
+            const int h = i / chunks;
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.out.data) + b * a.out.token_stride + h * a.out.head_stride +
+                                       8 * (i - h * chunks)) = make_uint4(0, 0, 0, 0);
+        }
+        if (a.lse)
+            for (int h = tid; h < a.q_heads; h += kAttnThreads) a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
     }
     const int64_t per_warp = (total + static_cast<int64_t>(gridDim.x) * kWarps - 1) / (static_cast<int64_t>(gridDim.x) * kWarps);
     const int64_t per = per_warp * kWarps;
@@ -369,6 +373,16 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
             pre_u = pre.u;
             pre_end = pre.left > 0 ? pre.end() : 0;
             set_head();
+            // the segment's q into L1, for when the computation gets there
+            const int tile = pre.s % a.row_tiles, rows_here = min(kAttnRows, a.group - tile * kAttnRows);
+            const char *q = reinterpret_cast<const char *>(static_cast<const T *>(a.q.data) + pre.b * a.q.token_stride +
+                                                           (pre.s / a.row_tiles * a.group + tile * kAttnRows) * a.q.head_stride);
+            const int lines = (2 * D + 127) / 128;
+            for (int i = lane; pre.left > 0 && i < rows_here * lines; i += 32) {
+                const int r = i / lines;
+                uint32_t unused;
+                asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(unused) : "l"(q + r * a.q.head_stride * 2 + (i - r * lines) * 128));
+            }
         }
         if (pre.left > 0) {
 #pragma unroll
@@ -452,7 +466,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     };
     set_head();
     find();
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < G::kStages - 1; ++i) copy();
 
     // element of the head that row `hi` (0: g, 1: g + 8) of output tile i is
@@ -853,14 +867,16 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                 float4 v = __ldcg(reinterpret_cast<const float4 *>(row0 + d));
                 const float w0 = __shfl_sync(~0u, w[0], 0);
                 v = make_float4(v.x * w0, v.y * w0, v.z * w0, v.w * w0);
+                for (int i = 0; i < kMost && first + 32 * i <= last; ++i) {
+                    float wi = w[0];                 // this round's weights (registers are not indexed)
 #pragma unroll
-                for (int i = 0; i < kMost; ++i) {
+                    for (int k = 1; k < kMost; ++k) wi = i == k ? w[k] : wi;
                     const int top = min(31, last - first - 32 * i);
 #pragma unroll 8
                     for (int k = i ? 0 : 1; k <= top; ++k) {
                         const float4 x = __ldcg(
                             reinterpret_cast<const float4 *>(rows + 2 * static_cast<int64_t>(first + 32 * i + k) * kPiece + d));
-                        const float f = __shfl_sync(~0u, w[i], k);
+                        const float f = __shfl_sync(~0u, wi, k);
                         v.x += f * x.x;
                         v.y += f * x.y;
                         v.z += f * x.z;
