@@ -52,9 +52,28 @@ constexpr float kLazy = 8.f;           // a score raises the maximum when it pas
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void *src, uint32_t bytes)
+// The cache's rows are read once per call and are first to leave L2, so that
+// they do not push out what the next call needs again (its code, q, the page
+// table, the workspace).
+__device__ __forceinline__ uint64_t evict_first_policy()
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void *src, uint32_t bytes, uint64_t policy)
+{
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(policy)
+                 : "memory");
+}
+
+// From L2, and not moved to its use: a batch of these is in flight together.
+__device__ __forceinline__ float4 ld_cg_f4(const float *p)
+{
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
@@ -138,6 +157,14 @@ __device__ __forceinline__ float col_sum(float v)
     return v + __shfl_xor_sync(~0u, v, 16);
 }
 
+// x / y for 0 <= x, 0 < y, short where both fit 32 bits (nearly always; a
+// 64-bit division is a long way through code that runs once).
+__device__ __forceinline__ int64_t div_up_to_64(int64_t x, int64_t y)
+{
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
+
 struct BatchView {
     const int32_t *seq_lens;
     const int32_t *s_len;     // lengths of sequences b0 .. b0 + kLens - 1
@@ -182,6 +209,13 @@ struct Cursor {
     }
 };
 
+// Warps of a block. An e4m3 unit costs about 2,800 cycles of a warp's time
+// and is due every 350 cycles of a multiprocessor, so that 8 warps only just
+// keep up with the memory; 16-bit units take half of that. Two tiles of
+// heads need the registers of 8 warps, 16-bit rows of 256 elements the shared
+// memory of 4 (16 KB a unit).
+constexpr int attn_warps(bool fp8, int dp, int nt) { return !fp8 && dp == 256 ? 4 : fp8 && nt == 1 && dp <= 128 ? 12 : 8; }
+
 // NT: tiles of 8 query heads.
 template <bool FP8, int DP, int NT>
 struct Geo {
@@ -192,15 +226,15 @@ struct Geo {
     static constexpr int kPlane = KT * kRow;
     static constexpr int kStage = 2 * kPlane;           // K rows, then V rows
     static constexpr int kPitch = attn_part_pitch(DP);  // floats of a part's row: output, maximum, sum
-    static constexpr int kPart = 8 * NT * kPitch * 4;   // bytes
-    // eight warps a block, four where they could not have two units each
-    static constexpr int kWarps = 8 * (2 * kStage + kPart) <= 230400 ? 8 : 4;
+    // Warps of a block, and units of each in shared memory (one in use, the
+    // others in flight; 64 to 128 KB in flight cover the latency, more only
+    // lengthens it).
+    static constexpr int kWarps = attn_warps(FP8, DP, NT);
     static constexpr int kThreads = 32 * kWarps;
-    // as many units in flight as shared memory holds beside the parts
-    static constexpr int kFit = (230400 - kWarps * kPart) / (kWarps * kStage);
-    static constexpr int kStages = kFit > 4 ? 4 : kFit;
-    static constexpr int kSmem = kWarps * (kStages * kStage + kPart);
-    static_assert(kStages >= 2 && kStages * kStage >= kPart, "a unit in flight beside the one in use");
+    static constexpr int kStages = kWarps * kStage > 64 * 1024 ? 2 : 3;
+    static constexpr int kSmem = kWarps * kStages * kStage;
+    static constexpr bool kPartsFit = kStages * kStage >= 2 * 8 * NT * kPitch * 4;     // two parts over a warp's ring
+    static_assert(kSmem <= 225 * 1024 && kStages * kStage >= 8 * NT * kPitch * 4, "a part fits over a warp's ring");
 
     // 16-byte chunk c of row r, placed so that 8 rows of one chunk fall into
     // different banks. Planes are aligned to a row, so chunk c ^ x of the row
@@ -248,7 +282,9 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     const int D = c.head_dim;
     uint8_t *const ring = smem + warp * G::kStages * G::kStage;
     const uint32_t ring_addr = smem_u32(ring);
-    float *const own_part = reinterpret_cast<float *>(smem + kWarps * G::kStages * G::kStage + warp * G::kPart);
+    // the workspace: two pieces per block, then the first part of every warp
+    constexpr int kPiece = kAttnRows * G::kPitch;
+    float *const block_parts = a.parts + (2 * kAttnMaxCtas + static_cast<int64_t>(blockIdx.x) * kWarps) * kPiece;
 
     // chunks past the head's end are never copied: they stay zero
     if (D != DP)
@@ -306,7 +342,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         if (a.lse)
             for (int h = tid; h < a.q_heads; h += kAttnThreads) a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
     }
-    const int64_t per_warp = (total + static_cast<int64_t>(gridDim.x) * kWarps - 1) / (static_cast<int64_t>(gridDim.x) * kWarps);
+    const int64_t per_warp = div_up_to_64(total + gridDim.x * kWarps - 1, gridDim.x * kWarps);
     const int64_t per = per_warp * kWarps;
     const int64_t begin = blockIdx.x * per, block_end = min(total, begin + per);
     if (begin >= total) return;
@@ -341,7 +377,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
             ++seg.b;
             seg.n = view.len(seg.b);
         }
-        seg.s = static_cast<int>(local / seg.units());
+        seg.s = static_cast<int>(div_up_to_64(local, seg.units()));
         seg.u = static_cast<int>(local - static_cast<int64_t>(seg.s) * seg.units());
     }
 
@@ -362,27 +398,28 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     const bool paged16 = c.page_size % 16 == 0;
     int32_t pre_page[TL], pre_place[TL];
 
-    auto set_head = [&]() {
-        const int head = pre.s / a.row_tiles;
-        k_head = head * c.k.head_stride * G::kElem;
-        v_head = head * c.v.head_stride * G::kElem;
+    // the copies' new segment: its KV head, and its q rows into L1 ahead of
+    // the computation (behind the copies they would wait for all of them)
+    auto new_segment = [&]() {
+        const int kv_head = a.row_tiles == 1 ? pre.s : pre.s / a.row_tiles, tile = pre.s - kv_head * a.row_tiles;
+        k_head = kv_head * c.k.head_stride * G::kElem;
+        v_head = kv_head * c.v.head_stride * G::kElem;
+        const int rows_here = pre.left > 0 ? min(kAttnRows, a.group - tile * kAttnRows) : 0;
+        const char *q = reinterpret_cast<const char *>(static_cast<const T *>(a.q.data) + pre.b * a.q.token_stride +
+                                                       (kv_head * a.group + tile * kAttnRows) * a.q.head_stride);
+        const int lines = (2 * D + 127) / 128;
+        for (int i = lane; i < rows_here * lines; i += 32) {
+            const int r = i / lines;
+            uint32_t unused;
+            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(unused) : "l"(q + r * a.q.head_stride * 2 + (i - r * lines) * 128));
+        }
     };
     auto find = [&]() {
         if (pre.left > 0 && pre_u >= pre_end) {
             pre.next_segment(view);
             pre_u = pre.u;
             pre_end = pre.left > 0 ? pre.end() : 0;
-            set_head();
-            // the segment's q into L1, for when the computation gets there
-            const int tile = pre.s % a.row_tiles, rows_here = min(kAttnRows, a.group - tile * kAttnRows);
-            const char *q = reinterpret_cast<const char *>(static_cast<const T *>(a.q.data) + pre.b * a.q.token_stride +
-                                                           (pre.s / a.row_tiles * a.group + tile * kAttnRows) * a.q.head_stride);
-            const int lines = (2 * D + 127) / 128;
-            for (int i = lane; pre.left > 0 && i < rows_here * lines; i += 32) {
-                const int r = i / lines;
-                uint32_t unused;
-                asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(unused) : "l"(q + r * a.q.head_stride * 2 + (i - r * lines) * 128));
-            }
+            new_segment();
         }
         if (pre.left > 0) {
 #pragma unroll
@@ -395,6 +432,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
             }
         }
     };
+    const uint64_t policy = evict_first_policy();
     int put = 0;                         // ring slot of the next copy
     auto copy = [&]() {
         if (pre.left > 0) {
@@ -428,8 +466,8 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                             const int r = 16 * sub + i * kRowsPer;               // + sub_row, which is below kRowsPer
                             const uint32_t at = (dst + r * G::kRow) ^ ((G::kRow >= 128 ? r & 7 : (r >> 1) & 3) << 4);
                             const uint32_t size = i * kRowsPer < have ? 16 : 0;
-                            cp_async_16_zfill(at, kp, size);
-                            cp_async_16_zfill(at + G::kPlane, vp, size);
+                            cp_async_16_zfill(at, kp, size, policy);
+                            cp_async_16_zfill(at + G::kPlane, vp, size, policy);
                             kp += k_step;
                             vp += v_step;
                         }
@@ -453,8 +491,8 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                     const uint32_t at = (dst + r * G::kRow) ^ ((G::kRow >= 128 ? r & 7 : (r >> 1) & 3) << 4);
                     const uint32_t size = good && row < rows ? 16 : 0;
                     if (in_row) {
-                        cp_async_16_zfill(at, k_data + k0 + ch * 16, size);
-                        cp_async_16_zfill(at + G::kPlane, v_data + v0 + ch * 16, size);
+                        cp_async_16_zfill(at, k_data + k0 + ch * 16, size, policy);
+                        cp_async_16_zfill(at + G::kPlane, v_data + v0 + ch * 16, size, policy);
                     }
                 }
             }
@@ -464,7 +502,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         put = put + 1 == G::kStages ? 0 : put + 1;
         find();
     };
-    set_head();
+    new_segment();
     find();
 #pragma unroll 1
     for (int i = 0; i < G::kStages - 1; ++i) copy();
@@ -481,7 +519,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     int64_t unit0 = begin + warp * per_warp;     // flat number of the segment's first unit of the warp
     while (seg.left > 0) {
         const int end = seg.end();
-        const int kv_head = seg.s / a.row_tiles, tile = seg.s % a.row_tiles;
+        const int kv_head = a.row_tiles == 1 ? seg.s : seg.s / a.row_tiles, tile = seg.s - kv_head * a.row_tiles;
         const int rows_here = min(kAttnRows, a.group - tile * kAttnRows);
         const int head0 = kv_head * a.group + tile * kAttnRows;
 
@@ -497,8 +535,8 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const int d0 = ks * 16 + (FP8 ? 4 * t4 : 2 * t4), d1 = ks * 16 + (FP8 ? 4 * t4 + 2 : 2 * t4 + 8);
-                qf[nt][ks][0] = ok && d0 < D ? *reinterpret_cast<const uint32_t *>(q + d0) ^ sign : 0u;
-                qf[nt][ks][1] = ok && d1 < D ? *reinterpret_cast<const uint32_t *>(q + d1) ^ sign : 0u;
+                qf[nt][ks][0] = ok && d0 < D ? __ldg(reinterpret_cast<const uint32_t *>(q + d0)) ^ sign : 0u;
+                qf[nt][ks][1] = ok && d1 < D ? __ldg(reinterpret_cast<const uint32_t *>(q + d1)) ^ sign : 0u;
             }
             float f = fabsf(a.scale) * c.k.scale * kLog2e;
             if constexpr (FP8 && !std::is_same<T, __half>::value) {
@@ -706,10 +744,10 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                         a.lse[static_cast<int64_t>(seg.b) * a.q_heads + head0 + r] = (m[nt][j] + log2f(l[nt][j])) * kLn2;
                 }
         } else {
-            // ---- a part: the warp's first segment in its own space, its last
+            // ---- a part: the warp's first segment in the workspace, its last
             // one over the ring, whose units have all been used
             const bool last = seg.left == end - seg.u;
-            float *buf = own_part;
+            float *buf = block_parts + warp * kPiece;
             if (last) {
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 __syncwarp();
@@ -733,6 +771,15 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         seg.next_segment(view);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    if (G::kPartsFit && s_meta[2 * warp].seg_begin >= 0) {
+        // back from the workspace, beside the last part, while other warps still work
+        const float *src = block_parts + warp * kPiece;
+        float *dst = reinterpret_cast<float *>(ring) + 8 * NT * G::kPitch;
+#pragma unroll 4
+        for (int i = 4 * lane; i < 8 * NT * G::kPitch; i += 128)
+            *reinterpret_cast<float4 *>(dst + i) = ld_cg_f4(src + i);
+    }
     __syncthreads();
 
     // ---- the warps' parts, in order; those of one segment are neighbours: a
@@ -750,7 +797,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
             gr.seg_begin = mt.seg_begin;
             gr.seg_end = mt.seg_begin + (view.len(mt.b) + KT - 1) / KT;
             gr.parts = valid & ~((1u << lane) - 1) & (after ? (after & (0u - after)) - 1 : ~0u);
-            const int kv_head = mt.s / a.row_tiles, tile = mt.s % a.row_tiles;
+            const int kv_head = a.row_tiles == 1 ? mt.s : mt.s / a.row_tiles, tile = mt.s - kv_head * a.row_tiles;
             gr.b = mt.b;
             gr.rows = min(kAttnRows, a.group - tile * kAttnRows);
             gr.head0 = kv_head * a.group + tile * kAttnRows;
@@ -761,7 +808,6 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     }
     __syncthreads();
     const int groups = s_groups;
-    constexpr int kPiece = kAttnRows * G::kPitch;
     // a row of 4 columns per lane: output, or piece
     auto finish = [&](const Group &gr, int r, int d, float mx, float sum, float4 v) {
         const float inv = sum > 0.f ? c.v.scale / sum : sum;     // the sum is 0 (no weight) or NaN otherwise
@@ -783,9 +829,8 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         for (int k = 0; k < (DP + 127) / 128; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (uint32_t rest = gr.parts; rest; rest &= rest - 1) {
             const int e = __ffs(rest) - 1;
-            const float *row = reinterpret_cast<const float *>(
-                                   smem + (e & 1 ? (e >> 1) * G::kStages * G::kStage
-                                                 : kWarps * G::kStages * G::kStage + (e >> 1) * G::kPart)) +
+            const float *const last_part = reinterpret_cast<const float *>(smem + (e >> 1) * G::kStages * G::kStage);
+            const float *row = (e & 1 ? last_part : G::kPartsFit ? last_part + 8 * NT * G::kPitch : block_parts + (e >> 1) * kPiece) +
                                r * G::kPitch;
             const float2 ml = *reinterpret_cast<const float2 *>(row + DP);
             const float mn = fmaxf(mx, ml.x);
@@ -819,7 +864,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 
     // ---- segments cut between blocks: only the first and the last group can be
     if (tid < groups && !s_group[tid].whole) {
-        const int64_t first = s_group[tid].seg_begin / per, last = (s_group[tid].seg_end - 1) / per;
+        const int64_t first = div_up_to_64(s_group[tid].seg_begin, per), last = div_up_to_64(s_group[tid].seg_end - 1, per);
         const bool joins = atomicAdd(a.counters + first, 1) == static_cast<int>(last - first);
         if (joins) {
             __threadfence();
@@ -833,7 +878,8 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         const int gi = k ? groups - 1 : 0;
         if ((k && groups == 1) || groups == 0 || s_group[gi].whole || !s_joins[k]) continue;
         const Group gr = s_group[gi];
-        const int first = static_cast<int>(gr.seg_begin / per), last = static_cast<int>((gr.seg_end - 1) / per);
+        const int first = static_cast<int>(div_up_to_64(gr.seg_begin, per));
+        const int last = static_cast<int>(div_up_to_64(gr.seg_end - 1, per));
         // a warp per head; a lane per piece for the maxima and sums, then one per 4 columns
         for (int r = warp; r < gr.rows; r += kWarps) {
             const float *const row0 = piece_of(gr.seg_begin, first) + r * G::kPitch;
@@ -872,15 +918,22 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
                     for (int k = 1; k < kMost; ++k) wi = i == k ? w[k] : wi;
                     const int top = min(31, last - first - 32 * i);
-#pragma unroll 8
-                    for (int k = i ? 0 : 1; k <= top; ++k) {
-                        const float4 x = __ldcg(
-                            reinterpret_cast<const float4 *>(rows + 2 * static_cast<int64_t>(first + 32 * i + k) * kPiece + d));
-                        const float f = __shfl_sync(~0u, wi, k);
-                        v.x += f * x.x;
-                        v.y += f * x.y;
-                        v.z += f * x.z;
-                        v.w += f * x.w;
+#pragma unroll 1
+                    for (int k0 = i ? 0 : 1; k0 <= top; k0 += 16) {      // 16 pieces in flight
+                        float4 x[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            x[k] = ld_cg_f4(rows + 2 * static_cast<int64_t>(first + 32 * i + min(k0 + k, top)) * kPiece + d);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float f = __shfl_sync(~0u, wi, min(k0 + k, 31));
+                            if (k0 + k <= top) {
+                                v.x += f * x[k].x;
+                                v.y += f * x[k].y;
+                                v.z += f * x[k].z;
+                                v.w += f * x[k].w;
+                            }
+                        }
                     }
                 }
                 if (d0 + 4 * lane < D) finish(gr, r, d, mx, sum, v);

@@ -203,9 +203,10 @@ awq_status launch_quantize(const QuantArgs &a, int dtype, bool wide, int sms, cu
 // vec: elements per access (8, 4 or 1).
 awq_status launch_rope(const RopeArgs &a, int dtype, int vec, cudaStream_t st);
 
-// The attention's grid never exceeds this many blocks (its workspace holds
-// two pieces and one counter for each).
+// The attention's grid never exceeds this many blocks of this many warps (its
+// workspace holds a counter and two pieces per block and a part per warp).
 constexpr int kAttnMaxCtas = 160;
+constexpr int kAttnMaxWarps = 12;
 constexpr int kAttnRows = 16;          // query heads of one tile
 constexpr size_t kAttnCounterBytes = (kAttnMaxCtas * sizeof(int32_t) + 255) / 256 * 256;
 // Padded head size of the kernel that takes `dim`.
@@ -216,7 +217,8 @@ constexpr int attn_part_pitch(int padded_dim) { return padded_dim + 4; }
 constexpr size_t attn_workspace_bytes(int dim)
 {
     return kAttnCounterBytes +
-           static_cast<size_t>(kAttnMaxCtas) * 2 * kAttnRows * attn_part_pitch(attn_padded_dim(dim)) * sizeof(float);
+           static_cast<size_t>(kAttnMaxCtas) * (2 + kAttnMaxWarps) * kAttnRows * attn_part_pitch(attn_padded_dim(dim)) *
+               sizeof(float);
 }
 awq_status launch_attention(const AttnArgs &a, int dtype, int sms, cudaStream_t st);
 
