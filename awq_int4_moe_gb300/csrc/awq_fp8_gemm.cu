@@ -39,7 +39,7 @@ constexpr int kRasterRows = 16;             // token tiles that a band of the ti
 
 template <int TN, bool SWAP>
 struct GemmGeo {
-    static constexpr int kCols = TN < 128 ? TN : 128;            // accumulator columns of an epilogue warp
+    static constexpr int kCols = TN < 64 ? TN : 64;              // accumulator columns of an epilogue warp
     static constexpr int kEpiWarps = 4 * (TN / kCols);
     static constexpr int kThreads = (kEpiWarps + 2) * 32;
     static constexpr int kA = kTM * kKB, kB = TN * kKB, kStage = kA + kB;
@@ -382,7 +382,7 @@ awq_status launch_gemm_tile(const GemmArgs &g, const uint8_t *a, int64_t lda, co
     // blocks per tile: as many as keep the grid within the blocks that fit
     int cluster = 1;
     if (TN < 256)
-        while (cluster < 8 && 2 * cluster <= KB && tiles * 2 * cluster <= sms * G::kBlocks) cluster *= 2;
+        cluster = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, KB, sms * G::kBlocks / tiles})));
     const int grid = cluster > 1 ? static_cast<int>(tiles) * cluster
                                  : static_cast<int>(std::min<int64_t>(tiles, sms * G::kBlocks));
     const awq_status r = set_smem(fp8_gemm_kernel<T, TN, SWAP>, G::kSmem);
