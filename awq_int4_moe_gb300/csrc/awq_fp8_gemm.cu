@@ -3,10 +3,10 @@
 // e4m3 operands on the 5th-generation tensor cores (tcgen05 kind::f8f6f4).
 //
 // The tensor core multiplies one K block of 128 at a time (four K = 32
-// instructions) into one of two fp32 accumulators in tensor memory; the
+// instructions) into one of several fp32 accumulators in tensor memory; the
 // epilogue warps read it back, multiply by the block's scale and add it to
-// fp32 registers while the other accumulator is filled, so a block's scale is
-// applied exactly once and the sums stay in fp32.
+// fp32 registers while the next ones are filled, so a block's scale is applied
+// exactly once and the sums stay in fp32.
 //
 // One operand's 128 rows are the UMMA M side, TN rows of the other its N side:
 //   few tokens (SWAP): weights on the M side, so that a tile of 16 tokens wastes
@@ -24,6 +24,7 @@
 // mod 4) ..), then the producer (TMA boxes of 128 bytes of K, 128-byte swizzle),
 // then the MMA issuer; they meet at mbarriers, every wait is bounded.
 #include <algorithm>
+#include <atomic>
 
 #include "awq_decoder_kernels.cuh"
 #include "awq_launch.cuh"
@@ -39,17 +40,19 @@ constexpr int kRasterRows = 16;             // token tiles that a band of the ti
 
 template <int TN, bool SWAP>
 struct GemmGeo {
-    static constexpr int kCols = TN < 64 ? TN : 64;              // accumulator columns of an epilogue warp
+    static constexpr int kDepth = TN == 256 ? 2 : 4;             // accumulators in tensor memory
+    static constexpr int kCols = TN < 64 ? TN : 64;              // columns of an epilogue warp
     static constexpr int kEpiWarps = 4 * (TN / kCols);
     static constexpr int kThreads = (kEpiWarps + 2) * 32;
     static constexpr int kA = kTM * kKB, kB = TN * kKB, kStage = kA + kB;
     // two blocks per multiprocessor where the tile is small
     static constexpr int kBlocks = TN <= 64 ? 2 : 1;
-    static constexpr int kStages = (kBlocks == 2 ? 104 : 200) * 1024 / kStage;
-    static constexpr int kTmemCols = 2 * TN < 32 ? 32 : 2 * TN;
+    static constexpr int kStages = (kBlocks == 2 ? 104 : 192) * 1024 / kStage;
+    static constexpr int kTmemCols = kDepth * TN < 32 ? 32 : kDepth * TN;
     static constexpr int kFactors = SWAP ? kEpiWarps * 2 * TN * 4 : 0;
-    static constexpr int kBars = 2 * kStages + 5;
-    static constexpr int kSmem = 1024 + kStages * kStage + kFactors + kBars * 8 + 16;
+    static constexpr int kOut = SWAP ? 0 : kEpiWarps * 2048;     // 32 rows of 32 columns per epilogue warp
+    static constexpr int kBars = 2 * kStages + 2 * kDepth + 1;
+    static constexpr int kSmem = 1024 + kStages * kStage + kFactors + kOut + kBars * 8 + 16;
     // partial sums of a cluster's blocks, over the operand stages
     static constexpr int kPartRow = SWAP ? kTM : TN + 4;
     static_assert((SWAP ? TN : kTM) * kPartRow * 4 <= kStages * kStage || TN == 256, "partial sums fit");
@@ -84,15 +87,24 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[16])
                  : "memory");
 }
 
-// (x, y) += (a, b) * (s, t)
-__device__ __forceinline__ void fma2(float &x, float &y, uint32_t a, uint32_t b, float s, float t)
+// Pairs of fp32 values in one 64-bit register: acc += (a, b) * f.
+__device__ __forceinline__ uint64_t pair(float x, float y)
 {
-    uint64_t acc, d, f;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(x), "f"(y));
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t a, uint32_t b, uint64_t f)
+{
+    uint64_t d;
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(f) : "f"(s), "f"(t));
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(f));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
 }
 
 // Tile `t` of token tiles x weight tiles, in bands of kRasterRows token tiles
@@ -116,11 +128,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     float *factors = reinterpret_cast<float *>(smem + G::kStages * G::kStage);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::kStages * G::kStage + G::kFactors);
+    uint8_t *const out_space = smem + G::kStages * G::kStage + G::kFactors;
+    uint64_t *full = reinterpret_cast<uint64_t *>(out_space + G::kOut);
     uint64_t *empty = full + G::kStages;
-    uint64_t *acc_full = empty + G::kStages;          // [2]
-    uint64_t *acc_empty = acc_full + 2;               // [2]
-    uint64_t *drain = acc_empty + 2;
+    uint64_t *acc_full = empty + G::kStages;          // [depth]
+    uint64_t *acc_empty = acc_full + G::kDepth;       // [depth]
+    uint64_t *drain = acc_empty + G::kDepth;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -129,7 +142,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < G::kDepth; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], EW);
         }
@@ -188,23 +201,25 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
             int it = 0;
             bool ok = true;
             for (int t = tile0; ok && t < tiles; t += tile_step) {
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % G::kStages, buf = it & 1;
-                    if ((it >= 2 && !mbar_wait_bounded(&acc_empty[buf], ((it >> 1) + 1) & 1, p.timeout_ns)) ||
-                        !mbar_wait_bounded(&full[s], (it / G::kStages) & 1, p.timeout_ns)) {
-                        set_status(p.status, AWQ_ERR_DEVICE_TIMEOUT);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                    const int s = it % G::kStages, buf = it % G::kDepth;
+                    if (!mbar_wait_bounded(&full[s], (it / G::kStages) & 1, p.timeout_ns)) ok = false;
                     const uint32_t at = smem_u32(smem + s * G::kStage);
-                    const uint64_t da = umma_desc_sw128(at), db = umma_desc_sw128(at + G::kA);
+                    const uint64_t da = umma_desc_sw128(at);
+                    if (ok && it >= G::kDepth &&
+                        !mbar_wait_bounded(&acc_empty[buf], ((it / G::kDepth) + 1) & 1, p.timeout_ns))
+                        ok = false;
+                    if (ok) {
+                        tc_fence_after();
+                        const uint64_t db = umma_desc_sw128(at + G::kA);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tc_mma_f8(tmem + buf * TN, da + 2 * k, db + 2 * k, idesc, k > 0);
-                    tc_commit(&empty[s]);
-                    tc_commit(&acc_full[buf]);
+                        for (int k = 0; k < 4; ++k) tc_mma_f8(tmem + buf * TN, da + 2 * k, db + 2 * k, idesc, k > 0);
+                        tc_commit(&empty[s]);
+                        tc_commit(&acc_full[buf]);
+                    }
                 }
             }
+            if (!ok) set_status(p.status, AWQ_ERR_DEVICE_TIMEOUT);
             if (!ok) {
                 tc_commit(drain);
                 mbar_wait_bounded(drain, 0, p.timeout_ns);
@@ -216,14 +231,18 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
         const int l = quarter * 32 + lane;                           // this thread's row of the M side
         float *fac = factors + warp * 2 * TN;
+        // 0, which the compiler does not see: barrier addresses that it knows
+        // to be uniform go through the uniform registers, whose latency is on
+        // the path of every K block (M 8192, N 5120, K 8192: 344 us against 326)
+        const int none = col0 / TN;
         int it = 0;
         bool ok = true;
         for (int t = tile0; ok && t < tiles; t += tile_step) {
             const int2 tl = tile_at(t, tiles_m, tiles_n);
             const int m0 = tl.x * kTM, n0 = tl.y * TN;
-            float acc[NC];
+            uint64_t acc[NC / 2];                                    // pairs of columns
 #pragma unroll
-            for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+            for (int i = 0; i < NC / 2; ++i) acc[i] = 0;
             // the scales of the next K block
             const float *wb = p.b_scales + static_cast<int64_t>((SWAP ? m0 : min(n0 + col0, p.N - 1)) / AWQ_FP8_BLOCK) * KB;
             constexpr int F = SWAP ? (TN + 31) / 32 : 1;
@@ -240,16 +259,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
             };
             fetch(kb0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int buf = it & 1;
-                const float mine = next[0];
+                const int buf = it % G::kDepth, bar = buf + none;
+                const uint64_t mine = pair(next[0], next[0]);
+                float *const fb = fac + (it & 1) * TN;
                 if constexpr (SWAP) {
 #pragma unroll
                     for (int i = 0; i < F; ++i)
-                        if (TN >= 32 || lane < TN) fac[buf * TN + lane + 32 * i] = next[i];
+                        if (TN >= 32 || lane < TN) fb[lane + 32 * i] = next[i];
                     __syncwarp();
                 }
                 if (kb + 1 < kb1) fetch(kb + 1);
-                if (!mbar_wait_bounded(&acc_full[buf], (it >> 1) & 1, p.timeout_ns)) {
+                if (!mbar_wait_bounded(&acc_full[bar], (it / G::kDepth) & 1, p.timeout_ns)) {
                     if (lane == 0) set_status(p.status, AWQ_ERR_DEVICE_TIMEOUT);
                     ok = false;
                 }
@@ -266,15 +286,19 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
                     if (c + 1 < NC / 16) tc_ld16_async(taddr + buf * TN + (c + 1) * 16, d[(c + 1) & 1]);
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
-                        float4 f = make_float4(mine, mine, mine, mine);
-                        if constexpr (SWAP) f = *reinterpret_cast<const float4 *>(fac + buf * TN + c * 16 + i);
-                        fma2(acc[c * 16 + i], acc[c * 16 + i + 1], d[c & 1][i], d[c & 1][i + 1], f.x, f.y);
-                        fma2(acc[c * 16 + i + 2], acc[c * 16 + i + 3], d[c & 1][i + 2], d[c & 1][i + 3], f.z, f.w);
+                        uint64_t f0 = mine, f1 = mine;
+                        if constexpr (SWAP) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(fb + c * 16 + i);
+                            f0 = f.x;
+                            f1 = f.y;
+                        }
+                        fma2(acc[c * 8 + i / 2], d[c & 1][i], d[c & 1][i + 1], f0);
+                        fma2(acc[c * 8 + i / 2 + 1], d[c & 1][i + 2], d[c & 1][i + 3], f1);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                if (lane == 0) mbar_arrive(&acc_empty[bar]);
             }
             if (!ok) break;
             T *out = static_cast<T *>(p.out);
@@ -282,36 +306,65 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
                 // this block's part of the sum, over the operand stages: every
                 // copy into them has been consumed
                 float *part = reinterpret_cast<float *>(smem);
-                if constexpr (SWAP) {
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) part[i * G::kPartRow + l] = acc[i];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NC; i += 4)
-                        *reinterpret_cast<float4 *>(part + l * G::kPartRow + col0 + i) =
-                            make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                for (int i = 0; i < NC; i += 4) {
+                    const float2 x = unpair(acc[i / 2]), y = unpair(acc[i / 2 + 1]);
+                    if constexpr (SWAP) {
+                        part[(col0 + i) * G::kPartRow + l] = x.x;
+                        part[(col0 + i + 1) * G::kPartRow + l] = x.y;
+                        part[(col0 + i + 2) * G::kPartRow + l] = y.x;
+                        part[(col0 + i + 3) * G::kPartRow + l] = y.y;
+                    } else {
+                        *reinterpret_cast<float4 *>(part + l * G::kPartRow + col0 + i) = make_float4(x.x, x.y, y.x, y.y);
+                    }
                 }
             } else if constexpr (SWAP) {
                 const int n = m0 + l;
                 if (n < p.N)
 #pragma unroll
-                    for (int i = 0; i < NC; ++i)
-                        if (n0 + i < p.M) out[static_cast<int64_t>(n0 + i) * p.ldo + n] = from_f32<T>(acc[i]);
-            } else {
-                const int m = m0 + l, n = n0 + col0;
-                if (m < p.M && n < p.N) {
-                    T *row = out + static_cast<int64_t>(m) * p.ldo + n;
-                    if (n + NC <= p.N && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
-#pragma unroll
-                        for (int i = 0; i < NC; i += 8)
-                            *reinterpret_cast<uint4 *>(row + i) =
-                                make_uint4(pack2<T>(acc[i], acc[i + 1]), pack2<T>(acc[i + 2], acc[i + 3]),
-                                           pack2<T>(acc[i + 4], acc[i + 5]), pack2<T>(acc[i + 6], acc[i + 7]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < NC; ++i)
-                            if (n + i < p.N) row[i] = from_f32<T>(acc[i]);
+                    for (int i = 0; i < NC; i += 2) {
+                        const float2 x = unpair(acc[i / 2]);
+                        const int tok = n0 + col0 + i;
+                        if (tok < p.M) out[static_cast<int64_t>(tok) * p.ldo + n] = from_f32<T>(x.x);
+                        if (tok + 1 < p.M) out[static_cast<int64_t>(tok + 1) * p.ldo + n] = from_f32<T>(x.y);
                     }
+            } else {
+                // through shared memory, 32 columns at a time, so that
+                // neighbouring lanes store neighbouring columns
+                uint8_t *const space = out_space + warp * 2048;
+                const int m = m0 + quarter * 32, n = n0 + col0;
+                const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && p.ldo % 8 == 0;
+#pragma unroll
+                for (int c = 0; c < NC / 32; ++c) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 x = unpair(acc[c * 16 + j * 4 + i]);
+                            w[i] = pack2<T>(x.x, x.y);
+                        }
+                        *reinterpret_cast<uint4 *>(space + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 8 * j + (lane >> 2), q = lane & 3, col = n + 32 * c + 8 * q;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(space + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+                        if (m + r >= p.M || col >= p.N) continue;
+                        T *dst = out + static_cast<int64_t>(m + r) * p.ldo + col;
+                        if (wide && col + 8 <= p.N) {
+                            *reinterpret_cast<uint4 *>(dst) = v;
+                        } else {
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (col + i < p.N)
+                                    reinterpret_cast<uint16_t *>(dst)[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+                        }
+                    }
+                    __syncwarp();
                 }
             }
         }
@@ -367,6 +420,33 @@ bool make_map(CUtensorMap *m, const uint8_t *base, int64_t ld, int rows, int K, 
                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+// Clusters of `size` blocks that the device holds at once (looked up once per
+// device and size: a property of the device and the kernel).
+template <typename T, int TN, bool SWAP>
+int resident_clusters(int size)
+{
+    using G = GemmGeo<TN, SWAP>;
+    static std::atomic<int> known[64][9] = {};       // count + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (dev < 64)
+        if (const int n = known[dev][size].load(std::memory_order_relaxed)) return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(G::kThreads);
+    cfg.dynamicSmemBytes = G::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<T, TN, SWAP>, &cfg) != cudaSuccess) return 0;
+    if (dev < 64) known[dev][size].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 template <typename T, int TN, bool SWAP>
 awq_status launch_gemm_tile(const GemmArgs &g, const uint8_t *a, int64_t lda, const uint8_t *b, int64_t ldb, int sms,
                             cudaStream_t st)
@@ -379,14 +459,18 @@ awq_status launch_gemm_tile(const GemmArgs &g, const uint8_t *a, int64_t lda, co
     const int64_t tiles = static_cast<int64_t>(((SWAP ? g.N : g.M) + kTM - 1) / kTM) * (((SWAP ? g.M : g.N) + TN - 1) / TN);
     if (tiles > 0x3fffffff) return AWQ_ERR_UNSUPPORTED_SHAPE;
     const int KB = (g.K + kKB - 1) / kKB;
-    // blocks per tile: as many as keep the grid within the blocks that fit
-    int cluster = 1;
-    if (TN < 256)
-        cluster = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, KB, sms * G::kBlocks / tiles})));
-    const int grid = cluster > 1 ? static_cast<int>(tiles) * cluster
-                                 : static_cast<int>(std::min<int64_t>(tiles, sms * G::kBlocks));
     const awq_status r = set_smem(fp8_gemm_kernel<T, TN, SWAP>, G::kSmem);
     if (r) return r;
+    // Blocks per tile: as many, up to 8, as still run all at once (one token, N
+    // = 3584, K = 2560, 28 tiles: 9.1 us with 1, 5.0-5.5 with 4 to 8; clusters
+    // that do not all fit cost a second round: 64 tokens, N = K = 5120, 40
+    // tiles: 9.8 us with 6, 15.7 with 7).
+    int cluster = 1;
+    if (TN < 256)
+        for (cluster = std::min(KB, 8); cluster > 1; --cluster)
+            if (tiles <= resident_clusters<T, TN, SWAP>(cluster)) break;
+    const int grid = cluster > 1 ? static_cast<int>(tiles) * cluster
+                                 : static_cast<int>(std::min<int64_t>(tiles, sms * G::kBlocks));
     return launch(fp8_gemm_kernel<T, TN, SWAP>, dim3(grid), dim3(G::kThreads), G::kSmem, cluster, st, mm, mn, g, cluster);
 }
 
@@ -397,8 +481,13 @@ awq_status launch_gemm_t(const GemmArgs &g, const uint8_t *a, int64_t lda, const
     if (g.M <= 16) return launch_gemm_tile<T, 16, true>(g, a, lda, b, ldb, sms, st);
     if (g.M <= 32) return launch_gemm_tile<T, 32, true>(g, a, lda, b, ldb, sms, st);
     if (g.M <= 64) return launch_gemm_tile<T, 64, true>(g, a, lda, b, ldb, sms, st);
-    const int64_t wide = static_cast<int64_t>((g.M + 127) / 128) * ((g.N + 255) / 256);
-    if (wide >= sms) return launch_gemm_tile<T, 256, false>(g, a, lda, b, ldb, sms, st);
+    // Tiles of 128 x 256 take 3 / 2 of the time of tiles of 128 x 128 (the
+    // accumulators' hand-over costs as much as half of the products), so they
+    // win where they save a third of the rounds: M 512, N = K = 5120: 26 us
+    // against 35; M 1024, N 5120, K 2560: 30 against 28; M 4096: 65 against 78.
+    const int64_t mt = (g.M + 127) / 128, nt = (g.N + 127) / 128, nt2 = (g.N + 255) / 256;
+    if (3 * ((mt * nt2 + sms - 1) / sms) < 2 * ((mt * nt + sms - 1) / sms))
+        return launch_gemm_tile<T, 256, false>(g, a, lda, b, ldb, sms, st);
     return launch_gemm_tile<T, 128, false>(g, a, lda, b, ldb, sms, st);
 }
 
