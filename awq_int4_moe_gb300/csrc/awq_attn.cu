@@ -157,14 +157,6 @@ __device__ __forceinline__ float col_sum(float v)
     return v + __shfl_xor_sync(~0u, v, 16);
 }
 
-// x / y for 0 <= x, 0 < y, short where both fit 32 bits (nearly always; a
-// 64-bit division is a long way through code that runs once).
-__device__ __forceinline__ int64_t div_up_to_64(int64_t x, int64_t y)
-{
-    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-    return x / y;
-}
-
 struct BatchView {
     const int32_t *seq_lens;
     const int32_t *s_len;     // lengths of sequences b0 .. b0 + kLens - 1

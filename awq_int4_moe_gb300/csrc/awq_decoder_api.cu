@@ -83,8 +83,10 @@ awq_status awq_add_rmsnorm(const void *x, int64_t ldx, const void *residual, int
     const bool wide = hidden % 8 == 0 && aligned(weight, 16) && aligned_rows(x, ldx, 2, 16) &&
                       aligned_rows(residual, ldr, 2, 16) && aligned_rows(residual_out, ldro, 2, 16) &&
                       aligned_rows(out, ldo, 2, 16) && aligned_rows(out_q, ldq, 1, 8);
+    const int sms = current_sm_count();
+    if (sms <= 0) return AWQ_ERR_CUDA;
     const NormArgs a{x, residual, weight, residual_out, out, out_q, out_scales, ldx, ldr, ldro, ldo, ldq, eps, rows, hidden};
-    return launch_norm(a, dtype, wide, current_sm_count(), static_cast<cudaStream_t>(stream));
+    return launch_norm(a, dtype, wide, sms, static_cast<cudaStream_t>(stream));
 }
 
 awq_status awq_quantize_fp8(const void *x, int64_t ldx, uint8_t *q, int64_t ldq, float *scales, int32_t rows,
@@ -136,7 +138,9 @@ awq_status awq_rope_append(const awq_heads *q, const awq_heads *q_out, const awq
     }
     const RopeArgs a{*q, *q_out, *k, *v, positions, cos_sin, slots, *cache, dev_status, max_positions,
                      rotary_dim, interleaved != 0, tokens, q_heads};
-    return launch_rope(a, dtype, vec, static_cast<cudaStream_t>(stream));
+    const int sms = current_sm_count();
+    if (sms <= 0) return AWQ_ERR_CUDA;
+    return launch_rope(a, dtype, vec, sms, static_cast<cudaStream_t>(stream));
 }
 
 size_t awq_paged_attention_workspace_bytes(int32_t head_dim)

@@ -14,6 +14,14 @@
 
 namespace awq {
 
+// x / y for 0 <= x, 0 < y, short where both fit 32 bits (nearly always; a
+// 64-bit division is a long way through code that runs once).
+__device__ __forceinline__ int64_t div_up_to_64(int64_t x, int64_t y)
+{
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
+
 // ------------------------------------------------------------ conversions
 
 // One 16-bit activation as fp32 and back (round to nearest even).
@@ -78,30 +86,53 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }
 
-// N (1, 4 or 8) consecutive 16-bit elements; 4 and 8 in one aligned access.
-template <typename T, int N>
-__device__ __forceinline__ void load_elems(const T *p, float (&f)[N])
+// N (1, 4 or 8) consecutive 16-bit elements, 4 and 8 in one aligned access: as
+// loaded, and as fp32.
+template <int N>
+struct RawElems {
+    static_assert(N == 1 || N == 4 || N == 8, "1, 4 or 8 elements");
+    uint32_t w[N == 1 ? 1 : N / 2];
+};
+
+template <int N, typename T>
+__device__ __forceinline__ RawElems<N> load_raw(const T *p)
 {
+    RawElems<N> r;
     if constexpr (N == 8) {
         const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+        r.w[2] = v.z;
+        r.w[3] = v.w;
+    } else if constexpr (N == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+    } else {
+        r.w[0] = *reinterpret_cast<const uint16_t *>(p);
+    }
+    return r;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void unpack_raw(const RawElems<N> &r, float (&f)[N])
+{
+    if constexpr (N == 1) {
+        f[0] = unpack2<T>(r.w[0]).x;
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = unpack2<T>(w[i]);
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 x = unpack2<T>(r.w[i]);
             f[2 * i] = x.x;
             f[2 * i + 1] = x.y;
         }
-    } else if constexpr (N == 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        const float2 x = unpack2<T>(v.x), y = unpack2<T>(v.y);
-        f[0] = x.x;
-        f[1] = x.y;
-        f[2] = y.x;
-        f[3] = y.y;
-    } else {
-        static_assert(N == 1, "1, 4 or 8 elements");
-        f[0] = to_f32(*p);
     }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void load_elems(const T *p, float (&f)[N])
+{
+    unpack_raw<T>(load_raw<N>(p), f);
 }
 
 template <typename T, int N>
@@ -201,7 +232,7 @@ struct GemmArgs {
 awq_status launch_norm(const NormArgs &a, int dtype, bool wide, int sms, cudaStream_t st);
 awq_status launch_quantize(const QuantArgs &a, int dtype, bool wide, int sms, cudaStream_t st);
 // vec: elements per access (8, 4 or 1).
-awq_status launch_rope(const RopeArgs &a, int dtype, int vec, cudaStream_t st);
+awq_status launch_rope(const RopeArgs &a, int dtype, int vec, int sms, cudaStream_t st);
 
 // The attention's grid never exceeds this many blocks of this many warps (its
 // workspace holds a counter and two pieces per block and a part per warp).

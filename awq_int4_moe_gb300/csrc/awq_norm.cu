@@ -6,13 +6,16 @@
 // Each element is read once and written once per output: a row lives in the
 // registers of one block (or one warp) between its sum of squares and its
 // outputs. About six operations per element: bound by the bytes for many
-// rows, by the launch and one block's dependent steps for few.
+// rows (8192 x 5120 with residual, 52.9 us, 6.3 TB/s), by the launch and one
+// block's dependent steps for few (1.7 us).
 //
 // Columns are dealt so that a quantisation group never leaves a warp: with
 // 16-byte accesses (wide) 16 neighbouring lanes hold a group, 8 columns each;
 // otherwise a warp holds it, lane l the columns l, l + 32, l + 64, l + 96 (one
 // element per access, neighbouring lanes side by side). Its amax is a few
 // shuffles.
+#include <algorithm>
+
 #include "awq_decoder_kernels.cuh"
 #include "awq_launch.cuh"
 
@@ -36,19 +39,48 @@ struct Columns<false> {
     static constexpr int kGroupLanes = 32;
 };
 
+// A chunk's columns as loaded (0 past the row's end), and as fp32.
+struct RawCols {
+    uint32_t w[4];                       // wide: 8 packed elements; else one in each
+};
+
+template <typename T, bool WIDE>
+__device__ __forceinline__ RawCols load_raw_cols(const T *row, int c, int n)
+{
+    RawCols r = {{0, 0, 0, 0}};
+    if constexpr (WIDE) {
+        if (c < n) {
+            const RawElems<8> v = load_raw<8>(row + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.w[i] = v.w[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + 32 * i < n) r.w[i] = load_raw<1>(row + c + 32 * i).w[0];
+    }
+    return r;
+}
+
+template <typename T, bool WIDE>
+__device__ __forceinline__ void unpack_cols(const RawCols &r, float (&f)[Columns<WIDE>::kElems])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = unpack2<T>(r.w[i]);
+        if constexpr (WIDE) {
+            f[2 * i] = x.x;
+            f[2 * i + 1] = x.y;
+        } else {
+            f[i] = x.x;
+        }
+    }
+}
+
 template <typename T, bool WIDE>
 __device__ __forceinline__ void load_cols(const T *row, int c, int n, float (&f)[Columns<WIDE>::kElems])
 {
-    if constexpr (WIDE) {
-        if (c < n)
-            load_elems<T, 8>(row + c, f);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = 0.f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = c + 32 * i < n ? to_f32(row[c + 32 * i]) : 0.f;
-    }
+    unpack_cols<T, WIDE>(load_raw_cols<T, WIDE>(row, c, n), f);
 }
 
 template <typename T, bool WIDE>
@@ -89,130 +121,176 @@ __device__ __forceinline__ void quantize_cols(const float (&y)[Columns<WIDE>::kE
     if ((lane & (Columns<WIDE>::kGroupLanes - 1)) == 0 && c < n) scales[c / AWQ_FP8_BLOCK] = s.x;
 }
 
-// NV chunks of a row per thread. ROW_WARP: a row per warp, blockDim.x / 32
-// rows per block; else a row per block.
-template <typename T, bool WIDE, int NV, bool ROW_WARP>
-__global__ void __launch_bounds__(ROW_WARP ? 128 : 1024) norm_kernel(const NormArgs a)
+// NV chunks of a row per thread. THREADS 128: a row per warp, blockDim.x / 32
+// rows side by side; else a row per block. A block goes on to the row that is
+// gridDim.x (x 4) further, whose loads are on their way while the present
+// row is summed and written.
+template <typename T, bool WIDE, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a)
 {
     constexpr int E = Columns<WIDE>::kElems;
-    __shared__ float s_sum[32];
+    constexpr bool ROW_WARP = THREADS == 128;
+    __shared__ float s_sum[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = ROW_WARP ? 32 : blockDim.x;
     const int tid = ROW_WARP ? lane : threadIdx.x;
-    const int64_t row = ROW_WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+    const int64_t step = ROW_WARP ? static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) : gridDim.x;
+    int64_t row = ROW_WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
     const int n = a.hidden;
     grid_dependency_wait();
     grid_launch_dependents();
     if (row >= a.rows) return;              // whole warps (ROW_WARP) or never
-    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-    float r[NV][E];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) load_cols<T, WIDE>(x, Columns<WIDE>::first(j, R, tid), n, r[j]);
-    if (a.residual) {
-        const T *res = static_cast<const T *>(a.residual) + row * a.ldr;
-        float t[NV][E];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) load_cols<T, WIDE>(res, Columns<WIDE>::first(j, R, tid), n, t[j]);
+    RawCols x[NV], res[NV];
+    auto fetch = [&](int64_t at) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
+            x[j] = load_raw_cols<T, WIDE>(static_cast<const T *>(a.x) + at * a.ldx, Columns<WIDE>::first(j, R, tid), n);
+        if (a.residual) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) r[j][i] += t[j][i];
-    }
-    float sum = 0.f;
+            for (int j = 0; j < NV; ++j)
+                res[j] = load_raw_cols<T, WIDE>(static_cast<const T *>(a.residual) + at * a.ldr, Columns<WIDE>::first(j, R, tid), n);
+        }
+    };
+    fetch(row);
+    RawCols weight[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) weight[j] = load_raw_cols<T, WIDE>(static_cast<const T *>(a.weight), Columns<WIDE>::first(j, R, tid), n);
+    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+        float r[NV][E];
+        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) sum += r[j][i] * r[j][i];
-    if (a.residual_out) {
-        T *ro = static_cast<T *>(a.residual_out) + row * a.ldro;
+        for (int j = 0; j < NV; ++j) {
+            unpack_cols<T, WIDE>(x[j], r[j]);
+            if (a.residual) {
+                float t[E];
+                unpack_cols<T, WIDE>(res[j], t);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) store_cols<T, WIDE>(ro, Columns<WIDE>::first(j, R, tid), n, r[j]);
-    }
+                for (int i = 0; i < E; ++i) r[j][i] += t[i];
+            }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if constexpr (!ROW_WARP) {
-        if (lane == 0) s_sum[warp] = sum;
-        __syncthreads();
-        sum = lane < static_cast<int>(blockDim.x >> 5) ? s_sum[lane] : 0.f;
+            for (int i = 0; i < E; ++i) sum += r[j][i] * r[j][i];
+        }
+        if (row + step < a.rows) fetch(row + step);
+        if (a.residual_out) {
+            T *ro = static_cast<T *>(a.residual_out) + row * a.ldro;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) store_cols<T, WIDE>(ro, Columns<WIDE>::first(j, R, tid), n, r[j]);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    }
-    const float inv = 1.f / sqrtf(sum / static_cast<float>(n) + a.eps);
+        if constexpr (!ROW_WARP) {
+            // written again two rows on, with the next row's barrier between
+            if (lane == 0) s_sum[turn][warp] = sum;
+            __syncthreads();
+            sum = lane < static_cast<int>(blockDim.x >> 5) ? s_sum[turn][lane] : 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = Columns<WIDE>::first(j, R, tid);
-        float w[E];
-        load_cols<T, WIDE>(static_cast<const T *>(a.weight), c, n, w);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        }
+        const float inv = 1.f / sqrtf(sum / static_cast<float>(n) + a.eps);
 #pragma unroll
-        for (int i = 0; i < E; ++i) r[j][i] = r[j][i] * inv * w[i];
-        if (a.out) store_cols<T, WIDE>(static_cast<T *>(a.out) + row * a.ldo, c, n, r[j]);
-        if (a.out_q)
-            quantize_cols<WIDE>(r[j], c, n, a.out_q + row * a.ldq,
-                                a.out_scales + row * ((n + AWQ_FP8_BLOCK - 1) / AWQ_FP8_BLOCK), lane);
+        for (int j = 0; j < NV; ++j) {
+            const int c = Columns<WIDE>::first(j, R, tid);
+            float w[E];
+            unpack_cols<T, WIDE>(weight[j], w);
+#pragma unroll
+            for (int i = 0; i < E; ++i) r[j][i] = r[j][i] * inv * w[i];
+            if (a.out) store_cols<T, WIDE>(static_cast<T *>(a.out) + row * a.ldo, c, n, r[j]);
+            if (a.out_q)
+                quantize_cols<WIDE>(r[j], c, n, a.out_q + row * a.ldq,
+                                    a.out_scales + row * ((n + AWQ_FP8_BLOCK - 1) / AWQ_FP8_BLOCK), lane);
+        }
     }
 }
 
-// One warp per step of 256 (wide) or 128 columns of a row.
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a, int64_t steps, int steps_per_row)
+// A warp takes U neighbouring steps of 256 (wide) or 128 columns of a row, all
+// their loads in flight together.
+template <typename T, bool WIDE, int U>
+__global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a, int steps_per_row)
 {
     constexpr int kCols = 32 * Columns<WIDE>::kElems;
     const int lane = threadIdx.x & 31;
+    const int64_t s = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = s / steps_per_row;
+    if (row >= a.rows) return;                          // whole warps
+    const int c0 = static_cast<int>(s - row * steps_per_row) * kCols * U + Columns<WIDE>::first(0, 32, lane);
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
-    for (int64_t s = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); s < steps; s += stride) {
-        const int64_t row = s / steps_per_row;
-        const int c = static_cast<int>(s - row * steps_per_row) * kCols + Columns<WIDE>::first(0, 32, lane);
-        float v[Columns<WIDE>::kElems];
-        load_cols<T, WIDE>(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols, v);
-        quantize_cols<WIDE>(v, c, a.cols, a.q + row * a.ldq,
+    float v[U][Columns<WIDE>::kElems];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_cols<T, WIDE>(static_cast<const T *>(a.x) + row * a.ldx, c0 + u * kCols, a.cols, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        quantize_cols<WIDE>(v[u], c0 + u * kCols, a.cols, a.q + row * a.ldq,
                             a.scales + row * ((a.cols + AWQ_FP8_BLOCK - 1) / AWQ_FP8_BLOCK), lane);
-    }
 }
 
-template <typename T, bool WIDE, int NV>
-awq_status launch_norm_nv(const NormArgs &a, int row_threads, cudaStream_t st)
+template <typename T, bool WIDE, int NV, int THREADS>
+awq_status launch_norm_nv(const NormArgs &a, int threads, int sms, cudaStream_t st)
 {
-    if (row_threads == 32)
-        return launch(norm_kernel<T, WIDE, NV, true>, dim3((a.rows + 3) / 4), dim3(128), 0, 1, st, a);
-    return launch(norm_kernel<T, WIDE, NV, false>, dim3(a.rows), dim3(row_threads), 0, 1, st, a);
+    const int rows = THREADS == 128 ? 4 : 1;             // rows of a block
+    const int grid = std::min((a.rows + rows - 1) / rows, sms * std::max(1, 2048 / threads));
+    return launch(norm_kernel<T, WIDE, NV, THREADS>, dim3(grid), dim3(threads), 0, 1, st, a);
+}
+
+template <typename T, bool WIDE>
+awq_status launch_norm_w(const NormArgs &a, int sms, cudaStream_t st)
+{
+    constexpr int kChunk = 32 * Columns<WIDE>::kElems;   // columns of a warp's chunk
+    const int chunks = (a.hidden + kChunk - 1) / kChunk;
+    // A row per warp up to 4 chunks (16384 x 1024: 24.5 us; a row per block 26),
+    // else a row per block: a chunk per warp for few rows (fewer steps in a
+    // row's time), two where the rows are many and the row has more than 12
+    // chunks (8192 x 5120: 52.9 us, 62 with one; 4096 x 8192: 23.6, 28.5 with
+    // one, 26 with four). Narrow accesses keep one: they are bound by their
+    // number, not by the memory.
+    if (chunks == 1) return launch_norm_nv<T, WIDE, 1, 128>(a, 128, sms, st);
+    if (chunks == 2) return launch_norm_nv<T, WIDE, 2, 128>(a, 128, sms, st);
+    if (chunks <= 4) return launch_norm_nv<T, WIDE, 4, 128>(a, 128, sms, st);
+    const int most = WIDE && a.rows >= 4 * sms ? 12 : 32;
+    if (chunks <= most) return launch_norm_nv<T, WIDE, 1, 1024>(a, 32 * chunks, sms, st);
+    if (chunks <= 64) return launch_norm_nv<T, WIDE, 2, 1024>(a, 32 * ((chunks + 1) / 2), sms, st);
+    if (WIDE || chunks <= 128) return launch_norm_nv<T, WIDE, 4, 1024>(a, 32 * ((chunks + 3) / 4), sms, st);
+    if constexpr (!WIDE) return launch_norm_nv<T, WIDE, 8, 1024>(a, 32 * ((chunks + 7) / 8), sms, st);
 }
 
 template <typename T>
-awq_status launch_norm_t(const NormArgs &a, bool wide, cudaStream_t st)
+awq_status launch_norm_t(const NormArgs &a, bool wide, int sms, cudaStream_t st)
 {
-    // chunks of the row a warp holds: 256 columns wide, 128 otherwise
-    const int chunks = (a.hidden + (wide ? 255 : 127)) / (wide ? 256 : 128);
-    // a row per warp up to 4 chunks, else a row per block of up to 32 warps
-    const int nv = chunks <= 4 ? chunks : (chunks + 31) / 32;
-    const int threads = chunks <= 4 ? 32 : (chunks + nv - 1) / nv * 32;
-    if (wide)
-        return nv == 1   ? launch_norm_nv<T, true, 1>(a, threads, st)
-               : nv == 2 ? launch_norm_nv<T, true, 2>(a, threads, st)
-                         : launch_norm_nv<T, true, 4>(a, threads, st);
-    return nv == 1   ? launch_norm_nv<T, false, 1>(a, threads, st)
-           : nv == 2 ? launch_norm_nv<T, false, 2>(a, threads, st)
-           : nv <= 4 ? launch_norm_nv<T, false, 4>(a, threads, st)
-                     : launch_norm_nv<T, false, 8>(a, threads, st);
+    return wide ? launch_norm_w<T, true>(a, sms, st) : launch_norm_w<T, false>(a, sms, st);
+}
+
+template <typename T, bool WIDE, int U>
+awq_status launch_quantize_u(const QuantArgs &a, cudaStream_t st)
+{
+    const int per = 32 * Columns<WIDE>::kElems * U;
+    const int steps_per_row = (a.cols + per - 1) / per;
+    const int64_t blocks = (static_cast<int64_t>(a.rows) * steps_per_row + 7) / 8;
+    if (blocks > 0x7fffffff) return AWQ_ERR_UNSUPPORTED_SHAPE;
+    return launch(quantize_kernel<T, WIDE, U>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, st, a, steps_per_row);
+}
+
+template <typename T, bool WIDE>
+awq_status launch_quantize_w(const QuantArgs &a, int sms, cudaStream_t st)
+{
+    // Two steps a warp where there are several rounds of them (6000 x 8192: 32.4
+    // us with one, 27.0 with two, 26.4 with four; 16384 x 2560: 27.6, 23.1,
+    // 24.9), one where the warps should spread (48 x 4096: 1.3 us, 1.5, 1.7)
+    const int per = 32 * Columns<WIDE>::kElems;
+    const int64_t steps = static_cast<int64_t>(a.rows) * ((a.cols + per - 1) / per);
+    return steps >= 64ll * sms ? launch_quantize_u<T, WIDE, 2>(a, st) : launch_quantize_u<T, WIDE, 1>(a, st);
 }
 
 template <typename T>
 awq_status launch_quantize_t(const QuantArgs &a, bool wide, int sms, cudaStream_t st)
 {
-    const int per = wide ? 256 : 128;
-    const int steps_per_row = (a.cols + per - 1) / per;
-    const int64_t steps = static_cast<int64_t>(a.rows) * steps_per_row;
-    const int grid = static_cast<int>(min(steps / 8 + (steps % 8 != 0), static_cast<int64_t>(sms) * 64));
-    return wide ? launch(quantize_kernel<T, true>, dim3(grid), dim3(256), 0, 1, st, a, steps, steps_per_row)
-                : launch(quantize_kernel<T, false>, dim3(grid), dim3(256), 0, 1, st, a, steps, steps_per_row);
+    return wide ? launch_quantize_w<T, true>(a, sms, st) : launch_quantize_w<T, false>(a, sms, st);
 }
 
 }  // namespace
 
-awq_status launch_norm(const NormArgs &a, int dtype, bool wide, int, cudaStream_t st)
+awq_status launch_norm(const NormArgs &a, int dtype, bool wide, int sms, cudaStream_t st)
 {
-    return dtype == AWQ_DTYPE_F16 ? launch_norm_t<__half>(a, wide, st) : launch_norm_t<__nv_bfloat16>(a, wide, st);
+    return dtype == AWQ_DTYPE_F16 ? launch_norm_t<__half>(a, wide, sms, st) : launch_norm_t<__nv_bfloat16>(a, wide, sms, st);
 }
 
 awq_status launch_quantize(const QuantArgs &a, int dtype, bool wide, int sms, cudaStream_t st)

@@ -89,7 +89,8 @@ def run_norm(rows, hidden, kind, residual, outputs, pad, seed=0, scale=1.0):
 @pytest.mark.parametrize("rows,hidden,pad", [
     (1, 2560, 0), (1, 1, 0), (3, 2, 1), (5, 127, 0), (5, 128, 0), (5, 129, 3), (2, 1000, 0), (7, 1024, 8), (3, 1032, 0),
     (4, 4095, 0), (4, 4104, 8), (2, 8192, 0), (2, 8200, 0), (2, 16384, 0), (1, 16385, 0), (2, 32768, 0), (1, 32767, 2),
-    (1, 24000, 0), (130, 640, 5), (1000, 128, 0)])
+    (1, 24000, 0), (130, 640, 5), (1000, 128, 0), (2500, 1280, 0), (1400, 5120, 8), (700, 16384, 0), (5000, 96, 3),
+    (900, 1500, 1)])
 def test_norm_sizes(rows, hidden, pad, kind):
     run_norm(rows, hidden, kind, True, "yq", pad)
 
