@@ -3,6 +3,8 @@
 Each ``csrc/*.cu`` is compiled to an object in parallel with nvcc, then the
 objects are linked into one shared library next to this file. No CMake, no
 torch extension machinery: the library is plain C ABI over the CUDA runtime.
+Beside it goes ``_bind.so`` (``csrc/awq_bind.cpp``, host code), the CPython
+module that takes the tensors of the decoder operators' calls apart.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libawqmoe.so")
+BIND = os.path.join(HERE, "_bind.so")
 SOURCES = ["awq_moe_api.cu", "awq_moe_route.cu", "awq_moe_gemm.cu", "awq_moe_fused.cu", "awq_moe_prepare.cu",
            "awq_moe_sliced.cu", "awq_moe_tc.cu",
            "awq_moe_floor.cu", "awq_decoder_api.cu", "awq_norm.cu", "awq_rope.cu", "awq_attn.cu",
@@ -37,11 +40,36 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _bind_command(obj: str, src: str):
+    """g++ compile of the binding module against the installed torch."""
+    import importlib.util
+    import sysconfig
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = os.path.join(torch_dir, "include")
+    dirs = [include, os.path.join(include, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+            sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-Wall"]
+    for d in dirs:
+        cmd += ["-isystem", d]
+    link = ["g++", "-shared", "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-L", HERE, "-l:libawqmoe.so", "-Wl,-rpath,$ORIGIN"]
+    return cmd + ["-c", src, "-o", obj], link
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _link(cmd, inputs, target: str) -> None:
+    tmp = target + f".tmp{os.getpid()}"
+    r = subprocess.run(cmd + ["-o", tmp] + inputs, capture_output=True, text=True)
+    if r.returncode:
+        raise RuntimeError("link failed: " + r.stdout + r.stderr)
+    os.replace(tmp, target)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -59,6 +87,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if verbose:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
+    bind_src, bind_obj = os.path.join(CSRC, "awq_bind.cpp"), os.path.join(BUILD, "awq_bind.o")
+    bind_compile, bind_link = _bind_command(bind_obj, bind_src)
+    bind_stale = force or _stale(bind_obj, [bind_src] + deps_common)
+    lib_jobs = bool(jobs)
+    if bind_stale:
+        jobs.append(bind_compile)
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             res = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -66,14 +100,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if verbose or r.returncode:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
-    if force or jobs or _stale(LIB, objs):
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode:
-            raise RuntimeError("link failed: " + r.stdout + r.stderr)
-        os.replace(tmp, LIB)
+                raise RuntimeError("compilation failed: " + " ".join(cmd))
+    if force or lib_jobs or _stale(LIB, objs):
+        _link([nvcc()] + ARCH + ["-shared", "-cudart", "shared"], objs, LIB)
+    if bind_stale or _stale(BIND, [bind_obj]):
+        _link(bind_link[:2], [bind_obj] + bind_link[2:], BIND)
     return LIB
 
 

@@ -157,6 +157,19 @@ __device__ __forceinline__ float col_sum(float v)
     return v + __shfl_xor_sync(~0u, v, 16);
 }
 
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
 struct BatchView {
     const int32_t *seq_lens;
     const int32_t *s_len;     // lengths of sequences b0 .. b0 + kLens - 1
@@ -815,28 +828,33 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         const Group &gr = s_group[i / (8 * NT)];
         const int r = i % (8 * NT);
         if (r >= gr.rows) continue;
-        float mx = -INFINITY, sum = 0.f;
+        // part e: a warp's last one in its ring, its first one beside it or in
+        // the workspace
+        auto row_of = [&](int e) {
+            const float *const last_part = reinterpret_cast<const float *>(smem + (e >> 1) * G::kStages * G::kStage);
+            return (e & 1 ? last_part : G::kPartsFit ? last_part + 8 * NT * G::kPitch : block_parts + (e >> 1) * kPiece) +
+                   r * G::kPitch;
+        };
+        // a lane per part for the maximum and the sum, then one per 4 columns
+        const float2 ml = (gr.parts >> lane) & 1 ? *reinterpret_cast<const float2 *>(row_of(lane) + DP) : make_float2(-INFINITY, 0.f);
+        const float mx = warp_max(ml.x);
+        const float weight = fast_exp2(ml.x - (mx == -INFINITY ? 0.f : mx));
+        const float sum = warp_sum(weight * ml.y);
         float4 v[(DP + 127) / 128];
 #pragma unroll
         for (int k = 0; k < (DP + 127) / 128; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (uint32_t rest = gr.parts; rest; rest &= rest - 1) {
             const int e = __ffs(rest) - 1;
-            const float *const last_part = reinterpret_cast<const float *>(smem + (e >> 1) * G::kStages * G::kStage);
-            const float *row = (e & 1 ? last_part : G::kPartsFit ? last_part + 8 * NT * G::kPitch : block_parts + (e >> 1) * kPiece) +
-                               r * G::kPitch;
-            const float2 ml = *reinterpret_cast<const float2 *>(row + DP);
-            const float mn = fmaxf(mx, ml.x);
-            const float w0 = mx == -INFINITY ? 0.f : fast_exp2(mx - mn), w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mn);
-            mx = mn;
-            sum = sum * w0 + ml.y * w1;
+            const float f = __shfl_sync(~0u, weight, e);
 #pragma unroll
             for (int k = 0; k < (DP + 127) / 128; ++k)
                 if (4 * lane + 128 * k < DP) {
-                    const float4 x = *reinterpret_cast<const float4 *>(row + 4 * lane + 128 * k);
-                    v[k].x = v[k].x * w0 + x.x * w1;
-                    v[k].y = v[k].y * w0 + x.y * w1;
-                    v[k].z = v[k].z * w0 + x.z * w1;
-                    v[k].w = v[k].w * w0 + x.w * w1;
+                    const float4 x = *reinterpret_cast<const float4 *>(row_of(e) + 4 * lane + 128 * k);
+                    v[k].x += f * x.x;
+                    v[k].y += f * x.y;
+                    v[k].z += f * x.z;
+                    v[k].w += f * x.w;
                 }
         }
         float *const row = piece_of(gr.seg_begin, blockIdx.x) + r * G::kPitch;
@@ -889,16 +907,14 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                 l[i] = ml.y;
                 mx = fmaxf(mx, ml.x);
             }
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
+            mx = warp_max(mx);
             const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
             for (int i = 0; i < kMost; ++i) {
                 w[i] = fast_exp2(w[i] - base);
                 sum += w[i] * l[i];
             }
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
+            sum = warp_sum(sum);
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 128) {
                 const int d = min(d0 + 4 * lane, D - 4);
