@@ -68,12 +68,18 @@ __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void *src,
                  : "memory");
 }
 
-// From L2, and not moved to its use: a batch of these is in flight together.
-__device__ __forceinline__ float4 ld_cg_f4(const float *p)
+__device__ __forceinline__ float4 lds_f4(uint32_t addr)
 {
     float4 v;
-    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
+}
+
+__device__ __forceinline__ int atom_add_acq_rel(int32_t *p, int v)
+{
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr)
@@ -189,14 +195,14 @@ struct BatchView {
 template <int KT>
 struct Cursor {
     int b, s, n, u;
-    int64_t left;             // units from u to the end of the warp's range
+    int left;                 // units from u to the end of the warp's range
 
     __device__ __forceinline__ int units() const { return (n + KT - 1) / KT; }
     // the segment's units that belong to the warp: [u, end())
     __device__ __forceinline__ int end() const
     {
         const int e = units();
-        return left < e - u ? u + static_cast<int>(left) : e;
+        return left < e - u ? u + left : e;
     }
     // to the first unit of the next segment that has any
     __device__ __forceinline__ void next_segment(const BatchView &v)
@@ -238,8 +244,9 @@ struct Geo {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStages = kWarps * kStage > 64 * 1024 ? 2 : 3;
     static constexpr int kSmem = kWarps * kStages * kStage;
+    static constexpr int kJoinRows = kStages * kStage / (4 * kPitch) >= 32 ? 32 : 16;   // pieces' rows over a warp's ring
     static constexpr bool kPartsFit = kStages * kStage >= 2 * 8 * NT * kPitch * 4;     // two parts over a warp's ring
-    static_assert(kSmem <= 225 * 1024 && kStages * kStage >= 8 * NT * kPitch * 4, "a part fits over a warp's ring");
+    static_assert(kSmem <= 225 * 1024 && kStages * kStage >= 8 * NT * kPitch * 4 && kStages * kStage >= kJoinRows * kPitch * 4, "a part fits over a warp's ring");
 
     // 16-byte chunk c of row r, placed so that 8 rows of one chunk fall into
     // different banks. Planes are aligned to a row, so chunk c ^ x of the row
@@ -253,16 +260,8 @@ struct Geo {
 
 // A part of a segment, left by a warp.
 struct PartMeta {
-    int64_t seg_begin;        // flat number of the segment's first unit; -1: none
+    int32_t seg_begin;        // flat number of the segment's first unit; -1: none
     int32_t b, s;
-};
-
-// Neighbouring parts of one segment in a block.
-struct Group {
-    int64_t seg_begin, seg_end;   // flat units
-    uint32_t parts;               // which of the block's parts
-    int32_t b, head0, rows;       // sequence, first query head, query heads
-    int32_t whole;                // the segment lies inside the block
 };
 
 template <typename T, bool FP8, int DP, int NT>
@@ -274,12 +273,10 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     constexpr int kWarps = G::kWarps, kAttnThreads = G::kThreads;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int32_t s_len[kLens];
-    __shared__ int64_t s_scan[kWarps];
-    __shared__ int64_t s_first[2];                                // first sequence of the block, units before it
+    __shared__ int32_t s_scan[kWarps];
+    __shared__ int32_t s_first[2];                                // first sequence of the block, units before it
     __shared__ PartMeta s_meta[2 * kWarps];
-    __shared__ Group s_group[2 * G::kWarps];
-    __shared__ int32_t s_groups;
-    __shared__ int32_t s_joins[2];                                // whether this block joins the first, the last group
+    __shared__ uint32_t s_joins;                                  // cut segments that this block joins
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -312,7 +309,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     // ---- total units, and the block's range
     const int per_thread = (a.batch + kAttnThreads - 1) / kAttnThreads;
     const int b_lo = tid * per_thread, b_hi = min(a.batch, b_lo + per_thread);
-    int64_t mine = 0;
+    int mine = 0;                        // units (the host has checked that they number below 2^31)
     for (int b = b_lo; b < b_hi; ++b) {
         const int raw = a.seq_lens[b], n = view.clamp(raw);
         if (n != raw && blockIdx.x == 0) set_status(a.status, AWQ_ERR_BAD_INDEX);
@@ -320,16 +317,16 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         mine += (n + KT - 1) / KT;
     }
     mine *= view.per_seq;
-    int64_t incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(~0u, incl, o);
+        const int y = __shfl_up_sync(~0u, incl, o);
         if (lane >= o) incl += y;
     }
     if (lane == 31) s_scan[warp] = incl;
     if (tid < 2 * kWarps) s_meta[tid].seg_begin = -1;
     __syncthreads();
-    int64_t total = 0, before = incl - mine;
+    int total = 0, before = incl - mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s_scan[w];
@@ -347,43 +344,43 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         if (a.lse)
             for (int h = tid; h < a.q_heads; h += kAttnThreads) a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
     }
-    const int64_t per_warp = div_up_to_64(total + gridDim.x * kWarps - 1, gridDim.x * kWarps);
-    const int64_t per = per_warp * kWarps;
-    const int64_t begin = blockIdx.x * per, block_end = min(total, begin + per);
+    const int per_warp = (total - 1) / (static_cast<int>(gridDim.x) * kWarps) + 1;
+    const int per = per_warp * kWarps;
+    const int begin = min(total, static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * per, static_cast<int64_t>(total))));
+    const int block_end = total - begin < per ? total : begin + per;
     if (begin >= total) return;
-    if (begin >= before && begin < before + mine) {
-        int b = b_lo;
-        int64_t at = before;
+    if (begin >= before && begin - before < mine) {
+        int b = b_lo, at = before;
         for (; b < b_hi - 1; ++b) {
-            const int64_t u = static_cast<int64_t>((view.clamp(a.seq_lens[b]) + KT - 1) / KT) * view.per_seq;
-            if (begin < at + u) break;
+            const int u = (view.clamp(a.seq_lens[b]) + KT - 1) / KT * view.per_seq;
+            if (begin - at < u) break;
             at += u;
         }
         s_first[0] = b;
         s_first[1] = at;
     }
     __syncthreads();
-    int64_t local = begin + warp * per_warp - s_first[1];
     Cursor<KT> seg;                      // the segment being computed
-    seg.b = static_cast<int>(s_first[0]);
+    seg.b = s_first[0];
+    int local = begin - s_first[1] + warp * per_warp;
     if (a.batch > kLens) {
         view.b0 = seg.b;
         if (tid < kLens) s_len[tid] = view.b0 + tid < a.batch ? a.seq_lens[view.b0 + tid] : 0;
         __syncthreads();
     }
-    seg.left = max(static_cast<int64_t>(0), min(per_warp, total - begin - warp * per_warp));
+    seg.left = max(0, min(per_warp, block_end - begin - warp * per_warp));
     seg.n = view.len(seg.b);
     seg.s = seg.u = 0;
     if (seg.left > 0) {
         while (true) {
-            const int64_t u = static_cast<int64_t>(seg.units()) * view.per_seq;
+            const int u = seg.units() * view.per_seq;
             if (local < u) break;
             local -= u;
             ++seg.b;
             seg.n = view.len(seg.b);
         }
-        seg.s = static_cast<int>(div_up_to_64(local, seg.units()));
-        seg.u = static_cast<int>(local - static_cast<int64_t>(seg.s) * seg.units());
+        seg.s = local / seg.units();
+        seg.u = local - seg.s * seg.units();
     }
 
     // ---- the copies run ahead of the computation
@@ -521,7 +518,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     const uint32_t v_lane = ring_addr + G::kPlane + (FP8 ? G::at((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4)
                                                          : G::at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1));
     int get = 0;                         // ring slot of the next unit
-    int64_t unit0 = begin + warp * per_warp;     // flat number of the segment's first unit of the warp
+    int unit0 = begin + warp * per_warp;  // flat number of the segment's first unit of the warp
     while (seg.left > 0) {
         const int end = seg.end();
         const int kv_head = a.row_tiles == 1 ? seg.s : seg.s / a.row_tiles, tile = seg.s - kv_head * a.row_tiles;
@@ -746,7 +743,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                         }
                     }
                     if (a.lse && g == 0)
-                        a.lse[static_cast<int64_t>(seg.b) * a.q_heads + head0 + r] = (m[nt][j] + log2f(l[nt][j])) * kLn2;
+                        a.lse[static_cast<int64_t>(seg.b) * a.q_heads + head0 + r] = (m[nt][j] + __log2f(l[nt][j])) * kLn2;
                 }
         } else {
             // ---- a part: the warp's first segment in the workspace, its last
@@ -783,170 +780,166 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         float *dst = reinterpret_cast<float *>(ring) + 8 * NT * G::kPitch;
 #pragma unroll 4
         for (int i = 4 * lane; i < 8 * NT * G::kPitch; i += 128)
-            *reinterpret_cast<float4 *>(dst + i) = ld_cg_f4(src + i);
+            *reinterpret_cast<float4 *>(dst + i) = __ldcg(reinterpret_cast<const float4 *>(src + i));
     }
     __syncthreads();
 
     // ---- the warps' parts, in order; those of one segment are neighbours: a
-    // group. Lane e of the first warp looks at part e.
-    if (warp == 0) {
-        const PartMeta mt = s_meta[lane < 2 * kWarps ? lane : 0];
-        const uint32_t valid = __ballot_sync(~0u, lane < 2 * kWarps && mt.seg_begin >= 0);
-        const uint32_t below = valid & ((1u << lane) - 1);
-        const int64_t prev = __shfl_sync(~0u, mt.seg_begin, below ? 31 - __clz(below) : 0);
-        const bool head = ((valid >> lane) & 1) && (!below || prev != mt.seg_begin);
-        const uint32_t heads = __ballot_sync(~0u, head);
-        if (head) {
-            const uint32_t after = heads & ~((2u << lane) - 1);
-            Group gr;
-            gr.seg_begin = mt.seg_begin;
-            gr.seg_end = mt.seg_begin + (view.len(mt.b) + KT - 1) / KT;
-            gr.parts = valid & ~((1u << lane) - 1) & (after ? (after & (0u - after)) - 1 : ~0u);
-            const int kv_head = a.row_tiles == 1 ? mt.s : mt.s / a.row_tiles, tile = mt.s - kv_head * a.row_tiles;
-            gr.b = mt.b;
-            gr.rows = min(kAttnRows, a.group - tile * kAttnRows);
-            gr.head0 = kv_head * a.group + tile * kAttnRows;
-            gr.whole = gr.seg_begin >= begin && gr.seg_end <= block_end;
-            s_group[__popc(heads & ((1u << lane) - 1))] = gr;
-        }
-        if (lane == 0) s_groups = __popc(heads);
+    // group. Lane e of every warp looks at part e; the group's first lane, its
+    // head, knows the rest of it.
+    const PartMeta mt = s_meta[lane < 2 * kWarps ? lane : 0];
+    const uint32_t valid = __ballot_sync(~0u, lane < 2 * kWarps && mt.seg_begin >= 0);
+    const uint32_t below = valid & ((1u << lane) - 1);
+    const int before_it = __shfl_sync(~0u, mt.seg_begin, below ? 31 - __clz(below) : lane);
+    const bool head = ((valid >> lane) & 1) && (!below || before_it != mt.seg_begin);
+    const uint32_t heads = __ballot_sync(~0u, head);
+    int first = 0, last = 0;             // blocks of the head's segment
+    bool cut = false;                    // it does not lie inside this block
+    int head0 = 0, rows = 0;
+    if (head) {
+        const int kv_head = a.row_tiles == 1 ? mt.s : mt.s / a.row_tiles, tile = mt.s - kv_head * a.row_tiles;
+        rows = min(kAttnRows, a.group - tile * kAttnRows);
+        head0 = kv_head * a.group + tile * kAttnRows;
+        first = mt.seg_begin / per;
+        last = (mt.seg_begin + (view.len(mt.b) + KT - 1) / KT - 1) / per;
+        cut = first != last;
     }
-    __syncthreads();
-    const int groups = s_groups;
-    // a row of 4 columns per lane: output, or piece
-    auto finish = [&](const Group &gr, int r, int d, float mx, float sum, float4 v) {
-        const float inv = sum > 0.f ? c.v.scale / sum : sum;     // the sum is 0 (no weight) or NaN otherwise
-        *reinterpret_cast<uint2 *>(static_cast<T *>(a.out.data) + gr.b * a.out.token_stride + (gr.head0 + r) * a.out.head_stride + d) =
-            make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
-        if (a.lse && d == 0) a.lse[static_cast<int64_t>(gr.b) * a.q_heads + gr.head0 + r] = (mx + log2f(sum)) * kLn2;
+    const uint32_t cuts = __ballot_sync(~0u, cut);
+    auto piece_of = [&](int seg_begin, int block) {              // slot 0: the segment that holds the block's first unit
+        return a.parts + (2 * block + (seg_begin <= static_cast<int64_t>(block) * per ? 0 : 1)) * static_cast<int64_t>(kPiece);
     };
-    auto piece_of = [&](int64_t seg_begin, int64_t block) {      // slot 0: the segment that holds the block's first unit
-        return a.parts + (2 * block + (seg_begin <= block * per ? 0 : 1)) * kPiece;
-    };
-    bool pieces = false;
-    for (int i = warp; i < groups * 8 * NT; i += kWarps) {
-        const Group &gr = s_group[i / (8 * NT)];
-        const int r = i % (8 * NT);
-        if (r >= gr.rows) continue;
-        // part e: a warp's last one in its ring, its first one beside it or in
-        // the workspace
-        auto row_of = [&](int e) {
-            const float *const last_part = reinterpret_cast<const float *>(smem + (e >> 1) * G::kStages * G::kStage);
-            return (e & 1 ? last_part : G::kPartsFit ? last_part + 8 * NT * G::kPitch : block_parts + (e >> 1) * kPiece) +
-                   r * G::kPitch;
-        };
-        // a lane per part for the maximum and the sum, then one per 4 columns
-        const float2 ml = (gr.parts >> lane) & 1 ? *reinterpret_cast<const float2 *>(row_of(lane) + DP) : make_float2(-INFINITY, 0.f);
-        const float mx = warp_max(ml.x);
-        const float weight = fast_exp2(ml.x - (mx == -INFINITY ? 0.f : mx));
-        const float sum = warp_sum(weight * ml.y);
-        float4 v[(DP + 127) / 128];
-#pragma unroll
-        for (int k = 0; k < (DP + 127) / 128; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (uint32_t rest = gr.parts; rest; rest &= rest - 1) {
-            const int e = __ffs(rest) - 1;
-            const float f = __shfl_sync(~0u, weight, e);
-#pragma unroll
-            for (int k = 0; k < (DP + 127) / 128; ++k)
-                if (4 * lane + 128 * k < DP) {
-                    const float4 x = *reinterpret_cast<const float4 *>(row_of(e) + 4 * lane + 128 * k);
-                    v[k].x += f * x.x;
-                    v[k].y += f * x.y;
-                    v[k].z += f * x.z;
-                    v[k].w += f * x.w;
-                }
-        }
-        float *const row = piece_of(gr.seg_begin, blockIdx.x) + r * G::kPitch;
-#pragma unroll
-        for (int k = 0; k < (DP + 127) / 128; ++k)
-            if (const int d = 4 * lane + 128 * k; d < D) {
-                if (gr.whole)
-                    finish(gr, r, d, mx, sum, v[k]);
-                else
-                    *reinterpret_cast<float4 *>(row + d) = v[k];
-            }
-        if (!gr.whole && lane == 0) *reinterpret_cast<float2 *>(row + DP) = make_float2(mx, sum);
-        pieces |= !gr.whole;
-    }
-    if (pieces) __threadfence();
-    __syncthreads();
 
-    // ---- segments cut between blocks: only the first and the last group can be
-    if (tid < groups && !s_group[tid].whole) {
-        const int64_t first = div_up_to_64(s_group[tid].seg_begin, per), last = div_up_to_64(s_group[tid].seg_end - 1, per);
-        const bool joins = atomicAdd(a.counters + first, 1) == static_cast<int>(last - first);
-        if (joins) {
-            __threadfence();
-            a.counters[first] = 0;
-        }
-        s_joins[tid ? 1 : 0] = joins;
-    }
-    __syncthreads();
+    // Pass 0 turns a group's parts into an output or the block's piece of a cut
+    // segment, pass 1 the pieces of the cut segments that this block is the last
+    // to leave into outputs. One loop for both: its instructions are fetched
+    // once, and their first fetch is most of the time of a pass.
+    uint32_t todo = heads;
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-        const int gi = k ? groups - 1 : 0;
-        if ((k && groups == 1) || groups == 0 || s_group[gi].whole || !s_joins[k]) continue;
-        const Group gr = s_group[gi];
-        const int first = static_cast<int>(div_up_to_64(gr.seg_begin, per));
-        const int last = static_cast<int>(div_up_to_64(gr.seg_end - 1, per));
-        // a warp per head; a lane per piece for the maxima and sums, then one per 4 columns
-        for (int r = warp; r < gr.rows; r += kWarps) {
-            const float *const row0 = piece_of(gr.seg_begin, first) + r * G::kPitch;
-            const float *const rows = a.parts + r * G::kPitch;       // + 2 p kPiece for a later block p
-            constexpr int kMost = (kAttnMaxCtas + 31) / 32;
-            float w[kMost], l[kMost];
-            float mx = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < kMost; ++i) {
-                const int p = first + lane + 32 * i;
-                const float2 ml = p > last ? make_float2(-INFINITY, 0.f)
-                                           : __ldcg(reinterpret_cast<const float2 *>(
-                                                 (p == first ? row0 : rows + 2 * static_cast<int64_t>(p) * kPiece) + DP));
-                w[i] = ml.x;
-                l[i] = ml.y;
-                mx = fmaxf(mx, ml.x);
-            }
-            mx = warp_max(mx);
-            const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-            for (int i = 0; i < kMost; ++i) {
-                w[i] = fast_exp2(w[i] - base);
-                sum += w[i] * l[i];
-            }
-            sum = warp_sum(sum);
+    for (int pass = 0;; ++pass) {
 #pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 128) {
-                const int d = min(d0 + 4 * lane, D - 4);
-                float4 v = __ldcg(reinterpret_cast<const float4 *>(row0 + d));
-                const float w0 = __shfl_sync(~0u, w[0], 0);
-                v = make_float4(v.x * w0, v.y * w0, v.z * w0, v.w * w0);
-                for (int i = 0; i < kMost && first + 32 * i <= last; ++i) {
-                    float wi = w[0];                 // this round's weights (registers are not indexed)
-#pragma unroll
-                    for (int k = 1; k < kMost; ++k) wi = i == k ? w[k] : wi;
-                    const int top = min(31, last - first - 32 * i);
+        for (; todo; todo &= todo - 1) {
+            const int hl = __ffs(todo) - 1;
+            const uint32_t after = heads & ~((2u << hl) - 1);
+            const uint32_t mask = valid & ~((1u << hl) - 1) & (after ? (after & (0u - after)) - 1 : ~0u);
+            const int seg_begin = __shfl_sync(~0u, mt.seg_begin, hl), b = __shfl_sync(~0u, mt.b, hl);
+            const int h0 = __shfl_sync(~0u, head0, hl), nrows = __shfl_sync(~0u, rows, hl);
+            const int from = __shfl_sync(~0u, first, hl), to = __shfl_sync(~0u, last, hl);
+            const int n = pass ? to - from + 1 : 32 - __clz(mask) - hl;
 #pragma unroll 1
-                    for (int k0 = i ? 0 : 1; k0 <= top; k0 += 16) {      // 16 pieces in flight
-                        float4 x[16];
+            for (int r = warp; r < nrows; r += kWarps) {
+                constexpr int kCols = (DP + 127) / 128;      // turns of 4 columns per lane
+                float mx = -INFINITY, sum = 0.f;
+                float4 v[kCols];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            x[k] = ld_cg_f4(rows + 2 * static_cast<int64_t>(first + 32 * i + min(k0 + k, top)) * kPiece + d);
+                for (int c4 = 0; c4 < kCols; ++c4) v[c4] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int e0 = 0; e0 < n; e0 += G::kJoinRows) {
+                    const int cnt = min(G::kJoinRows, n - e0), e = e0 + lane;
+                    const float *row = reinterpret_cast<const float *>(ring) + lane * G::kPitch;
+                    bool ok = lane < cnt;
+                    if (pass) {
+                        // the pieces' rows into the warp's ring, all in flight together
+                        __syncwarp();
+                        uint32_t dst = ring_addr + 16 * lane;
+                        const float *next = a.parts + 2 * (from + e0) * static_cast<int64_t>(kPiece) + r * G::kPitch + 4 * lane;
+                        const float *src = e0 ? next : piece_of(seg_begin, from) + r * G::kPitch + 4 * lane;
+#pragma unroll 2
+                        for (int k = 0; k < cnt; ++k, dst += 4 * G::kPitch, src = next) {
+                            next += 2 * kPiece;      // every later block has its piece in slot 0
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float f = __shfl_sync(~0u, wi, min(k0 + k, 31));
-                            if (k0 + k <= top) {
-                                v.x += f * x[k].x;
-                                v.y += f * x[k].y;
-                                v.z += f * x[k].z;
-                                v.w += f * x[k].w;
+                            for (int c4 = 0; c4 < DP + 4; c4 += 128)
+                                if (4 * lane + c4 < DP + 4)
+                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 4 * c4), "l"(src + c4)
+                                                 : "memory");
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        __syncwarp();
+                    } else {
+                        // a warp's last part is in its ring, its first one beside it or in the workspace
+                        ok = ok && ((mask >> (hl + e)) & 1);
+                        const int w = (hl + e) >> 1;
+                        row = reinterpret_cast<const float *>(smem + w * G::kStages * G::kStage);
+                        if (!((hl + e) & 1)) row = G::kPartsFit ? row + 8 * NT * G::kPitch : block_parts + w * kPiece;
+                        row += r * G::kPitch;
+                    }
+                    // a lane per row for the maximum, the weights and the sum, then one per 4 columns
+                    const float2 ml = ok ? *reinterpret_cast<const float2 *>(row + DP) : make_float2(-INFINITY, 0.f);
+                    const float top = fmaxf(mx, warp_max(ml.x)), base = top == -INFINITY ? 0.f : top;
+                    const float weight = fast_exp2(ml.x - base), old = fast_exp2(mx - base);
+                    mx = top;
+                    sum = sum * old + warp_sum(weight * ml.y);
+#pragma unroll
+                    for (int c4 = 0; c4 < kCols; ++c4) v[c4] = make_float4(v[c4].x * old, v[c4].y * old, v[c4].z * old, v[c4].w * old);
+                    // four rows at a time
+                    const uint64_t row_addr = G::kPartsFit ? smem_u32(row) : reinterpret_cast<uint64_t>(row);
+                    uint32_t rest = __ballot_sync(~0u, ok);
+#pragma unroll 1
+                    while (rest) {
+                        float4 x[4][kCols];
+                        float f[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const bool some = rest != 0;
+                            const int from_lane = some ? __ffs(rest) - 1 : 0;
+                            rest &= rest - 1;
+                            f[k] = __shfl_sync(~0u, weight, from_lane);
+                            // 32 bits of a shared address where no row is in the workspace
+                            const uint64_t src =
+                                (G::kPartsFit ? __shfl_sync(~0u, static_cast<uint32_t>(row_addr), from_lane)
+                                              : __shfl_sync(~0u, row_addr, from_lane)) +
+                                16 * lane;
+#pragma unroll
+                            for (int c4 = 0; c4 < kCols; ++c4) {
+                                x[k][c4] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (some && 4 * lane + 128 * c4 < DP)
+                                    x[k][c4] = G::kPartsFit ? lds_f4(static_cast<uint32_t>(src) + 512 * c4)
+                                                            : *reinterpret_cast<const float4 *>(src + 512 * c4);
                             }
                         }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int c4 = 0; c4 < kCols; ++c4) {
+                                v[c4].x += f[k] * x[k][c4].x;
+                                v[c4].y += f[k] * x[k][c4].y;
+                                v[c4].z += f[k] * x[k][c4].z;
+                                v[c4].w += f[k] * x[k][c4].w;
+                            }
                     }
                 }
-                if (d0 + 4 * lane < D) finish(gr, r, d, mx, sum, v);
+                if (pass || !((cuts >> hl) & 1)) {
+                    const float inv = sum > 0.f ? c.v.scale / sum : sum;     // the sum is 0 (no weight) or NaN otherwise
+                    T *const out = static_cast<T *>(a.out.data) + b * a.out.token_stride + (h0 + r) * a.out.head_stride;
+#pragma unroll
+                    for (int c4 = 0; c4 < kCols; ++c4)
+                        if (const int d = 4 * lane + 128 * c4; d < D)
+                            *reinterpret_cast<uint2 *>(out + d) =
+                                make_uint2(pack2<T>(v[c4].x * inv, v[c4].y * inv), pack2<T>(v[c4].z * inv, v[c4].w * inv));
+                    if (a.lse && lane == 0) a.lse[static_cast<int64_t>(b) * a.q_heads + h0 + r] = (mx + __log2f(sum)) * kLn2;
+                } else {
+                    float *const piece = piece_of(seg_begin, blockIdx.x) + r * G::kPitch;
+#pragma unroll
+                    for (int c4 = 0; c4 < kCols; ++c4)
+                        if (const int d = 4 * lane + 128 * c4; d < D) *reinterpret_cast<float4 *>(piece + d) = v[c4];
+                    if (lane == 0) *reinterpret_cast<float2 *>(piece + DP) = make_float2(mx, sum);
+                }
             }
         }
+        if (pass || !cuts) break;
+        __syncthreads();
+        if (warp == 0) {
+            bool joins = false;
+            if (cut) {
+                // orders the block's pieces (through the barrier) before the
+                // count, and the others' before what follows it
+                joins = atom_add_acq_rel(a.counters + first, 1) == last - first;
+                if (joins) a.counters[first] = 0;
+            }
+            const uint32_t which = __ballot_sync(~0u, joins);
+            if (lane == 0) s_joins = which;
+        }
+        __syncthreads();
+        todo = s_joins;
     }
 }
 

@@ -1,6 +1,7 @@
 // Host side of the C ABI declared in include/awq_decoder.h: argument checks
 // (nothing is launched on a host-visible error) and the choice of the access
 // width.
+#include <algorithm>
 #include <cmath>
 
 #include "awq_decoder_kernels.cuh"
@@ -195,6 +196,9 @@ awq_status awq_paged_attention(const awq_heads *q, const awq_kv_cache *cache, co
     a.same_strides = cache->k.page_stride == cache->v.page_stride && cache->k.token_stride == cache->v.token_stride &&
                      cache->k.head_stride == cache->v.head_stride;
     a.scale = scale;
+    // units (of at least 16 tokens) are numbered in 32 bits
+    const int64_t most = static_cast<int64_t>(max_pages) * cache->page_size, units = std::min<int64_t>(most, 0x7fffffc0) / 16 + 1;
+    if (units > 0x7fffffff / batch || units * batch > 0x7fffffff / cache->num_heads / a.row_tiles) return AWQ_ERR_UNSUPPORTED_SHAPE;
     const int sms = current_sm_count();
     if (sms <= 0) return AWQ_ERR_CUDA;
     return launch_attention(a, dtype, sms, static_cast<cudaStream_t>(stream));

@@ -162,7 +162,8 @@ AWQ_API awq_status awq_rope_append(const awq_heads *q, const awq_heads *q_out, c
  * seq_lens i32[batch]; lse f32[batch][q_heads], dense, or NULL.
  * batch >= 0 (0 launches nothing), q_heads a multiple of the cache's
  * num_heads, head_dim a multiple of 8 (16 for an e4m3 cache) up to
- * AWQ_ATTN_MAX_HEAD_DIM; q, out and both planes 16-byte aligned with strides
+ * AWQ_ATTN_MAX_HEAD_DIM, batch * num_heads * ceil(q_heads / num_heads / 16) *
+ * (max_pages * page_size / 16 + 1) below 2^31; q, out and both planes 16-byte aligned with strides
  * that are multiples of 16 bytes.
  * The work is split over the sequences' lengths (read on the device) and
  * joined in the same launch. workspace: at least
