@@ -214,6 +214,9 @@ awq_status awq_fp8_gemm(const uint8_t *a, int64_t lda, const float *a_scales, co
     if (M == 0 || N == 0) return AWQ_OK;
     if (!a || !a_scales || !b || !b_scales || !out || !dev_status || lda < K || ldb < K || ldo < N)
         return AWQ_ERR_INVALID_ARG;
+    // the stride of a single row is never used
+    if (M == 1) lda = (lda + 15) / 16 * 16;
+    if (N == 1) ldb = (ldb + 15) / 16 * 16;
     if (!aligned_rows(a, lda, 1, 16) || !aligned_rows(b, ldb, 1, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
         !aligned(out, 2) || !aligned(dev_status, 4))
         return AWQ_ERR_MISALIGNED;

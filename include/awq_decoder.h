@@ -195,8 +195,9 @@ AWQ_API size_t awq_paged_attention_workspace_bytes(int32_t head_dim);
  * (a weight, row n = output n), row stride ldb; b_scales f32[ceil(N / 128)]
  * [ceil(K / 128)], dense; out: 16-bit [M][N], row stride ldo (elements).
  * M, N >= 0 (0 launches nothing), K >= 1. a and b 16-byte aligned with row
- * strides that are multiples of 16 bytes; K itself is any size, as are M and
- * N (out of any alignment is taken).
+ * strides that are multiples of 16 bytes (a single row's stride is not used);
+ * K itself is any size, as are M and N (out of any alignment is taken) up to
+ * 2^30 tiles of 128 x 128.
  */
 AWQ_API awq_status awq_fp8_gemm(const uint8_t *a, int64_t lda, const float *a_scales, const uint8_t *b,
                                 int64_t ldb, const float *b_scales, void *out, int64_t ldo, int32_t M,

@@ -40,8 +40,9 @@
  *     be freed afterwards;
  *   - all memory is owned by the caller; the library allocates nothing and
  *     keeps no state between calls except the looked-up address of the
- *     driver's tensor-map encoder, each device's multiprocessor count and
- *     occupancy of the persistent kernel, and a table of encoded W2 tensor
+ *     driver's tensor-map encoder, each device's multiprocessor count,
+ *     occupancy of the persistent kernel and resident clusters of the 8-bit
+ *     product's kernels (awq_decoder.h), and a table of encoded W2 tensor
  *     maps (a pure function of bank addresses, shape and box);
  *   - work is enqueued asynchronously on `stream` (a cudaStream_t; NULL means
  *     the legacy default stream); the call never synchronises the device and

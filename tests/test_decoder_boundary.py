@@ -127,6 +127,7 @@ def attention(**over):
     (dict(cache=cache(v=plane(page=2052))), ALIGN), (dict(cache=cache(dtype=2, k=plane(token=136))), ALIGN),
     (dict(table=P + 2), ALIGN), (dict(lens=P + 2), ALIGN), (dict(lse=P + 2), ALIGN), (dict(ws=P + 128), ALIGN),
     (dict(status=P + 2), ALIGN), (dict(ws_bytes=1000), awq.ERR_WORKSPACE_TOO_SMALL),
+    (dict(batch=4096, pages=1 << 27, stride=1 << 27), SHAPE), (dict(batch=1 << 30, pages=64, stride=64), SHAPE),
     (dict(ws_bytes=awq.paged_attention_workspace_bytes(64) - 1), awq.ERR_WORKSPACE_TOO_SMALL)])
 def test_attention_refusals(over, code):
     assert attention(**over) == code

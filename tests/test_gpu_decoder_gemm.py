@@ -105,6 +105,19 @@ def test_strided_operands_and_misaligned_output():
         assert bool((flat[:3] == 9.0).all()) and bool((flat[-2:] == 9.0).all())
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 40, 1001), (1, 1, 77), (64, 1, 48), (200, 1, 1000)])
+def test_single_rows_of_any_depth(m, n, k):
+    import awq_int4_moe_gb300 as awq
+    t = torch()
+    a, sa, b, sb = operands(m, n, k)
+    a, b = (x.contiguous() if x.shape[0] == 1 else x for x in (a, b))
+    out, st = t.empty((m, n), device="cuda", dtype=t.float16), t.zeros(1, dtype=t.int32, device="cuda")
+    awq.fp8_gemm(a, sa, b, sb, out, st)
+    t.cuda.synchronize()
+    assert int(st) == 0
+    check(a, sa, b, sb, out)
+
+
 def test_scales_of_zero_and_extremes():
     import awq_int4_moe_gb300 as awq
     t = torch()
