@@ -26,7 +26,8 @@
 // more than 2^8 (P stays below 2^8, the sums are fp32), which drops both the
 // search for the maximum and the scaling of O' from nearly every unit. P
 // enters the tensor core as two 16-bit terms, P = hi + lo, so that its
-// rounding does not reach the output.
+// rounding does not reach the output (one fp16 term where the cache is e4m3
+// and the output bf16).
 //
 // e4m3 planes are expanded to fp16 in registers (exact): a 4-byte lane of an
 // ldmatrix row holds 4 neighbouring elements of the head, so Q's elements are
@@ -269,6 +270,9 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 {
     using G = Geo<FP8, DP, NT>;
     using C = typename std::conditional<FP8, __half, T>::type;   // the tensor core's type
+    // a second term for the rounding of P, except where P is fp16 and the output
+    // bf16, whose own rounding is eight times coarser
+    constexpr bool LO = !(FP8 && std::is_same<T, __nv_bfloat16>::value);
     constexpr int KS = DP / 16, KT = G::KT, SUB = KT / 16;
     constexpr int kWarps = G::kWarps, kAttnThreads = G::kThreads;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -450,15 +454,16 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                     pre_page[i] = 0;
                 }
                 k_at[i] = (pre_page[i] * c.k.page_stride + pre_place[i] * c.k.token_stride) * G::kElem + k_head;
-                v_at[i] = a.same_strides ? k_at[i]
-                                         : (pre_page[i] * c.v.page_stride + pre_place[i] * c.v.token_stride) * G::kElem + v_head;
+                v_at[i] = k_at[i];
+                if (!a.same_strides)
+                    v_at[i] = (pre_page[i] * c.v.page_stride + pre_place[i] * c.v.token_stride) * G::kElem + v_head;
             }
             if (paged16) {
                 const int64_t k_step = kRowsPer * c.k.token_stride * G::kElem, v_step = kRowsPer * c.v.token_stride * G::kElem;
 #pragma unroll
                 for (int sub = 0; sub < SUB; ++sub) {
                     const int good = __shfl_sync(~0u, static_cast<int>(ok[0]), sub);
-                    const int64_t k0 = __shfl_sync(~0u, k_at[0], sub), v0 = __shfl_sync(~0u, v_at[0], sub);
+                    const int64_t k0 = __shfl_sync(~0u, k_at[0], sub), v0 = a.same_strides ? k0 : __shfl_sync(~0u, v_at[0], sub);
                     const char *kp = k_data + k0 + sub_row * c.k.token_stride * G::kElem + ch * 16;
                     const char *vp = v_data + v0 + sub_row * c.v.token_stride * G::kElem + ch * 16;
                     const int have = good ? rows - 16 * sub - sub_row : 0;       // rows from this lane's first on
@@ -675,7 +680,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                     for (int h = 0; h < 2; ++h) {
                         split2<C>(p[2 * h], p[2 * h + 1], ph[nt][h], pl[nt][h]);
                         ph[nt][h] = movmatrix_trans(ph[nt][h]);
-                        pl[nt][h] = movmatrix_trans(pl[nt][h]);
+                        if constexpr (LO) pl[nt][h] = movmatrix_trans(pl[nt][h]);
                     }
                 }
                 // ---- O' += V' P'
@@ -693,7 +698,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
                                     mma16816<C>(o[i + j][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                                    mma16816<C>(o[i + j][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                                    if constexpr (LO) mma16816<C>(o[i + j][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
                                 }
                             }
                         }
