@@ -420,8 +420,9 @@ bool make_map(CUtensorMap *m, const uint8_t *base, int64_t ld, int rows, int K, 
                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-// Clusters of `size` blocks that the device holds at once (looked up once per
-// device and size: a property of the device and the kernel).
+// Clusters of `size` blocks that the device holds at once, one block on a
+// multiprocessor (looked up once per device and size: a property of the device
+// and the kernel).
 template <typename T, int TN, bool SWAP>
 int resident_clusters(int size)
 {
@@ -461,14 +462,21 @@ awq_status launch_gemm_tile(const GemmArgs &g, const uint8_t *a, int64_t lda, co
     const int KB = (g.K + kKB - 1) / kKB;
     const awq_status r = set_smem(fp8_gemm_kernel<T, TN, SWAP>, G::kSmem);
     if (r) return r;
-    // Blocks per tile: as many, up to 8, as still run all at once (one token, N
-    // = 3584, K = 2560, 28 tiles: 9.1 us with 1, 5.0-5.5 with 4 to 8; clusters
-    // that do not all fit cost a second round: 64 tokens, N = K = 5120, 40
-    // tiles: 9.8 us with 6, 15.7 with 7).
+    // Blocks per tile: as many, up to 8, as still run all at once with one block
+    // per multiprocessor (one token, N = 3584, K = 2560, 28 tiles: 9.1 us with 1,
+    // 5.0 with 5, 5.2 with 8), or with kBlocks of them where that gives fewer
+    // than 4 (64 tokens, N = K = 5120, 40 tiles: 10.2 us with 3, 9.8 with 6; 7 do
+    // not all fit: 15.7).
     int cluster = 1;
-    if (TN < 256)
-        for (cluster = std::min(KB, 8); cluster > 1; --cluster)
-            if (tiles <= resident_clusters<T, TN, SWAP>(cluster)) break;
+    if (TN < 256) {
+        auto most = [&](int blocks) {
+            int n = std::min(KB, 8);
+            while (n > 1 && tiles > blocks * resident_clusters<T, TN, SWAP>(n)) --n;
+            return n;
+        };
+        cluster = most(1);
+        if (cluster < 4 && G::kBlocks > 1) cluster = most(G::kBlocks);
+    }
     const int grid = cluster > 1 ? static_cast<int>(tiles) * cluster
                                  : static_cast<int>(std::min<int64_t>(tiles, sms * G::kBlocks));
     return launch(fp8_gemm_kernel<T, TN, SWAP>, dim3(grid), dim3(G::kThreads), G::kSmem, cluster, st, mm, mn, g, cluster);
