@@ -244,10 +244,11 @@ struct Geo {
     static constexpr int kWarps = attn_warps(FP8, DP, NT);
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStages = kWarps * kStage > 64 * 1024 ? 2 : 3;
-    static constexpr int kSmem = kWarps * kStages * kStage;
+    static constexpr int kQPitch = 2 * DP + 16;         // bytes of a q row on its way to the fragments: no bank twice
+    static constexpr int kSmem = kWarps * (kStages * kStage + 8 * kQPitch);
     static constexpr int kJoinRows = kStages * kStage / (4 * kPitch) >= 32 ? 32 : 16;   // pieces' rows over a warp's ring
     static constexpr bool kPartsFit = kStages * kStage >= 2 * 8 * NT * kPitch * 4;     // two parts over a warp's ring
-    static_assert(kSmem <= 225 * 1024 && kStages * kStage >= 8 * NT * kPitch * 4 && kStages * kStage >= kJoinRows * kPitch * 4, "a part fits over a warp's ring");
+    static_assert(kSmem <= 226 * 1024 && kStages * kStage >= 8 * NT * kPitch * 4 && kStages * kStage >= kJoinRows * kPitch * 4, "a part fits over a warp's ring");
 
     // 16-byte chunk c of row r, placed so that 8 rows of one chunk fall into
     // different banks. Planes are aligned to a row, so chunk c ^ x of the row
@@ -288,6 +289,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     const int D = c.head_dim;
     uint8_t *const ring = smem + warp * G::kStages * G::kStage;
     const uint32_t ring_addr = smem_u32(ring);
+    uint8_t *const q_space = smem + kWarps * G::kStages * G::kStage + warp * 8 * G::kQPitch;
     // the workspace: two pieces per block, then the first part of every warp
     constexpr int kPiece = kAttnRows * G::kPitch;
     float *const block_parts = a.parts + (2 * kAttnMaxCtas + static_cast<int64_t>(blockIdx.x) * kWarps) * kPiece;
@@ -536,14 +538,36 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const bool ok = 8 * nt + g < rows_here;
-            const T *q = static_cast<const T *>(a.q.data) + seg.b * a.q.token_stride +
-                         (head0 + (ok ? 8 * nt + g : 0)) * a.q.head_stride;
+            // 16 bytes a lane through shared memory: a fragment's own words would
+            // be 4-byte loads from eight rows at a time
+            const T *q = static_cast<const T *>(a.q.data) + seg.b * a.q.token_stride + head0 * a.q.head_stride;
+            __syncwarp();
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const int d0 = ks * 16 + (FP8 ? 4 * t4 : 2 * t4), d1 = ks * 16 + (FP8 ? 4 * t4 + 2 : 2 * t4 + 8);
-                qf[nt][ks][0] = ok && d0 < D ? __ldg(reinterpret_cast<const uint32_t *>(q + d0)) ^ sign : 0u;
-                qf[nt][ks][1] = ok && d1 < D ? __ldg(reinterpret_cast<const uint32_t *>(q + d1)) ^ sign : 0u;
+            for (int i = lane; i < 8 * (DP / 8); i += 32) {
+                const int r = i / (DP / 8), d = 8 * (i % (DP / 8));
+                const uint4 v = 8 * nt + r < rows_here && d < D
+                                    ? __ldg(reinterpret_cast<const uint4 *>(q + (8 * nt + r) * a.q.head_stride + d))
+                                    : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(q_space + r * G::kQPitch + 2 * d) = v;
+            }
+            __syncwarp();
+            if constexpr (FP8) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(q_space + g * G::kQPitch + ks * 32 + 8 * t4);
+                    qf[nt][ks][0] = v.x ^ sign;
+                    qf[nt][ks][1] = v.y ^ sign;
+                }
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ks += 2) {
+                    uint32_t v[4];
+                    ldmatrix_x4(v, smem_u32(q_space) + (lane & 7) * G::kQPitch + ks * 32 + (lane >> 3) * 16);
+                    qf[nt][ks][0] = v[0] ^ sign;
+                    qf[nt][ks][1] = v[1] ^ sign;
+                    qf[nt][ks + 1][0] = v[2] ^ sign;
+                    qf[nt][ks + 1][1] = v[3] ^ sign;
+                }
             }
             float f = fabsf(a.scale) * c.k.scale * kLog2e;
             if constexpr (FP8 && !std::is_same<T, __half>::value) {
