@@ -406,8 +406,28 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     const bool paged16 = c.page_size % 16 == 0;
     int32_t pre_page[TL], pre_place[TL];
 
-    // the copies' new segment: its KV head, and its q rows into L1 ahead of
-    // the computation (behind the copies they would wait for all of them)
+    // a segment's q rows, 16 bytes a lane: 8 heads of DP elements per tile
+    uint4 q_raw[NT][DP / 32];
+    auto load_q = [&]() {
+        const int kv_head = a.row_tiles == 1 ? seg.s : seg.s / a.row_tiles, tile = seg.s - kv_head * a.row_tiles;
+        const int rows_here = min(kAttnRows, a.group - tile * kAttnRows);
+        const T *q = static_cast<const T *>(a.q.data) + seg.b * a.q.token_stride + (kv_head * a.group + tile * kAttnRows) * a.q.head_stride;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+                const int r = 8 * nt + (32 * i + lane) / (DP / 8), d = 8 * ((32 * i + lane) % (DP / 8));
+                q_raw[nt][i] = r < rows_here && d < D ? __ldg(reinterpret_cast<const uint4 *>(q + r * a.q.head_stride + d))
+                                                      : make_uint4(0, 0, 0, 0);
+            }
+    };
+    // ahead of the copies, behind which it would wait for all of them (where the
+    // registers last that long)
+    constexpr bool kEarlyQ = NT * DP <= 256;
+    if (kEarlyQ && seg.left > 0) load_q();
+
+    // the copies' new segment: its KV head, and its q rows into L1 for when the
+    // computation gets there
     auto new_segment = [&]() {
         const int kv_head = a.row_tiles == 1 ? pre.s : pre.s / a.row_tiles, tile = pre.s - kv_head * a.row_tiles;
         k_head = kv_head * c.k.head_stride * G::kElem;
@@ -511,7 +531,8 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         put = put + 1 == G::kStages ? 0 : put + 1;
         find();
     };
-    new_segment();
+    k_head = (a.row_tiles == 1 ? pre.s : pre.s / a.row_tiles) * c.k.head_stride * G::kElem;
+    v_head = (a.row_tiles == 1 ? pre.s : pre.s / a.row_tiles) * c.v.head_stride * G::kElem;
     find();
 #pragma unroll 1
     for (int i = 0; i < G::kStages - 1; ++i) copy();
@@ -536,19 +557,16 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         uint32_t qf[NT][KS][2];
         float fac[NT][2];                // score to base-2 logarithm
         const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+        if (!kEarlyQ) load_q();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // 16 bytes a lane through shared memory: a fragment's own words would
             // be 4-byte loads from eight rows at a time
-            const T *q = static_cast<const T *>(a.q.data) + seg.b * a.q.token_stride + head0 * a.q.head_stride;
             __syncwarp();
 #pragma unroll
-            for (int i = lane; i < 8 * (DP / 8); i += 32) {
-                const int r = i / (DP / 8), d = 8 * (i % (DP / 8));
-                const uint4 v = 8 * nt + r < rows_here && d < D
-                                    ? __ldg(reinterpret_cast<const uint4 *>(q + (8 * nt + r) * a.q.head_stride + d))
-                                    : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(q_space + r * G::kQPitch + 2 * d) = v;
+            for (int i = 0; i < DP / 32; ++i) {
+                const int at = 32 * i + lane;
+                *reinterpret_cast<uint4 *>(q_space + at / (DP / 8) * G::kQPitch + 16 * (at % (DP / 8))) = q_raw[nt][i];
             }
             __syncwarp();
             if constexpr (FP8) {
@@ -800,6 +818,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         }
         unit0 += end - seg.u;
         seg.next_segment(view);
+        if (kEarlyQ && seg.left > 0) load_q();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
