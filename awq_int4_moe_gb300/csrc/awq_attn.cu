@@ -864,6 +864,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     uint32_t todo = heads;
 #pragma unroll 1
     for (int pass = 0;; ++pass) {
+        int turn = 0;                    // the warp whose turn it is: the rows go round the warps, group after group
 #pragma unroll 1
         for (; todo; todo &= todo - 1) {
             const int hl = __ffs(todo) - 1;
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
             const int from = __shfl_sync(~0u, first, hl), to = __shfl_sync(~0u, last, hl);
             const int n = pass ? to - from + 1 : 32 - __clz(mask) - hl;
 #pragma unroll 1
-            for (int r = warp; r < nrows; r += kWarps) {
+            for (int r = turn <= warp ? warp - turn : warp - turn + kWarps; r < nrows; r += kWarps) {
                 constexpr int kCols = (DP + 127) / 128;      // turns of 4 columns per lane
                 float mx = -INFINITY, sum = 0.f;
                 float4 v[kCols];
@@ -972,6 +973,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                     if (lane == 0) *reinterpret_cast<float2 *>(piece + DP) = make_float2(mx, sum);
                 }
             }
+            turn = (turn + nrows) % kWarps;
         }
         if (pass || !cuts) break;
         __syncthreads();
