@@ -384,14 +384,20 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
         const int r0 = kRows * rank / cluster, r1 = min(kRows * (rank + 1) / cluster, p.M - tok0);
         for (int i = tid; i < (r1 - r0) * kRow4; i += G::kThreads) {
             const int r = r0 + i / kRow4, c = i % kRow4 * 4;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < cluster; ++k) {
-                const float4 v = ld_shared_cluster_f4(map_shared_rank(part + r * G::kPartRow + c, k));
-                sum.x += v.x;
-                sum.y += v.y;
-                sum.z += v.z;
-                sum.w += v.w;
-            }
+            // all blocks' values on their way together, then added in block order
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < cluster) v[k] = ld_shared_cluster_f4(map_shared_rank(part + r * G::kPartRow + c, k));
+            float4 sum = v[0];
+#pragma unroll
+            for (int k = 1; k < 8; ++k)
+                if (k < cluster) {
+                    sum.x += v[k].x;
+                    sum.y += v[k].y;
+                    sum.z += v[k].z;
+                    sum.w += v[k].w;
+                }
             const int n = col_base + c;
             T *dst = out + static_cast<int64_t>(tok0 + r) * p.ldo + n;
             if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
