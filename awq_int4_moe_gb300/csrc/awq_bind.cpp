@@ -179,6 +179,13 @@ double number(PyObject *o)
     return v;
 }
 
+bool truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Bad{nullptr, ""};
+    return v;
+}
+
 // A size as the C ABI's int32.
 int32_t size32(int64_t n, const char *name)
 {
@@ -240,7 +247,7 @@ awq_status rope_append(PyObject *const *a)
     void *pt = c.dense(a[4], "cos_sin", at::kFloat, table.sizes());
     void *pp = c.dense(a[3], "positions", at::kInt, {shape[0]}), *ps = c.dense(a[5], "slots", at::kLong, {shape[0]});
     return awq_rope_append(&hq, &ho, &hk, &hv, static_cast<int32_t *>(pp), static_cast<float *>(pt), size32(table.size(0), "cos_sin"),
-                           size32(table.size(1), "cos_sin"), PyObject_IsTrue(a[10]) == 1, static_cast<int64_t *>(ps), &cache,
+                           size32(table.size(1), "cos_sin"), truth(a[10]), static_cast<int64_t *>(ps), &cache,
                            size32(shape[0], "q"), size32(shape[1], "q"), code, c.status(a[8]), c.stream(a[13]));
 }
 

@@ -24,9 +24,7 @@ __device__ __forceinline__ int64_t div_up_to_64(int64_t x, int64_t y)
 
 // ------------------------------------------------------------ conversions
 
-// One 16-bit activation as fp32 and back (round to nearest even).
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+// fp32 as one 16-bit activation (round to nearest even).
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
 template <>
