@@ -241,16 +241,23 @@ awq_status launch_norm_w(const NormArgs &a, int sms, cudaStream_t st)
     // else a row per block: a chunk per warp for few rows (fewer steps in a
     // row's time), two where the rows are many and the row has more than 12
     // chunks (8192 x 5120: 52.9 us, 62 with one; 4096 x 8192: 23.6, 28.5 with
-    // one, 26 with four). Narrow accesses keep one: they are bound by their
-    // number, not by the memory.
+    // one, 26 with four). Narrow accesses take one up to 32 chunks, then four in
+    // blocks of up to 512 threads, whose registers let two blocks share a
+    // multiprocessor (8192 x 5120, stride 5125: 94.3 us, 143 with two chunks;
+    // 4000 x 6001: 51.9, 81.2; as e4m3 too, 4000 x 4501: 61.9, 57.3).
     if (chunks == 1) return launch_norm_nv<T, WIDE, 1, 128>(a, 128, sms, st);
     if (chunks == 2) return launch_norm_nv<T, WIDE, 2, 128>(a, 128, sms, st);
     if (chunks <= 4) return launch_norm_nv<T, WIDE, 4, 128>(a, 128, sms, st);
     const int most = WIDE && a.rows >= 4 * sms ? 12 : 32;
     if (chunks <= most) return launch_norm_nv<T, WIDE, 1, 1024>(a, 32 * chunks, sms, st);
-    if (chunks <= 64) return launch_norm_nv<T, WIDE, 2, 1024>(a, 32 * ((chunks + 1) / 2), sms, st);
-    if (WIDE || chunks <= 128) return launch_norm_nv<T, WIDE, 4, 1024>(a, 32 * ((chunks + 3) / 4), sms, st);
-    if constexpr (!WIDE) return launch_norm_nv<T, WIDE, 8, 1024>(a, 32 * ((chunks + 7) / 8), sms, st);
+    if constexpr (WIDE) {
+        if (chunks <= 64) return launch_norm_nv<T, WIDE, 2, 1024>(a, 32 * ((chunks + 1) / 2), sms, st);
+        return launch_norm_nv<T, WIDE, 4, 1024>(a, 32 * ((chunks + 3) / 4), sms, st);
+    } else {
+        if (chunks <= 64) return launch_norm_nv<T, WIDE, 4, 512>(a, 32 * ((chunks + 3) / 4), sms, st);
+        if (chunks <= 128) return launch_norm_nv<T, WIDE, 4, 1024>(a, 32 * ((chunks + 3) / 4), sms, st);
+        return launch_norm_nv<T, WIDE, 8, 1024>(a, 32 * ((chunks + 7) / 8), sms, st);
+    }
 }
 
 template <typename T>
