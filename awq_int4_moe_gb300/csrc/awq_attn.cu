@@ -23,8 +23,9 @@
 // so no row of the tile is padding at 8 heads, a head's statistics and its
 // output are in the same lanes, and P moves from the accumulator's layout to
 // the B operand's with movmatrix. m is raised only where a score passes it by
-// more than 2^8 (P stays below 2^8, the sums are fp32), which drops both the
-// search for the maximum and the scaling of O' from nearly every unit. P
+// more than 2^8 (P stays below 2^8 times the maximum's own weight, the sums are
+// fp32), which drops both the search for the maximum and the scaling of O' from
+// nearly every unit. P
 // enters the tensor core as two 16-bit terms, P = hi + lo, so that its
 // rounding does not reach the output (one fp16 term where the cache is e4m3
 // and the output bf16).
@@ -50,6 +51,13 @@ namespace {
 
 constexpr int kLens = 128;              // sequence lengths kept in shared memory
 constexpr float kLazy = 8.f;           // a score raises the maximum when it passes it by this (base 2)
+// fp16 weights are taken against 2^-7 of the maximum: they stay below 2^15 and
+// keep 31 bits below the maximum's own before they vanish (with 24, thousands
+// of tokens of a weight of 2^-25 would vanish beside a single large one).
+constexpr float kRaiseF16 = 7.f;
+// Below every factor that turns a score into a base-2 logarithm: with a factor
+// of 0 (a scale of 0) a masked score of -infinity would be NaN.
+constexpr float kMinFactor = 1.17549435e-38f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -274,6 +282,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
     // a second term for the rounding of P, except where P is fp16 and the output
     // bf16, whose own rounding is eight times coarser
     constexpr bool LO = !(FP8 && std::is_same<T, __nv_bfloat16>::value);
+    constexpr float kRaise = std::is_same<C, __half>::value ? kRaiseF16 : 0.f;
     constexpr int KS = DP / 16, KT = G::KT, SUB = KT / 16;
     constexpr int kWarps = G::kWarps, kAttnThreads = G::kThreads;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) {
                 const int r = 8 * nt + (32 * i + lane) / (DP / 8), d = 8 * ((32 * i + lane) % (DP / 8));
-                q_raw[nt][i] = r < rows_here && d < D ? __ldg(reinterpret_cast<const uint4 *>(q + r * a.q.head_stride + d))
+                q_raw[nt][i] = r < rows_here && d < D ? *reinterpret_cast<const uint4 *>(q + r * a.q.head_stride + d)
                                                       : make_uint4(0, 0, 0, 0);
             }
     };
@@ -439,7 +448,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
         for (int i = lane; i < rows_here * lines; i += 32) {
             const int r = i / lines;
             uint32_t unused;
-            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(unused) : "l"(q + r * a.q.head_stride * 2 + (i - r * lines) * 128));
+            asm volatile("ld.global.u32 %0, [%1];" : "=r"(unused) : "l"(q + r * a.q.head_stride * 2 + (i - r * lines) * 128));
         }
     };
     auto find = [&]() {
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                 const int tok = min(pre_u * KT + row, paged16 ? (pre.n - 1) & ~15 : pre.n - 1);
                 const int page = a.page_shift ? static_cast<int>(__umulhi(tok, a.page_magic) >> (a.page_shift - 1)) : tok;
                 pre_place[i] = tok - page * c.page_size;
-                pre_page[i] = __ldg(a.page_table + pre.b * a.table_stride + page);
+                pre_page[i] = a.page_table[pre.b * a.table_stride + page];
             }
         }
     };
@@ -611,6 +620,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                         qf[nt][ks][i] = pack2<C>(x.x * down, x.y * down);
                     }
             }
+            f = fmaxf(f, kMinFactor);
             fac[nt][0] = __shfl_sync(~0u, f, 8 * t4);
             fac[nt][1] = __shfl_sync(~0u, f, 8 * t4 + 4);
         }
@@ -688,14 +698,14 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                     for (int sub = 0; sub < SUB; ++sub)
                         top[nt][j] = fmaxf(top[nt][j], fmaxf(s[sub][nt][j], s[sub][nt][2 + j]));
                     top[nt][j] *= fac[nt][j];
-                    grew |= top[nt][j] - kLazy > m[nt][j];
+                    grew |= top[nt][j] - (kLazy + kRaise) > m[nt][j];
                 }
             if (__any_sync(~0u, grew)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float mn = fmaxf(m[nt][j], col_max(top[nt][j]));
+                        const float mn = fmaxf(m[nt][j], col_max(top[nt][j]) - kRaise);
                         const float corr = m[nt][j] == mn ? 1.f : fast_exp2(m[nt][j] - mn);
                         m[nt][j] = mn;
                         l[nt][j] *= corr;

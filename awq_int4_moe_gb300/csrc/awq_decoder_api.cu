@@ -157,7 +157,7 @@ awq_status awq_paged_attention(const awq_heads *q, const awq_kv_cache *cache, co
 {
     awq_status r = check_dtype(dtype);
     if (r) return r;
-    if (batch < 0 || q_heads < 1 || max_pages < 1) return AWQ_ERR_INVALID_ARG;
+    if (batch < 0 || q_heads < 1 || max_pages < 1 || !std::isfinite(scale)) return AWQ_ERR_INVALID_ARG;
     r = check_cache(cache, dtype, AWQ_ATTN_MAX_HEAD_DIM);
     if (r) return r;
     const int64_t elem = cache->dtype == AWQ_DTYPE_E4M3 ? 1 : 2;

@@ -248,12 +248,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
             constexpr int F = SWAP ? (TN + 31) / 32 : 1;
             float next[F];
             auto fetch = [&](int kb) {
-                const float w = __ldg(wb + kb);
+                const float w = wb[kb];
 #pragma unroll
                 for (int i = 0; i < F; ++i) {
                     const int tok = SWAP ? n0 + lane + 32 * i : m0 + l;
                     next[i] = tok < p.M && (TN >= 32 || !SWAP || lane < TN)
-                                  ? __ldg(p.a_scales + static_cast<int64_t>(tok) * KB + kb) * w
+                                  ? p.a_scales[static_cast<int64_t>(tok) * KB + kb] * w
                                   : 0.f;
                 }
             };

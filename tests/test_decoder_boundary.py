@@ -133,6 +133,11 @@ def test_attention_refusals(over, code):
     assert attention(**over) == code
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_attention_refuses_a_scale_that_is_not_finite(scale):
+    assert attention(scale=scale) == INVALID
+
+
 def test_attention_workspace():
     assert awq.paged_attention_workspace_bytes(0) == awq.paged_attention_workspace_bytes(264) == 0
     assert awq.paged_attention_workspace_bytes(12) == 0

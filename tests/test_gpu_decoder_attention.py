@@ -176,6 +176,61 @@ def test_peaked_scores():
 
 
 @pytest.mark.parametrize("kind,cache", TYPES)
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.1, 1e-40])
+def test_scales_of_zero_and_below(kind, cache, scale):
+    c = Case(EDGES, 8, 2, 128, kind, cache, 16)
+    c.scale = scale
+    out, lse, st = c.call()
+    assert st == 0
+    c.scale = abs(scale)                                       # what the tolerances take
+    if scale < 0:
+        c.q = -c.q
+    c.check(out, lse)
+
+
+def test_query_of_zeros_with_a_small_cache_scale():
+    c = Case(EDGES, 8, 2, 128, "bf16", "e4m3", 16)
+    c.q.zero_()
+    c.scales = (1e-8, 0.03)
+    out, lse, st = c.call()
+    assert st == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("kind,cache", TYPES)
+def test_many_small_weights_beside_a_large_one(kind, cache):
+    """Token 0 outweighs each other one by 2^26.6 and has values of 0: the output
+    is what the other 2,499 leave. A weight in fp16 is off by at most 2^-25 of
+    2^7 times the largest one, which adds 2^-32 per token to the tolerance
+    (nothing for a bf16 cache). Segments outnumber the warps, so that whole
+    ones are in a single warp."""
+    t = torch()
+    n, few = 2500, [0, 77, 159]
+    c = Case([n] * 160, 8, 8, 64, kind, cache, 64, spare=0)
+    first = c.table[:, 0].long()
+    raw = t.zeros(c.kc.shape, device="cuda")
+    raw[first, 0, :, 0] = 11.0 / c.scales[0]
+    c.kc.copy_(raw.to(c.kc.dtype))
+    raw.fill_(400.0 if cache == "e4m3" else 12.0)
+    raw[first, 0] = 0.0
+    c.vc.copy_(raw.to(c.vc.dtype))
+    c.q.zero_()
+    c.q[:, :, 0] = 13.4
+    out, lse, st = c.call()
+    assert st == 0
+    u = 2.0 ** -11 if kind == "f16" else 2.0 ** -8
+    for b in few:
+        k, v = c.rows(b)
+        s = t.einsum("hd,nhd->hn", c.q[b].double(), k) * c.scale
+        want = t.einsum("hn,nhd->hd", t.softmax(s, 1), v)
+        relative = u + 2 * (64 + 8) * 2.0 ** -23 * float(s.max()) + 2.0 ** -20 + 2 * (n / 16 + 384) * 2.0 ** -24
+        relative += 2.0 ** -12 if kind == "bf16" and cache == "e4m3" else 0.0
+        tol = want * relative + 2.0 ** -25 + (0.0 if cache == "bf16" else n * 2.0 ** -32 * float(v.max()))
+        err = (out[b].double() - want).abs()
+        assert float(tol.max()) < 0.1 * float(want.min()) and bool((err <= tol).all()), float((err - tol).max())
+
+
+@pytest.mark.parametrize("kind,cache", TYPES)
 def test_values_past_the_end_do_not_matter(kind, cache):
     """NaN and infinities in free pages and in the places after a sequence's
     last token; the result has the same bits as with zeros there."""
