@@ -231,10 +231,17 @@ struct Cursor {
 
 // Warps of a block. An e4m3 unit costs about 2,800 cycles of a warp's time
 // and is due every 350 cycles of a multiprocessor, so that 8 warps only just
-// keep up with the memory; 16-bit units take half of that. Two tiles of
-// heads need the registers of 8 warps, 16-bit rows of 256 elements the shared
-// memory of 4 (16 KB a unit).
-constexpr int attn_warps(bool fp8, int dp, int nt) { return !fp8 && dp == 256 ? 4 : fp8 && nt == 1 && dp <= 128 ? 12 : 8; }
+// keep up with the memory; 16-bit units take half of that. 12 for 16-bit rows
+// of 64 as well (128 sequences of up to 1500, 8 heads: 38.3 us, 42.8 with 8;
+// 64 / 8 heads: 42.6, 47.4; 256 of 512, 20 / 4 heads: 31.0, 29.2), but not for
+// those of 128 (1 of 131071, 32 / 4 heads: 54.1 us, 51.6 with 8). Two tiles of
+// heads need the registers of 8 warps (64 of up to 4000, 64 / 4 heads, e4m3:
+// 46.7 us, 51.3 with 12), 16-bit rows of 256 elements the shared memory of 4
+// (16 KB a unit).
+constexpr int attn_warps(bool fp8, int dp, int nt)
+{
+    return !fp8 && dp == 256 ? 4 : nt == 1 && dp <= (fp8 ? 128 : 64) ? 12 : 8;
+}
 
 // NT: tiles of 8 query heads.
 template <bool FP8, int DP, int NT>
