@@ -224,6 +224,52 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a, int st
                             a.scales + row * ((a.cols + AWQ_FP8_BLOCK - 1) / AWQ_FP8_BLOCK), lane);
 }
 
+// Steps of a warp and blocks of a multiprocessor where there are many steps
+// (6000 x 8192, row stride 8448: 24.3 us; 4 steps with 5 blocks 28.6, with 3
+// blocks 26.7; 8 steps with 2 blocks 25.3).
+constexpr int kManySteps = 4, kManyBlocks = 4;
+
+// The same for many steps, with a grid that stays: a warp goes on to the steps
+// that are all the grid's warps further (row_step rows and col_step times U
+// steps), whose loads are on their way while the present ones are written.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256, kManyBlocks) quantize_many_kernel(const QuantArgs a, int steps_per_row, int row_step, int col_step)
+{
+    constexpr int U = kManySteps, kCols = 32 * Columns<WIDE>::kElems;
+    const int lane = threadIdx.x & 31;
+    const int first = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    int64_t row = first / steps_per_row;
+    int step = first - static_cast<int>(row) * steps_per_row;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    RawCols x[U];
+    auto fetch = [&]() {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            x[u] = load_raw_cols<T, WIDE>(static_cast<const T *>(a.x) + row * a.ldx,
+                                          (step * U + u) * kCols + Columns<WIDE>::first(0, 32, lane), a.cols);
+    };
+    if (row < a.rows) fetch();
+    while (row < a.rows) {                              // whole warps
+        float v[U][Columns<WIDE>::kElems];
+#pragma unroll
+        for (int u = 0; u < U; ++u) unpack_cols<T, WIDE>(x[u], v[u]);
+        const int64_t at = row;
+        const int c0 = step * U * kCols + Columns<WIDE>::first(0, 32, lane);
+        row += row_step;
+        step += col_step;
+        if (step >= steps_per_row) {
+            step -= steps_per_row;
+            ++row;
+        }
+        if (row < a.rows) fetch();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            quantize_cols<WIDE>(v[u], c0 + u * kCols, a.cols, a.q + at * a.ldq,
+                                a.scales + at * ((a.cols + AWQ_FP8_BLOCK - 1) / AWQ_FP8_BLOCK), lane);
+    }
+}
+
 template <typename T, bool WIDE, int NV, int THREADS>
 awq_status launch_norm_nv(const NormArgs &a, int threads, int sms, cudaStream_t st)
 {
@@ -279,11 +325,20 @@ awq_status launch_quantize_u(const QuantArgs &a, cudaStream_t st)
 template <typename T, bool WIDE>
 awq_status launch_quantize_w(const QuantArgs &a, int sms, cudaStream_t st)
 {
-    // Two steps a warp where there are several rounds of them (6000 x 8192: 32.4
-    // us with one, 27.0 with two, 26.4 with four; 16384 x 2560: 27.6, 23.1,
-    // 24.9), one where the warps should spread (48 x 4096: 1.3 us, 1.5, 1.7)
-    const int per = 32 * Columns<WIDE>::kElems;
-    const int64_t steps = static_cast<int64_t>(a.rows) * ((a.cols + per - 1) / per);
+    // One step a warp where the warps should spread (48 x 4096: 1.2 us, 1.5 with
+    // two), two where there are several rounds of them (2000 x 2560: 3.1 us;
+    // 16384 x 2560: 27.6 us with one, 23.0 with two), and a grid that stays where
+    // there are many rounds and few of its steps lie past a row's end (16384 x
+    // 2560: 22.0 us; 6000 x 8192, stride 8448: 24.3, 26.6 with two steps a warp;
+    // 8000 x 2560: 12.0, 12.3; but 4000 x 2560: 7.3, 6.1, and 16384 x 400: 6.6, 4.5).
+    const int per = 32 * Columns<WIDE>::kElems, row_steps = (a.cols + per - 1) / per;
+    const int many_steps = (row_steps + kManySteps - 1) / kManySteps;
+    const int64_t steps = static_cast<int64_t>(a.rows) * row_steps;
+    if (steps >= 400ll * sms && 4ll * kManySteps * many_steps <= 5ll * row_steps) {
+        const int warps = 8 * kManyBlocks * sms;
+        return launch(quantize_many_kernel<T, WIDE>, dim3(kManyBlocks * sms), dim3(256), 0, 1, st, a, many_steps,
+                      warps / many_steps, warps % many_steps);
+    }
     return steps >= 64ll * sms ? launch_quantize_u<T, WIDE, 2>(a, st) : launch_quantize_u<T, WIDE, 1>(a, st);
 }
 

@@ -163,6 +163,21 @@ def test_quantize(rows, cols, pad, kind):
     assert float(top[-1, :128].max()) == 448.0
 
 
+@pytest.mark.parametrize("rows,cols,pad", [(17000, 1024, 0), (8001, 2560, 8), (3001, 2563, 2), (40, 200001, 0), (500, 40960, 0)])
+def test_quantize_of_many_rows(rows, cols, pad):
+    import awq_int4_moe_gb300 as awq
+    t = torch()
+    wide = t.full((rows, cols + pad), 9.0, device="cuda").bfloat16()
+    x = wide[:, :cols]
+    x.copy_(data(cols, rows, cols))
+    q = t.zeros((rows, cols + pad), device="cuda", dtype=t.uint8).view(t.float8_e4m3fn)
+    sc = t.full((rows, (cols + 127) // 128), -1.0, device="cuda")
+    awq.quantize_fp8(x, q[:, :cols], sc)
+    t.cuda.synchronize()
+    check_groups(x.double(), q[:, :cols], sc)
+    assert int(q.view(t.uint8)[:, cols:].sum()) == 0
+
+
 @pytest.mark.parametrize("cols", [256, 250])
 def test_quantize_non_finite(cols):
     import awq_int4_moe_gb300 as awq
