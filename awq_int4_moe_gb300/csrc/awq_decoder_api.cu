@@ -96,6 +96,7 @@ awq_status awq_quantize_fp8(const void *x, int64_t ldx, uint8_t *q, int64_t ldq,
     awq_status r = check_dtype(dtype);
     if (r) return r;
     if (rows < 0 || cols < 1) return AWQ_ERR_INVALID_ARG;
+    if (cols > 1 << 30) return AWQ_ERR_UNSUPPORTED_SHAPE;    // columns are counted in 32 bits
     if (rows == 0) return AWQ_OK;
     if (!x || !q || !scales || ldx < cols || ldq < cols) return AWQ_ERR_INVALID_ARG;
     if (!aligned(x, 2) || !aligned(scales, 4)) return AWQ_ERR_MISALIGNED;
@@ -211,6 +212,7 @@ awq_status awq_fp8_gemm(const uint8_t *a, int64_t lda, const float *a_scales, co
     awq_status r = check_dtype(dtype);
     if (r) return r;
     if (M < 0 || N < 0 || K < 1) return AWQ_ERR_INVALID_ARG;
+    if (M > 1 << 30 || N > 1 << 30 || K > 1 << 30) return AWQ_ERR_UNSUPPORTED_SHAPE;    // counted in 32 bits
     if (M == 0 || N == 0) return AWQ_OK;
     if (!a || !a_scales || !b || !b_scales || !out || !dev_status || lda < K || ldb < K || ldo < N)
         return AWQ_ERR_INVALID_ARG;

@@ -82,7 +82,7 @@ AWQ_API awq_status awq_add_rmsnorm(const void *x, int64_t ldx, const void *resid
  * 128 columns: the quantisation of awq_add_rmsnorm without the norm (for the
  * operand of a product that no norm precedes). x: 16-bit [rows][cols], row
  * stride ldx; q: e4m3 [rows][cols], row stride ldq; scales: f32[rows][ceil(
- * cols / 128)], dense. rows >= 0 (0 launches nothing), cols >= 1, any size.
+ * cols / 128)], dense. rows >= 0 (0 launches nothing), cols 1..2^30.
  */
 AWQ_API awq_status awq_quantize_fp8(const void *x, int64_t ldx, uint8_t *q, int64_t ldq, float *scales,
                                     int32_t rows, int32_t cols, int32_t dtype, void *stream);
@@ -194,10 +194,9 @@ AWQ_API size_t awq_paged_attention_workspace_bytes(int32_t head_dim);
  * dense (as awq_add_rmsnorm and awq_quantize_fp8 write them); b: e4m3 [N][K]
  * (a weight, row n = output n), row stride ldb; b_scales f32[ceil(N / 128)]
  * [ceil(K / 128)], dense; out: 16-bit [M][N], row stride ldo (elements).
- * M, N >= 0 (0 launches nothing), K >= 1. a and b 16-byte aligned with row
- * strides that are multiples of 16 bytes (a single row's stride is not used);
- * K itself is any size, as are M and N (out of any alignment is taken) up to
- * 2^30 tiles of 128 x 128.
+ * M, N 0..2^30 (0 launches nothing), K 1..2^30, any size up to 2^30 tiles of
+ * 128 x 128. a and b 16-byte aligned with row strides that are multiples of 16
+ * bytes (a single row's stride is not used); out of any alignment is taken.
  */
 AWQ_API awq_status awq_fp8_gemm(const uint8_t *a, int64_t lda, const float *a_scales, const uint8_t *b,
                                 int64_t ldb, const float *b_scales, void *out, int64_t ldo, int32_t M,

@@ -110,6 +110,10 @@ def test_rope_refusals(over, code):
     assert rope(**over) == code
 
 
+def test_quantize_refuses_rows_that_32_bits_do_not_count():
+    assert awq.lib().awq_quantize_fp8(P, 1 << 31, P, 1 << 31, P, 3, (1 << 30) + 1, 1, None) == SHAPE
+
+
 def attention(**over):
     a = dict(q=heads(), cache=cache(), table=P, stride=10, pages=10, lens=P, batch=3, q_heads=4, dtype=0, scale=0.1,
              out=heads(), lse=P, ws=P, ws_bytes=1 << 26, status=P)
@@ -160,6 +164,11 @@ def gemm(**over):
     (dict(status=P + 2), ALIGN)])
 def test_gemm_refusals(over, code):
     assert gemm(**over) == code
+
+
+@pytest.mark.parametrize("size", [dict(M=(1 << 30) + 1), dict(N=(1 << 30) + 1, ldo=1 << 31), dict(K=(1 << 30) + 1, lda=1 << 31, ldb=1 << 31)])
+def test_gemm_refuses_sizes_that_32_bits_do_not_count(size):
+    assert gemm(**size) == SHAPE
 
 
 def test_binding_checks_types_shapes_and_devices():
