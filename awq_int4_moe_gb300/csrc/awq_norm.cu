@@ -6,7 +6,7 @@
 // Each element is read once and written once per output: a row lives in the
 // registers of one block (or one warp) between its sum of squares and its
 // outputs. About six operations per element: bound by the bytes for many
-// rows (8192 x 5120 with residual, 52.9 us, 6.3 TB/s), by the launch and one
+// rows (8192 x 5120 with residual, 52.8 us, 6.4 TB/s), by the launch and one
 // block's dependent steps for few (1.7 us).
 //
 // Columns are dealt so that a quantisation group never leaves a warp: with
