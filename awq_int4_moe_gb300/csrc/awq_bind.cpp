@@ -8,6 +8,7 @@
 #include <sstream>
 #include <string>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -54,9 +55,11 @@ const at::Tensor &tensor(PyObject *o, const char *name)
 int act_code(at::ScalarType t) { return t == at::kHalf ? AWQ_DTYPE_F16 : t == at::kBFloat16 ? AWQ_DTYPE_BF16 : -1; }
 
 // The arguments of one call: the first tensor gives the device that all others
-// have to be on, and the stream.
+// have to be on, and the stream; the device is the current one while the call
+// lives.
 struct Call {
     c10::DeviceIndex device = -1;
+    c10::cuda::OptionalCUDAGuard guard;
 
     void check(const at::Tensor &t, const char *name, at::ScalarType type, at::IntArrayRef shape)
     {
@@ -158,8 +161,9 @@ struct Call {
     }
 
     // A stream handle, or None for the device's current stream.
-    void *stream(PyObject *o) const
+    void *stream(PyObject *o)
     {
+        if (c10::cuda::current_device() != device) guard.set_index(device);
         if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device).stream();
         void *p = PyLong_AsVoidPtr(o);
         if (PyErr_Occurred()) throw Bad{nullptr, ""};
