@@ -414,12 +414,20 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
                     if (n + j < p.N) dst[j] = from_f32<T>(f[j]);
             }
         }
-        cluster_sync();                  // no block leaves while its sums are read
+        // no block leaves while its sums are read; all that this warp reads has
+        // arrived (it went into the sums), and it has written nothing that the
+        // others wait for
+        __syncwarp();
+        cluster_arrive_relaxed();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tc_dealloc(tmem, G::kTmemCols);
+    if (cluster > 1) {
+        __syncwarp();
+        cluster_wait();
+    }
 }
 
 bool make_map(CUtensorMap *m, const uint8_t *base, int64_t ld, int rows, int K, int box_rows)
