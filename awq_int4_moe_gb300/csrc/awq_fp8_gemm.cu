@@ -386,7 +386,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
         // SWAP: rows of the partial sums are tokens; else M-side rows, also tokens
         constexpr int kRows = SWAP ? TN : kTM, kRow4 = (SWAP ? kTM : TN) / 4;
         const int tok0 = SWAP ? n0 : m0, col_base = SWAP ? m0 : n0;
-        const int r0 = kRows * rank / cluster, r1 = min(kRows * (rank + 1) / cluster, p.M - tok0);
+        const int rows = min(kRows, p.M - tok0), r0 = rows * rank / cluster, r1 = rows * (rank + 1) / cluster;
         for (int i = tid; i < (r1 - r0) * kRow4; i += G::kThreads) {
             const int r = r0 + i / kRow4, c = i % kRow4 * 4;
             // all blocks' values on their way together, then added in block order
