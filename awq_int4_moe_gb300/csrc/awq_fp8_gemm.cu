@@ -25,7 +25,7 @@
 // then the MMA issuer; they meet at mbarriers, every wait is bounded.
 //
 // Bound: few tokens by the weights' bytes (1 x 16384 x 16384: 43.3 us, 6.2
-// TB/s), or by start and cluster sum where those are few (1 x 3584 x 2560: 4.6
+// TB/s), or by start and cluster sum where those are few (1 x 3584 x 2560: 4.4
 // us); many tokens by the accumulators' hand-over (8192 x 5120 x 8192: 324 us,
 // 2,120 TFLOP/s; the products alone 216).
 #include <algorithm>
@@ -483,8 +483,8 @@ awq_status launch_gemm_tile(const GemmArgs &g, const uint8_t *a, int64_t lda, co
     if (r) return r;
     // Blocks per tile: as many, up to 8, as still run all at once with one block
     // per multiprocessor (one token, N = 3584, K = 2560, 28 tiles: 9.1 us with 1,
-    // 4.6 with 5, 5.2 with 8), or with kBlocks of them where that gives fewer
-    // than 4 (64 tokens, N = K = 5120, 40 tiles: 10.2 us with 3, 9.5 with 6; 7 do
+    // 4.4 with 5, 5.2 with 8), or with kBlocks of them where that gives fewer
+    // than 4 (64 tokens, N = K = 5120, 40 tiles: 10.2 us with 3, 9.3 with 6; 7 do
     // not all fit: 15.7).
     int cluster = 1;
     if (TN < 256) {
