@@ -388,7 +388,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
         const int tok0 = SWAP ? n0 : m0, col_base = SWAP ? m0 : n0;
         const int rows = min(kRows, p.M - tok0), r0 = rows * rank / cluster, r1 = rows * (rank + 1) / cluster;
         for (int i = tid; i < (r1 - r0) * kRow4; i += G::kThreads) {
-            const int r = r0 + i / kRow4, c = i % kRow4 * 4;
+            const int r = r0 + i / kRow4, c = i % kRow4 * 4, n = col_base + c;
+            if (n >= p.N) continue;      // nothing is read that no store needs: see the barrier below
             // all blocks' values on their way together, then added in block order
             float4 v[8];
 #pragma unroll
@@ -403,7 +404,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
                     sum.z += v[k].z;
                     sum.w += v[k].w;
                 }
-            const int n = col_base + c;
             T *dst = out + static_cast<int64_t>(tok0 + r) * p.ldo + n;
             if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
@@ -415,8 +415,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant
             }
         }
         // no block leaves while its sums are read; all that this warp reads has
-        // arrived (it went into the sums), and it has written nothing that the
-        // others wait for
+        // arrived (the stores above took it), and it has written nothing that
+        // the others wait for
         __syncwarp();
         cluster_arrive_relaxed();
     }
