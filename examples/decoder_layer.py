@@ -136,6 +136,7 @@ def main():
     layer = DecoderLayer(a.batch, a.steps + 8)
     layer.x.normal_()
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())        # weights, zeroed workspaces and x were made there
     with torch.cuda.stream(side):
         for _ in range(2):                               # set-up outside the graph
             layer.step()
