@@ -26,9 +26,9 @@
 // more than 2^8 (P stays below 2^8 times the maximum's own weight, the sums are
 // fp32), which drops both the search for the maximum and the scaling of O' from
 // nearly every unit. P
-// enters the tensor core as two 16-bit terms, P = hi + lo, so that its
-// rounding does not reach the output (one fp16 term where the cache is e4m3
-// and the output bf16).
+// enters the tensor core as two 16-bit terms, P = hi + lo (2^-23 of a weight is
+// lost with fp16, 2^-17 with bf16), so that the numerator takes the weights
+// that the fp32 sum takes and their rounding does not reach the output.
 //
 // e4m3 planes are expanded to fp16 in registers (exact): a 4-byte lane of an
 // ldmatrix row holds 4 neighbouring elements of the head, so Q's elements are
@@ -40,7 +40,7 @@
 // Bound: 4 * group operations per cached element of 1 or 2 bytes, so the
 // bytes decide; the tensor-core tiles have a few times the rate they need. 1
 // sequence of 131071 tokens, 32 / 4 heads of 128, bf16: 51.5 us, 5.2 TB/s; 64 of
-// up to 16000, 64 / 8 heads, e4m3: 169 us, 6.0 TB/s; the fixed part (lengths,
+// up to 16000, 64 / 8 heads, e4m3: 172 us, 5.9 TB/s; the fixed part (lengths,
 // table, first copies, merge, join) is about 9 us of each.
 #include <algorithm>
 #include <type_traits>
@@ -239,7 +239,7 @@ struct Cursor {
 // 64 / 8 heads: 42.6, 47.4; 256 of 512, 20 / 4 heads: 31.0, 29.2), but not for
 // those of 128 (1 of 131071, 32 / 4 heads: 54.1 us, 51.6 with 8). Two tiles of
 // heads need the registers of 8 warps (64 of up to 4000, 64 / 4 heads, e4m3:
-// 46.7 us, 51.3 with 12), 16-bit rows of 256 elements the shared memory of 4
+// 49.7 us, 55.1 with 12), 16-bit rows of 256 elements the shared memory of 4
 // (16 KB a unit).
 constexpr int attn_warps(bool fp8, int dp, int nt)
 {
@@ -289,9 +289,6 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 {
     using G = Geo<FP8, DP, NT>;
     using C = typename std::conditional<FP8, __half, T>::type;   // the tensor core's type
-    // a second term for the rounding of P, except where P is fp16 and the output
-    // bf16, whose own rounding is eight times coarser
-    constexpr bool LO = !(FP8 && std::is_same<T, __nv_bfloat16>::value);
     constexpr float kRaise = std::is_same<C, __half>::value ? kRaiseF16 : 0.f;
     constexpr int KS = DP / 16, KT = G::KT, SUB = KT / 16;
     constexpr int kWarps = G::kWarps, kAttnThreads = G::kThreads;
@@ -742,7 +739,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                     for (int h = 0; h < 2; ++h) {
                         split2<C>(p[2 * h], p[2 * h + 1], ph[nt][h], pl[nt][h]);
                         ph[nt][h] = movmatrix_trans(ph[nt][h]);
-                        if constexpr (LO) pl[nt][h] = movmatrix_trans(pl[nt][h]);
+                        pl[nt][h] = movmatrix_trans(pl[nt][h]);
                     }
                 }
                 // ---- O' += V' P'
@@ -760,7 +757,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
                                     mma16816<C>(o[i + j][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                                    if constexpr (LO) mma16816<C>(o[i + j][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                                    mma16816<C>(o[i + j][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
                                 }
                             }
                         }

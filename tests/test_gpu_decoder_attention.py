@@ -360,3 +360,46 @@ def test_graph_capture_with_new_lengths():
         t.cuda.synchronize()
         assert int(st) == 0
         c.check(out, lse)
+
+
+@pytest.mark.parametrize("kind,cache", TYPES)
+def test_weights_of_tokens_that_cancel(kind, cache):
+    """Two tokens with weights of any 24 bits and values that nearly cancel: the
+    rounding of the weights shows. Scores are one product each, so a weight's
+    error is that of the score's scaling (8 roundings of |s| log2 e <= 1.5), of
+    the exponential and of its two 16-bit terms: 2^-20 with fp16, and 2^-17 (8 +
+    8 bits and the sign of the second term) with bf16."""
+    t = torch()
+    n, dim, heads = 2, 64, 8
+    c = Case([n] * 40, heads, 1, dim, kind, cache, 16, seed=7)
+    g = t.Generator(device="cuda")
+    g.manual_seed(8)
+    first = c.table[:, 0].long()
+    k, v = t.zeros(c.kc.shape, device="cuda"), t.zeros(c.vc.shape, device="cuda")
+    k[first, 1, 0, 0] = 8.0                                      # token 0 scores 0
+    c.kc.copy_(k.to(c.kc.dtype))
+    c.scales = (1.0, 1.0)
+    c.scale = 0.125
+    c.q.zero_()
+    c.q[:, :, 0] = -t.rand((len(c.lens), 1), generator=g, device="cuda").to(c.q.dtype)    # token 1 between -1 and 0
+    weight = t.exp(c.q[:, 0, 0].double())
+    v[first, 1, 0] = t.randn((len(c.lens), dim), generator=g, device="cuda")
+    c.vc.copy_(v.to(c.vc.dtype))
+    v[first, 0, 0] = (-weight[:, None] * c.vc[first, 1, 0].double()).float()
+    c.vc.copy_(v.to(c.vc.dtype))
+    out, lse, st = c.call()
+    assert st == 0
+    u = 2.0 ** -11 if kind == "f16" else 2.0 ** -8
+    split = 2.0 ** -17 if cache == "bf16" else 2.0 ** -20
+    fine = 0
+    for b in range(len(c.lens)):
+        keys, values = c.rows(b)
+        s = t.einsum("hd,nhd->hn", c.q[b].double(), keys.expand(n, heads, dim)) * c.scale
+        p = t.softmax(s, 1)
+        want = t.einsum("hn,nhd->hd", p, values.expand(n, heads, dim))
+        size = t.einsum("hn,nhd->hd", p, values.abs().expand(n, heads, dim))
+        tol = want.abs() * u + (split + 8 * 1.5 * 2.0 ** -24 + 8 * 2.0 ** -24) * size + 2.0 ** -25
+        err = (out[b].double() - want).abs()
+        assert bool((err <= tol).all()), f"sequence {b}: {float((err / tol).max())} times the tolerance"
+        fine += int((tol < 2.0 ** -13 * size).sum())
+    assert cache == "bf16" or fine > 100                       # outputs at which one fp16 term would show
