@@ -273,9 +273,9 @@ __global__ void __launch_bounds__(256, kManyBlocks) quantize_many_kernel(const Q
 template <typename T, bool WIDE, int NV, int THREADS>
 awq_status launch_norm_nv(const NormArgs &a, int threads, int sms, cudaStream_t st)
 {
-    const int rows = THREADS == 128 ? 4 : 1;             // rows of a block
-    const int grid = std::min((a.rows + rows - 1) / rows, sms * std::max(1, 2048 / threads));
-    return launch(norm_kernel<T, WIDE, NV, THREADS>, dim3(grid), dim3(threads), 0, 1, st, a);
+    const int64_t rows = THREADS == 128 ? 4 : 1;         // rows of a block (64 bits: the sum may pass 2^31)
+    const int64_t grid = std::min<int64_t>((a.rows + rows - 1) / rows, sms * std::max(1, 2048 / threads));
+    return launch(norm_kernel<T, WIDE, NV, THREADS>, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, 1, st, a);
 }
 
 template <typename T, bool WIDE>

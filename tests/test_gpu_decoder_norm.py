@@ -217,3 +217,18 @@ def test_same_bits_on_a_side_stream():
     awq.add_rmsnorm(x, w, 1e-6, out=b, stream=side)
     t.cuda.synchronize()
     assert bool((a == b).all())
+
+
+@pytest.mark.parametrize("rows", [2 ** 31 - 1, 2 ** 31 - 3])
+def test_norm_of_as_many_rows_as_there_can_be(rows):
+    """One column: every y is the weight, with the sign of x (x^2 + eps is x^2 in
+    fp32 for the magnitudes taken)."""
+    import awq_int4_moe_gb300 as awq
+    t = torch()
+    x = t.full((rows, 1), 4.0, device="cuda", dtype=t.float16)
+    x[-2:] = t.tensor([[-8.0], [16.0]])
+    out = t.zeros((rows, 1), device="cuda", dtype=t.float16)
+    awq.add_rmsnorm(x, t.full((1,), 3.0, device="cuda", dtype=t.float16), 1e-9, out=out)
+    t.cuda.synchronize()
+    assert out[-2:].flatten().tolist() == [-3.0, 3.0]
+    assert all(bool((part == 3.0).all()) for part in out[:-2].split(1 << 28))
