@@ -4,7 +4,8 @@ Each ``csrc/*.cu`` is compiled to an object in parallel with nvcc, then the
 objects are linked into one shared library next to this file. No CMake, no
 torch extension machinery: the library is plain C ABI over the CUDA runtime.
 Beside it goes ``_bind.so`` (``csrc/awq_bind.cpp``, host code), the CPython
-module that takes the tensors of the decoder operators' calls apart.
+module that takes the tensors of the decoder operators' calls apart; where
+torch is not installed the library is built alone.
 """
 from __future__ import annotations
 
@@ -41,10 +42,14 @@ def nvcc() -> str:
 
 
 def _bind_command(obj: str, src: str):
-    """g++ compile of the binding module against the installed torch."""
+    """g++ compile and link of the binding module against the installed torch;
+    None where there is none."""
     import importlib.util
     import sysconfig
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch_dir = os.path.dirname(spec.origin)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     include = os.path.join(torch_dir, "include")
     dirs = [include, os.path.join(include, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
@@ -88,11 +93,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
     bind_src, bind_obj = os.path.join(CSRC, "awq_bind.cpp"), os.path.join(BUILD, "awq_bind.o")
-    bind_compile, bind_link = _bind_command(bind_obj, bind_src)
-    bind_stale = force or _stale(bind_obj, [bind_src] + deps_common)
+    bind = _bind_command(bind_obj, bind_src)
+    if bind is None:
+        sys.stderr.write("torch is not installed: the library is built without its torch binding\n")
+    bind_stale = bind is not None and (force or _stale(bind_obj, [bind_src] + deps_common))
     lib_jobs = bool(jobs)
     if bind_stale:
-        jobs.append(bind_compile)
+        jobs.append(bind[0])
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             res = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -103,8 +110,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 raise RuntimeError("compilation failed: " + " ".join(cmd))
     if force or lib_jobs or _stale(LIB, objs):
         _link([nvcc()] + ARCH + ["-shared", "-cudart", "shared"], objs, LIB)
-    if bind_stale or _stale(BIND, [bind_obj]):
-        _link(bind_link[:2], [bind_obj] + bind_link[2:], BIND)
+    if bind is not None and (bind_stale or _stale(BIND, [bind_obj])):
+        _link(bind[1][:2], [bind_obj] + bind[1][2:], BIND)
     return LIB
 
 
