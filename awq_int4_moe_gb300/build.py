@@ -62,6 +62,24 @@ def _bind_command(obj: str, src: str):
     return cmd + ["-c", src, "-o", obj], link
 
 
+def _torch_identity() -> str:
+    """The installed torch, whose C++ libraries the binding is linked to."""
+    import importlib.metadata
+    import importlib.util
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"{version} {importlib.util.find_spec('torch').origin}\n"
+
+
+def _read(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -96,7 +114,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     bind = _bind_command(bind_obj, bind_src)
     if bind is None:
         sys.stderr.write("torch is not installed: the library is built without its torch binding\n")
-    bind_stale = bind is not None and (force or _stale(bind_obj, [bind_src] + deps_common))
+    bind_of = os.path.join(BUILD, "awq_bind.torch")          # which torch the binding was built against
+    bind_stale = bind is not None and (force or _stale(bind_obj, [bind_src] + deps_common) or _read(bind_of) != _torch_identity())
     lib_jobs = bool(jobs)
     if bind_stale:
         jobs.append(bind[0])
@@ -112,6 +131,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         _link([nvcc()] + ARCH + ["-shared", "-cudart", "shared"], objs, LIB)
     if bind is not None and (bind_stale or _stale(BIND, [bind_obj])):
         _link(bind[1][:2], [bind_obj] + bind[1][2:], BIND)
+        with open(bind_of, "w") as f:
+            f.write(_torch_identity())
     return LIB
 
 

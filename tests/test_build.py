@@ -37,3 +37,16 @@ def test_library_is_built_where_torch_is_not_installed(commands, monkeypatch, ca
     assert b.build() == b.LIB and os.path.exists(b.LIB)
     assert not of_binding(commands) and not os.path.exists(b.BIND)
     assert "torch" in capsys.readouterr().err
+
+
+def test_binding_is_built_again_for_another_torch(commands, monkeypatch):
+    b.build()
+    assert len(of_binding(commands)) == 1 and os.path.exists(b.BIND)
+    b.build()
+    assert len(of_binding(commands)) == 1                     # nothing has changed
+    real = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0.1" if name == "torch" else real(name))
+    before = len(commands)
+    b.build()
+    assert len(of_binding(commands)) == 2
+    assert len(commands) == before + 2                        # the binding's compilation and its link, nothing else
