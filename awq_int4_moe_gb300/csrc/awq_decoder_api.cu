@@ -46,6 +46,25 @@ awq_status check_cache(const awq_kv_cache *c, int32_t dtype, int max_dim)
     return r ? r : check_plane(c->v, fp8);
 }
 
+// The stride of a dimension of one is never used: 0, which every alignment
+// allows.
+awq_heads used_strides(const awq_heads &h, int32_t tokens, int32_t heads)
+{
+    return awq_heads{h.data, tokens > 1 ? h.token_stride : 0, heads > 1 ? h.head_stride : 0};
+}
+awq_kv_plane used_strides(const awq_kv_plane &p, const awq_kv_cache &c)
+{
+    return awq_kv_plane{p.data, c.num_pages > 1 ? p.page_stride : 0, c.page_size > 1 ? p.token_stride : 0,
+                        c.num_heads > 1 ? p.head_stride : 0, p.scale};
+}
+awq_kv_cache used_strides(const awq_kv_cache &c)
+{
+    awq_kv_cache u = c;
+    u.k = used_strides(c.k, c);
+    u.v = used_strides(c.v, c);
+    return u;
+}
+
 // Every address of the plane's rows is a multiple of `a` bytes.
 bool plane_aligned(const awq_kv_plane &p, int64_t elem, int64_t a)
 {
@@ -127,18 +146,21 @@ awq_status awq_rope_append(const awq_heads *q, const awq_heads *q_out, const awq
     if (!aligned(positions, 4) || !aligned(slots, 8) || !aligned(dev_status, 4) || !aligned(cos_sin, 16))
         return AWQ_ERR_MISALIGNED;
     const int64_t elem = cache->dtype == AWQ_DTYPE_E4M3 ? 1 : 2;
+    const awq_kv_cache uc = used_strides(*cache);
+    const awq_heads uq = used_strides(*q, tokens, q_heads), uo = used_strides(*q_out, tokens, q_heads),
+                    uk = used_strides(*k, tokens, cache->num_heads), uv = used_strides(*v, tokens, cache->num_heads);
     // the widest access that every row, the head and the rotated part allow
     int vec = 1;
     for (int n : {8, 4}) {
-        const bool rows = heads_aligned(*q, 2 * n) && heads_aligned(*q_out, 2 * n) && heads_aligned(*k, 2 * n) &&
-                          heads_aligned(*v, 2 * n) && plane_aligned(cache->k, elem, elem * n) &&
-                          plane_aligned(cache->v, elem, elem * n);
+        const bool rows = heads_aligned(uq, 2 * n) && heads_aligned(uo, 2 * n) && heads_aligned(uk, 2 * n) &&
+                          heads_aligned(uv, 2 * n) && plane_aligned(uc.k, elem, elem * n) &&
+                          plane_aligned(uc.v, elem, elem * n);
         if (rows && cache->head_dim % n == 0 && (interleaved ? rotary_dim : rotary_dim / 2) % n == 0) {
             vec = n;
             break;
         }
     }
-    const RopeArgs a{*q, *q_out, *k, *v, positions, cos_sin, slots, *cache, dev_status, max_positions,
+    const RopeArgs a{uq, uo, uk, uv, positions, cos_sin, slots, uc, dev_status, max_positions,
                      rotary_dim, interleaved != 0, tokens, q_heads};
     const int sms = current_sm_count();
     if (sms <= 0) return AWQ_ERR_CUDA;
@@ -169,15 +191,16 @@ awq_status awq_paged_attention(const awq_heads *q, const awq_kv_cache *cache, co
         if (r) return r;
     }
     if (!page_table || !seq_lens || !workspace || !dev_status || table_stride < max_pages) return AWQ_ERR_INVALID_ARG;
-    if (!heads_aligned(*q, 16) || !heads_aligned(*out, 16) || !plane_aligned(cache->k, elem, 16) ||
-        !plane_aligned(cache->v, elem, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
+    const awq_kv_cache uc = used_strides(*cache);
+    const awq_heads uq = used_strides(*q, batch, q_heads), uo = used_strides(*out, batch, q_heads);
+    if (!heads_aligned(uq, 16) || !heads_aligned(uo, 16) || !plane_aligned(uc.k, elem, 16) || !plane_aligned(uc.v, elem, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
         !aligned(workspace, 256) || !aligned(dev_status, 4))
         return AWQ_ERR_MISALIGNED;
     if (ws_bytes < attn_workspace_bytes(cache->head_dim)) return AWQ_ERR_WORKSPACE_TOO_SMALL;
     AttnArgs a{};
-    a.q = *q;
-    a.out = *out;
-    a.cache = *cache;
+    a.q = uq;
+    a.out = uo;
+    a.cache = uc;
     a.page_table = page_table;
     a.seq_lens = seq_lens;
     a.lse = lse;
@@ -194,8 +217,8 @@ awq_status awq_paged_attention(const awq_heads *q, const awq_kv_cache *cache, co
     // floor(2^(31 + shift) / page_size) + 1 exceeds the quotient by at most 1
     while ((1ll << a.page_shift) < cache->page_size) ++a.page_shift;
     a.page_magic = static_cast<uint32_t>((1ull << (31 + a.page_shift)) / cache->page_size + 1);
-    a.same_strides = cache->k.page_stride == cache->v.page_stride && cache->k.token_stride == cache->v.token_stride &&
-                     cache->k.head_stride == cache->v.head_stride;
+    a.same_strides = uc.k.page_stride == uc.v.page_stride && uc.k.token_stride == uc.v.token_stride &&
+                     uc.k.head_stride == uc.v.head_stride;
     a.scale = scale;
     // units (of at least 16 tokens) are numbered in 32 bits
     const int64_t most = static_cast<int64_t>(max_pages) * cache->page_size, units = std::min<int64_t>(most, 0x7fffffc0) / 16 + 1;

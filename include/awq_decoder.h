@@ -88,7 +88,8 @@ AWQ_API awq_status awq_quantize_fp8(const void *x, int64_t ldx, uint8_t *q, int6
                                     int32_t rows, int32_t cols, int32_t dtype, void *stream);
 
 /* Vectors of one head each, [tokens][heads][head_dim]: element (t, h, d) is
- * data[t * token_stride + h * head_stride + d]. Strides in elements. */
+ * data[t * token_stride + h * head_stride + d]. Strides in elements; that of a
+ * dimension of one is not used. */
 typedef struct {
     void *data;
     int64_t token_stride;
@@ -98,8 +99,9 @@ typedef struct {
 /* One plane (K or V) of a paged cache: element (page, i, h, d) of the page's
  * i-th token is data[page * page_stride + i * token_stride + h * head_stride
  * + d], so that pages of [page_size][heads][dim] and of [heads][page_size]
- * [dim] are both described. Strides in elements. In an e4m3 cache the stored
- * value stands for value * scale; in a 16-bit cache scale must be 1. */
+ * [dim] are both described. Strides in elements; that of a dimension of one is
+ * not used. In an e4m3 cache the stored value stands for value * scale; in a
+ * 16-bit cache scale must be 1. */
 typedef struct {
     void *data;
     int64_t page_stride;

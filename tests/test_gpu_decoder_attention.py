@@ -403,3 +403,29 @@ def test_weights_of_tokens_that_cancel(kind, cache):
         assert bool((err <= tol).all()), f"sequence {b}: {float((err / tol).max())} times the tolerance"
         fine += int((tol < 2.0 ** -13 * size).sum())
     assert cache == "bf16" or fine > 100                       # outputs at which one fp16 term would show
+
+
+@pytest.mark.parametrize("kind,cache", TYPES)
+def test_strides_of_dimensions_of_one_are_not_used(kind, cache):
+    """One sequence, KV head and page: the strides between them carry nothing,
+    so odd ones change neither the result nor what is accepted."""
+    t = torch()
+    c = Case([13], 1, 1, 64, kind, cache, 16, spare=0)
+    want, wl, st = c.call()
+    assert st == 0
+
+    def odd(x, *dims):
+        strides = list(x.stride())
+        for d in dims:
+            assert x.shape[d] == 1
+            strides[d] = 67
+        return x.as_strided(x.shape, strides)
+
+    out = t.full_like(c.q, 9.0)
+    got, gl, st = c.call(q=odd(c.q, 0, 1), k_cache=odd(c.kc, 0, 2), v_cache=odd(c.vc, 0), out=odd(out, 0, 1))
+    assert st == 0 and t.equal(got, want) and t.equal(gl, wl)
+    c = Case([1], 1, 1, 64, kind, cache, 1, spare=0)           # pages of one token
+    want, wl, st = c.call()
+    got, gl, st = c.call(k_cache=odd(c.kc, 0, 1, 2), v_cache=odd(c.vc, 1))
+    assert st == 0 and t.equal(got, want) and t.equal(gl, wl)
+    c.check(got, gl)

@@ -166,3 +166,27 @@ def test_saturation_and_nan_into_e4m3():
                     t.zeros(1, dtype=t.int64, device="cuda"), kc, vc, st, q_out=z.clone())
     got = vc.float().flatten()
     assert float(got[0]) == 448.0 and float(got[1]) == -448.0 and bool(got[2].isnan()) and float(got[3]) == 448.0
+
+
+@pytest.mark.parametrize("kind,cache", [("f16", "f16"), ("bf16", "e4m3")])
+def test_strides_of_dimensions_of_one_are_not_used(kind, cache):
+    """One token, KV head and page of one token: the same bits whatever the
+    strides behind them."""
+    import awq_int4_moe_gb300 as awq
+    t = torch()
+    g = t.Generator(device="cuda")
+    g.manual_seed(5)
+    q, k, v = (t.randn((1, 1, 64), generator=g, device="cuda").to(dtype_of(kind)) for _ in range(3))
+    pos, slots = t.tensor([3], dtype=t.int32, device="cuda"), t.zeros(1, dtype=t.int64, device="cuda")
+    found = []
+    for strides in ((64, 64, 64), (67, 71, 73)):
+        heads = lambda x: x.as_strided((1, 1, 64), (strides[0], strides[1], 1))  # noqa: E731
+        plane = lambda x: x.as_strided((1, 1, 1, 64), (*strides, 1))  # noqa: E731
+        kc, vc = make_cache(1, 1, 1, 64, cache, False), make_cache(1, 1, 1, 64, cache, False)
+        out, st = t.full_like(q, 9.0), t.zeros(1, dtype=t.int32, device="cuda")
+        awq.rope_append(heads(q), heads(k), heads(v), pos, table(10, 64), slots, plane(kc), plane(vc), st, q_out=heads(out),
+                        k_scale=0.5 if cache == "e4m3" else 1.0, v_scale=0.5 if cache == "e4m3" else 1.0)
+        t.cuda.synchronize()
+        assert int(st) == 0 and bool((out != 9.0).any())
+        found.append((out, kc.float(), vc.float()))
+    assert all(t.equal(a, b) for a, b in zip(*found))
