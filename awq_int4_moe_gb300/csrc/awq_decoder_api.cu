@@ -100,6 +100,7 @@ awq_status awq_add_rmsnorm(const void *x, int64_t ldx, const void *residual, int
     if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(residual_out, 2) || !aligned(weight, 2) ||
         !aligned(out, 2) || !aligned(out_scales, 4))
         return AWQ_ERR_MISALIGNED;
+    if (rows == 1) ldx = ldr = ldro = ldo = ldq = 0;    // the stride of a single row is not used
     const bool wide = hidden % 8 == 0 && aligned(weight, 16) && aligned_rows(x, ldx, 2, 16) &&
                       aligned_rows(residual, ldr, 2, 16) && aligned_rows(residual_out, ldro, 2, 16) &&
                       aligned_rows(out, ldo, 2, 16) && aligned_rows(out_q, ldq, 1, 8);
@@ -119,6 +120,7 @@ awq_status awq_quantize_fp8(const void *x, int64_t ldx, uint8_t *q, int64_t ldq,
     if (rows == 0) return AWQ_OK;
     if (!x || !q || !scales || ldx < cols || ldq < cols) return AWQ_ERR_INVALID_ARG;
     if (!aligned(x, 2) || !aligned(scales, 4)) return AWQ_ERR_MISALIGNED;
+    if (rows == 1) ldx = ldq = 0;                       // the stride of a single row is not used
     const bool wide = cols % 8 == 0 && aligned_rows(x, ldx, 2, 16) && aligned_rows(q, ldq, 1, 8);
     const int sms = current_sm_count();
     if (sms <= 0) return AWQ_ERR_CUDA;

@@ -232,3 +232,23 @@ def test_norm_of_as_many_rows_as_there_can_be(rows):
     t.cuda.synchronize()
     assert out[-2:].flatten().tolist() == [-3.0, 3.0]
     assert all(bool((part == 3.0).all()) for part in out[:-2].split(1 << 28))
+
+
+def test_stride_of_a_single_row_is_not_used():
+    """The same accesses, so the same bits, whatever the stride behind the only row."""
+    import awq_int4_moe_gb300 as awq
+    t = torch()
+    for seed in range(8):
+        x, res = (data(seed + 10 * i, 1, 2560).half() for i in range(2))
+        w = (1 + 0.3 * data(seed + 20, 2560)).half()
+        odd = lambda r: r.as_strided((1, r.shape[1]), (r.shape[1] + 5, 1))  # noqa: E731
+        sums = []
+        for view in (lambda r: r, odd):
+            ro, out = t.empty_like(x), t.empty_like(x)
+            q, sc = t.empty((1, 2560), device="cuda", dtype=t.float8_e4m3fn), t.empty((1, 20), device="cuda")
+            awq.add_rmsnorm(view(x), w, 1e-6, residual=view(res), residual_out=view(ro), out=view(out), out_q=view(q), out_scales=sc)
+            q2, sc2 = t.empty_like(q), t.empty_like(sc)
+            awq.quantize_fp8(view(x), view(q2), sc2)
+            sums.append((ro, out, q.view(t.uint8), sc, q2.view(t.uint8), sc2))
+        t.cuda.synchronize()
+        assert all(t.equal(a, b) for a, b in zip(*sums))
