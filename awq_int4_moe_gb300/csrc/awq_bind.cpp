@@ -5,6 +5,8 @@
 // these checks cost several times what the smallest calls take on the device.
 #include <Python.h>
 
+#include <algorithm>
+#include <cmath>
 #include <sstream>
 #include <string>
 
@@ -278,8 +280,9 @@ awq_status paged_attention(PyObject *const *a)
     const at::Tensor &ws = tensor(a[6], "workspace");
     c.check_device(ws, "workspace");
     if (!ws.is_contiguous()) Call::strides(ws, "workspace");
+    const double scale = a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(std::max<int64_t>(shape[2], 1))) : number(a[8]);
     return awq_paged_attention(&hq, &cache, static_cast<int32_t *>(pt), ldt, size32(pages, "page_table"), static_cast<int32_t *>(pl),
-                               size32(shape[0], "q"), size32(shape[1], "q"), code, static_cast<float>(number(a[8])), &ho,
+                               size32(shape[0], "q"), size32(shape[1], "q"), code, static_cast<float>(scale), &ho,
                                static_cast<float *>(ps), ws.data_ptr(), ws.nbytes(), c.status(a[7]), c.stream(a[12]));
 }
 

@@ -111,9 +111,8 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_lens, out, workspace, d
     [batch][q heads][dim]; page_table i32[batch][max pages]; seq_lens
     i32[batch]; lse f32[batch][q heads] or None; scale: 1 / sqrt(dim) where
     None. workspace: zero-filled once, then reused."""
-    code = (_bind or _load()).paged_attention(q, k_cache, v_cache, page_table, seq_lens, out, workspace, dev_status,
-                                              q.shape[-1] ** -0.5 if scale is None else scale, lse, k_scale, v_scale,
-                                              _handle(stream))
+    code = (_bind or _load()).paged_attention(q, k_cache, v_cache, page_table, seq_lens, out, workspace, dev_status, scale, lse,
+                                              k_scale, v_scale, _handle(stream))
     if code:
         raise AwqError(code, "awq_paged_attention")
 

@@ -193,3 +193,12 @@ def test_binding_checks_types_shapes_and_devices():
     with pytest.raises(ValueError, match="CUDA"):
         awq.fp8_gemm(torch.zeros(4, 256).to(f8), torch.zeros(4, 2), torch.zeros(8, 256).to(f8), torch.zeros(1, 2),
                      torch.zeros(4, 8, dtype=f16), torch.zeros(1, dtype=i32))
+
+
+def test_binding_names_the_argument_that_is_no_query():
+    import torch
+    c = torch.zeros(1, 1, 1, 64, dtype=torch.float16)
+    with pytest.raises(TypeError, match="q: expected a tensor, got list"):
+        awq.paged_attention([1.0], c, c, None, None, None, None, None)
+    with pytest.raises(ValueError, match="q: must be a CUDA device tensor"):
+        awq.paged_attention(torch.zeros(1, 2, 0, dtype=torch.float16), c, c, None, None, None, None, None)
