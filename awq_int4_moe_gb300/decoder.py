@@ -102,7 +102,10 @@ def rope_append(q, k, v, positions, cos_sin, slots, k_cache, v_cache, dev_status
 
 def paged_attention_workspace_bytes(head_dim: int) -> int:
     """Workspace bytes of paged_attention at a head size, for any batch."""
-    return int(lib().awq_paged_attention_workspace_bytes(int(head_dim)))
+    head_dim = int(head_dim)
+    if head_dim != C.c_int32(head_dim).value:            # no head size that the C call could be asked about
+        return 0
+    return int(lib().awq_paged_attention_workspace_bytes(head_dim))
 
 
 def paged_attention(q, k_cache, v_cache, page_table, seq_lens, out, workspace, dev_status, scale=None, lse=None,

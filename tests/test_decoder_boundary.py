@@ -202,3 +202,8 @@ def test_binding_names_the_argument_that_is_no_query():
         awq.paged_attention([1.0], c, c, None, None, None, None, None)
     with pytest.raises(ValueError, match="q: must be a CUDA device tensor"):
         awq.paged_attention(torch.zeros(1, 2, 0, dtype=torch.float16), c, c, None, None, None, None, None)
+
+
+def test_attention_workspace_of_sizes_that_32_bits_do_not_hold():
+    for dim in ((1 << 32) + 64, -(1 << 32) + 64, 1 << 31):
+        assert awq.paged_attention_workspace_bytes(dim) == 0
