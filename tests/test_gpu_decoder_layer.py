@@ -121,3 +121,35 @@ def test_graph_replay_matches_eager_steps(example):
         outs.append((layer.x.clone(), layer.residual.clone(), layer.seq_lens.clone()))
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("batch", [1, 5])
+def test_expert_half_against_the_calls_one_by_one_and_the_oracle(example, batch, oracle_lib):
+    """The routing weights and the stage's output bit for bit, and the output
+    within the stage's tolerance of the oracle's."""
+    import numpy as np
+    import synth
+    import torch
+    import awq_int4_moe_gb300 as awq
+    layer = example.DecoderLayer(batch, 8, seed=20 + batch)
+    layer.x.normal_()
+    layer.attention_half()
+    before, o = layer.residual.clone(), layer.o.clone()
+    layer.expert_half()
+    h, res = torch.empty_like(layer.h), torch.empty_like(layer.h)
+    awq.add_rmsnorm(o, layer.norm2, 1e-6, residual=before, residual_out=res, out=h)
+    logits = h.float() @ layer.router.t()
+    ids, w = torch.empty_like(layer.ids), torch.empty_like(layer.weights)
+    awq.moe_router_topk(logits, batch, layer.shape, ids, w)
+    out, status = torch.empty_like(layer.x), torch.zeros_like(layer.status)
+    ws = torch.zeros_like(layer.moe_ws)
+    awq.moe_layer(h, ids, w, batch, layer.shape, layer.experts, out, ws, layer.moe_ws_bytes, status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and int(layer.status) == 0
+    assert torch.equal(h, layer.h) and torch.equal(res, layer.residual)
+    assert torch.equal(ids, layer.ids) and torch.equal(w, layer.weights)
+    assert torch.equal(out, layer.x)
+    expert = synth.ExpertShape(num_experts=512, top_k=10, hidden=2560, inter=160, meta_bytes=4)
+    ref, _ = oracle_lib.layer_from_synth(expert, 20 + batch, 0, h.cpu().numpy(), ids.cpu().numpy(), w.cpu().numpy())
+    err = np.abs(layer.x.cpu().numpy().astype(np.float64) - ref)
+    assert np.all(err <= gc.ATOL + gc.RTOL * np.abs(ref)), float(err.max())
