@@ -190,3 +190,30 @@ def test_strides_of_dimensions_of_one_are_not_used(kind, cache):
         assert int(st) == 0 and bool((out != 9.0).any())
         found.append((out, kc.float(), vc.float()))
     assert all(t.equal(a, b) for a, b in zip(*found))
+
+
+@pytest.mark.parametrize("kind,cache", [("f16", "f16"), ("bf16", "bf16"), ("f16", "e4m3"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("tokens,hq,hk,dim,rotary", [
+    (1300, 20, 4, 128, 128), (2500, 32, 8, 128, 128), (1300, 7, 1, 100, 40), (1217, 5, 2, 13, 6), (1300, 3, 1, 80, 0),
+    (1300, 2, 1, 576, 64), (1216, 1, 1, 1024, 1024)])
+def test_rope_append_of_prompts(tokens, hq, hk, dim, rotary, inter, kind, cache):
+    """From 8 tokens per multiprocessor on a token has two warps, which go over
+    its rows in several turns."""
+    run(tokens, hq, hk, dim, rotary, inter, kind, cache, 16, False, seed=tokens + dim)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_append_of_more_rows_than_a_block_holds(inter):
+    run(9, 64, 8, 128, 128, inter, "f16", "f16", 4, False)      # 80 rows, 32 at once
+    run(9, 90, 5, 128, 64, inter, "bf16", "e4m3", 4, True, in_place=True)
+    run(1300, 24, 4, 128, 64, inter, "bf16", "bf16", 4, True, in_place=True)
+
+
+@pytest.mark.parametrize("page", [5, 16])
+@pytest.mark.parametrize("kind,cache", [("f16", "f16"), ("bf16", "e4m3")])
+def test_rope_append_with_planes_of_different_layouts(page, kind, cache, monkeypatch):
+    turns = iter([True, False])
+    real = make_cache
+    monkeypatch.setitem(globals(), "make_cache", lambda pages, page, heads, dim, kind, first: real(pages, page, heads, dim, kind, next(turns)))
+    run(33, 6, 2, 128, 128, False, kind, cache, page, None)
