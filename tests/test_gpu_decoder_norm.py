@@ -252,3 +252,34 @@ def test_stride_of_a_single_row_is_not_used():
             sums.append((ro, out, q.view(t.uint8), sc, q2.view(t.uint8), sc2))
         t.cuda.synchronize()
         assert all(t.equal(a, b) for a, b in zip(*sums))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,hidden,pad", [
+    # unaligned rows of 4097 to 16384 columns: four chunks a thread
+    (3, 4097, 0), (700, 6001, 0), (2, 8191, 3), (3, 8192, 5), (2, 8193, 0), (400, 12000, 1), (2, 16383, 0),
+    # aligned rows of 257 to 512 columns: two chunks a lane
+    (5, 264, 0), (900, 384, 8), (3, 512, 0),
+    # more rows than the grid's warps: a row per warp that goes on to a second and a third
+    (9733, 128, 0), (25000, 256, 0), (10001, 384, 0), (12000, 1000, 0), (11000, 100, 3), (10007, 300, 1)])
+def test_norm_of_the_other_forms(rows, hidden, pad, kind):
+    run_norm(rows, hidden, kind, True, "yq", pad, seed=rows)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,cols,pad", [(10000, 256, 0), (4000, 2560, 0), (16384, 400, 8), (3000, 515, 2), (9728, 1, 1), (5001, 130, 0),
+                                           (30001, 384, 0)])
+def test_quantize_with_two_steps_a_warp(rows, cols, pad, kind):
+    """From 64 steps per multiprocessor on, below 400 of them or where rows are
+    short."""
+    import awq_int4_moe_gb300 as awq
+    t = torch()
+    wide = t.full((rows, cols + pad), 9.0, device="cuda").to(dtype_of(kind))
+    x = wide[:, :cols]
+    x.copy_(data(cols, rows, cols))
+    q = t.zeros((rows, cols + pad), device="cuda", dtype=t.uint8).view(t.float8_e4m3fn)
+    sc = t.full((rows, (cols + 127) // 128), -1.0, device="cuda")
+    awq.quantize_fp8(x, q[:, :cols], sc)
+    t.cuda.synchronize()
+    check_groups(x.double(), q[:, :cols], sc)
+    assert int(q.view(t.uint8)[:, cols:].sum()) == 0
