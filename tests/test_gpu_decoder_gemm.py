@@ -177,3 +177,13 @@ def test_weight_past_32_bit_offsets():
     assert int(st) == 0
     check(a, sa, tail[:48].contiguous(), sb[:1], out[:, n - 48:])
     assert bool((out[:, : n - 48] == 0).all())
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (1, 40960, 640), (20, 39100, 640), (30, 50000, 144), (50, 40001, 640), (64, 39000, 272),      # weights on the M side
+    (200, 5120, 700), (1100, 1280, 700), (129, 9800, 400), (1025, 1400, 2560)])                 # tiles of 128 x 128
+def test_tiles_of_one_block_and_several_k_blocks(m, n, k):
+    """More tiles than clusters that run at once: a block per tile, which goes
+    on to further tiles where there are more than blocks."""
+    run(m, n, k, "bf16", pad=3, seed=m)
+    run(m, n, k, "f16", seed=m + 1)
