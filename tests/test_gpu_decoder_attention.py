@@ -429,3 +429,50 @@ def test_strides_of_dimensions_of_one_are_not_used(kind, cache):
     got, gl, st = c.call(k_cache=odd(c.kc, 0, 1, 2), v_cache=odd(c.vc, 1))
     assert st == 0 and t.equal(got, want) and t.equal(gl, wl)
     c.check(got, gl)
+
+
+@pytest.mark.parametrize("kind,cache", TYPES)
+@pytest.mark.parametrize("group,hk", [(17, 3), (24, 4), (40, 2)])
+def test_many_heads_of_several(kind, cache, group, hk):
+    """More than one tile of query heads and more than one KV head."""
+    run([33, 0, 700, 1], group * hk, hk, 128, kind, cache, 16, seed=group)
+    run([90, 5], group * hk, hk, 64, kind, cache, 5, seed=group)
+
+
+@pytest.mark.parametrize("kind,cache", TYPES)
+@pytest.mark.parametrize("page", [1, 5, 16, 48])
+@pytest.mark.parametrize("k_first", [False, True])
+def test_planes_of_different_strides(kind, cache, page, k_first):
+    """K's pages with heads before tokens and V's with tokens before heads, and
+    the other way round."""
+    c = Case(EDGES, 8, 2, 128, kind, cache, page, heads_first=k_first, seed=page)
+    other = c.vc.transpose(1, 2).contiguous().transpose(1, 2) if not k_first else c.vc.contiguous()
+    assert c.page == 1 or other.stride() != c.kc.stride()
+    out, lse, st = c.call(v_cache=other)
+    assert st == 0
+    c.check(out, lse)
+    want, wl, _ = c.call()
+    assert bool((out == want).all()) and bool((lse == wl).all())
+
+
+@pytest.mark.parametrize("kind,cache", [("f16", "f16"), ("bf16", "bf16")])
+def test_sums_of_few_tokens(kind, cache):
+    """As check(), with the additions that a few units make in a row: a chain of
+    products per unit, the units of a warp, at most 24 parts of a block and 8
+    pieces of a segment cut between blocks, and the two bf16 terms' own 2^-17."""
+    t = torch()
+    c = Case([1, 2, 7, 16, 40, 64], 8, 2, 64, kind, cache, 16, seed=3)
+    out, lse, st = c.call()
+    assert st == 0
+    u = 2.0 ** -11 if kind == "f16" else 2.0 ** -8
+    for b, n in enumerate(c.lens):
+        k, v = c.rows(b)
+        q = c.q[b].double().view(2, 4, 64)
+        s = t.einsum("hgd,nhd->hgn", q, k) * c.scale
+        want = t.einsum("hgn,nhd->hgd", t.softmax(s, 2), v).reshape(8, 64)
+        d = (64 + 8) * 2.0 ** -23 * float(q.norm(dim=2).max() * k.norm(dim=2).max()) * c.scale
+        sums = (n + 40) * 2.0 ** -24
+        split = 2.0 ** -20 if cache == "f16" else 2.0 ** -17
+        tol = want.abs() * u + (2 * d + split + 2 * sums) * float(v.abs().max()) + 2.0 ** -25
+        err = (out[b].double() - want).abs()
+        assert bool((err <= tol).all()), f"sequence {b}: {float((err / tol).max())} times the tolerance"
