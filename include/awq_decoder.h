@@ -154,9 +154,12 @@ AWQ_API awq_status awq_rope_append(const awq_heads *q, const awq_heads *q_out, c
  * page_size]. Query head h reads KV head h / (q_heads / num_heads):
  *   s[j] = scale * (q . k[j]),  out = sum_j softmax(s)[j] v[j],
  *   lse = log(sum_j exp(s[j]))
- * k and v as the values the cache's codes stand for; scale is any finite number. n = 0 gives out = 0 and
- * lse = -infinity. Pages past a sequence's last token are not read, nor are
- * the places after it. A length outside [0, max_pages * page_size] or a page
+ * k and v as the values the cache's codes stand for; scale is any finite
+ * number. n = 0 gives out = 0 and lse = -infinity. A value of v that is not
+ * finite makes its element of out NaN or infinite, which of the two is not
+ * defined (a weight is multiplied as two terms, the second of any sign or 0);
+ * other elements and lse do not change. Pages past a sequence's last token are
+ * not read, nor are the places after it. A length outside [0, max_pages * page_size] or a page
  * outside [0, num_pages) that is needed sets AWQ_ERR_BAD_INDEX; that
  * sequence's output is then undefined.
  * q, out: 16-bit [batch][q_heads][head_dim] (token_stride = between

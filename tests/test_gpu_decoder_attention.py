@@ -476,3 +476,21 @@ def test_sums_of_few_tokens(kind, cache):
         tol = want.abs() * u + (2 * d + split + 2 * sums) * float(v.abs().max()) + 2.0 ** -25
         err = (out[b].double() - want).abs()
         assert bool((err <= tol).all()), f"sequence {b}: {float((err / tol).max())} times the tolerance"
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_values_that_are_not_finite_stay_in_their_column(kind, bad):
+    """NaN or infinite there, whichever; every other output keeps its bits."""
+    t = torch()
+    c = Case([40, 700, 17], 8, 2, 128, kind, kind, 16, seed=4)
+    want, wl, _ = c.call()
+    c.vc[c.table[0, 1].long(), 3, 0, 5] = bad
+    c.vc[c.table[1, 40].long(), 0, 1, 9] = bad
+    out, lse, st = c.call()
+    assert st == 0
+    hit = t.zeros_like(out, dtype=t.bool)
+    hit[0, :4, 5] = True
+    hit[1, 4:, 9] = True
+    assert bool((out.isfinite() != hit).all())
+    assert bool((out == want)[~hit].all()) and bool((lse == wl).all())
