@@ -40,7 +40,7 @@
 // Bound: 4 * group operations per cached element of 1 or 2 bytes, so the
 // bytes decide; the tensor-core tiles have a few times the rate they need. 1
 // sequence of 131071 tokens, 32 / 4 heads of 128, bf16: 51.5 us, 5.2 TB/s; 64 of
-// up to 16000, 64 / 8 heads, e4m3: 172 us, 5.9 TB/s; the fixed part (lengths,
+// up to 16000, 64 / 8 heads, e4m3: 173 us, 5.9 TB/s; the fixed part (lengths,
 // table, first copies, merge, join) is about 9 us of each.
 #include <algorithm>
 #include <type_traits>
@@ -239,8 +239,9 @@ struct Cursor {
 // 64 / 8 heads: 42.6, 47.4; 256 of 512, 20 / 4 heads: 31.0, 29.2), but not for
 // those of 128 (1 of 131071, 32 / 4 heads: 54.1 us, 51.6 with 8). Two tiles of
 // heads need the registers of 8 warps (64 of up to 4000, 64 / 4 heads, e4m3:
-// 49.7 us, 55.1 with 12), 16-bit rows of 256 elements the shared memory of 4
-// (16 KB a unit).
+// 49.7 us, 55.1 with 12; with heads of 256 the compiler spills 36 to 84 bytes:
+// 55.6 us, bf16 84.2, floors 20 and 40), 16-bit rows of 256 elements the shared
+// memory of 4 (16 KB a unit).
 constexpr int attn_warps(bool fp8, int dp, int nt)
 {
     return !fp8 && dp == 256 ? 4 : nt == 1 && dp <= (fp8 ? 128 : 64) ? 12 : 8;

@@ -291,6 +291,11 @@ awq_status launch_norm_w(const NormArgs &a, int sms, cudaStream_t st)
     // blocks of up to 512 threads, whose registers let two blocks share a
     // multiprocessor (8192 x 5120, stride 5125: 94.3 us, 143 with two chunks;
     // 4000 x 6001: 51.9, 81.2; as e4m3 too, 4000 x 4501: 61.9, 57.3).
+    // Rows that need 1,024 threads with four chunks or more have 64 registers a
+    // thread for them, and the compiler spills: wide from 16385 columns on 200 to
+    // 310 bytes (2000 x 32768 with residual: 127 us bf16, 113 fp16, floor 77),
+    // narrow from 8193 about 100 (2000 x 16383: 135 us, floor 39) and from 16385
+    // 860 (2000 x 32767: 459 us, floor 77).
     if (chunks == 1) return launch_norm_nv<T, WIDE, 1, 128>(a, 128, sms, st);
     if (chunks == 2) return launch_norm_nv<T, WIDE, 2, 128>(a, 128, sms, st);
     if (chunks <= 4) return launch_norm_nv<T, WIDE, 4, 128>(a, 128, sms, st);

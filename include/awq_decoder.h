@@ -57,10 +57,11 @@ typedef enum {
  *     out_scales = max(amax, AWQ_FP8_MIN_AMAX) / 448,
  *     out_q = e4m3(y * (448 / max(amax, AWQ_FP8_MIN_AMAX)))
  * y is taken from r before r is rounded for residual_out, and out_q from y
- * before y is rounded for out. A NaN in a group is left out of its amax and
+ * before y is rounded for out. A row whose sum of squares passes fp32's range
+ * (finite bf16 values can) has y = 0. A NaN in a group is left out of its amax and
  * stays NaN in out_q; an infinity makes its group's scale infinite.
  * x, residual, residual_out, out: 16-bit [rows][hidden], row strides ldx, ldr,
- * ldro, ldo in elements (each >= hidden). weight: 16-bit [hidden]. out_q:
+ * ldro, ldo in elements (each >= hidden; not used for a single row). weight: 16-bit [hidden]. out_q:
  * e4m3 [rows][hidden], row stride ldq. out_scales: f32[rows][ceil(hidden /
  * 128)], dense. residual, residual_out, out and the pair out_q/out_scales may
  * each be NULL, but out or out_q must be given. residual_out may be residual
@@ -158,9 +159,13 @@ AWQ_API awq_status awq_rope_append(const awq_heads *q, const awq_heads *q_out, c
  * number. n = 0 gives out = 0 and lse = -infinity. A value of v that is not
  * finite makes its element of out NaN or infinite, which of the two is not
  * defined (a weight is multiplied as two terms, the second of any sign or 0);
- * other elements and lse do not change. Pages past a sequence's last token are
- * not read, nor are the places after it. A length outside [0, max_pages * page_size] or a page
- * outside [0, num_pages) that is needed sets AWQ_ERR_BAD_INDEX; that
+ * other elements and lse do not change. Held in fewer than 32 bits: a weight, in
+ * two terms of the tensor core's type (fp16: off by at most 2^-23 of it or 2^-32
+ * of the largest one; bf16 cache: 2^-17 of it), and a bf16 query over an e4m3
+ * cache, as fp16 with its head's power of two taken out (off by at most 2^-24 of
+ * its largest element). Pages past a sequence's last token are not read, nor
+ * are the places after it. A length outside [0, max_pages * page_size] or a
+ * page outside [0, num_pages) that is needed sets AWQ_ERR_BAD_INDEX; that
  * sequence's output is then undefined.
  * q, out: 16-bit [batch][q_heads][head_dim] (token_stride = between
  * sequences); page_table i32[batch][max_pages], row stride table_stride;
@@ -194,7 +199,9 @@ AWQ_API size_t awq_paged_attention_workspace_bytes(int32_t head_dim);
  * 128:
  *   out[m][n] = sum over blocks j of 128 columns of K of
  *     a_scales[m][j] * b_scales[n / 128][j] * (sum over k in j of a[m][k] b[n][k])
- * The products are exact, the sums and scales fp32, one rounding at the end.
+ * The products are exact; the tensor core adds a block's 128 to within 2^-17 of
+ * the sum of their magnitudes; the scales and the sum over the blocks are fp32,
+ * with one rounding at the end.
  * a: e4m3 [M][K], row stride lda (bytes); a_scales f32[M][ceil(K / 128)],
  * dense (as awq_add_rmsnorm and awq_quantize_fp8 write them); b: e4m3 [N][K]
  * (a weight, row n = output n), row stride ldb; b_scales f32[ceil(N / 128)]
