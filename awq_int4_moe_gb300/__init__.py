@@ -1,8 +1,9 @@
 """Python binding of the GB300 AWQ int4 MoE expert-stage library.
 
 Thin marshalling layer over the C ABI in ``include/awq_moe.h`` (the expert
-stage) and ``include/awq_decoder.h`` (the decoder layer around it: norm,
-8-bit quantisation and product, rotary cache append, paged attention): every
+stage), ``include/awq_decoder.h`` (the decoder layer around it: norm, 8-bit
+quantisation and product, rotary cache append, paged attention) and
+``include/awq_prompt.h`` (prompts and chunks of new tokens in it): every
 function here has the same name as its C entry point (without the ``awq_``
 prefix), passes ``tensor.data_ptr()`` and the current CUDA stream through
 ctypes, and raises :class:`AwqError` on a non-zero status. All computation
@@ -119,6 +120,7 @@ def lib() -> C.CDLL:
         L.awq_moe_latency_floor.restype = C.c_int
         L.awq_moe_latency_floor.argtypes = [P, i32, SP, WP, P, P, C.c_size_t, P, P]
         decoder.declare(L)
+        prompt.declare(L)
         _lib = L
     return _lib
 
@@ -333,3 +335,6 @@ def moe_latency_floor(topk_ids, M: int, shape, weights: Weights, out, workspace,
 from . import decoder  # noqa: E402
 from .decoder import (DTYPE_BF16, DTYPE_E4M3, DTYPE_F16, FP8_BLOCK, add_rmsnorm, fp8_gemm,  # noqa: E402,F401
                       paged_attention, paged_attention_workspace_bytes, quantize_fp8, rope_append)
+from . import prompt  # noqa: E402
+from .prompt import (chunk_attention, prompt_attention, prompt_attention_workspace_bytes,  # noqa: E402,F401
+                     qk_norm_rope_append)

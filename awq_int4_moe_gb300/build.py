@@ -24,10 +24,12 @@ BIND = os.path.join(HERE, "_bind.so")
 SOURCES = ["awq_moe_api.cu", "awq_moe_route.cu", "awq_moe_gemm.cu", "awq_moe_fused.cu", "awq_moe_prepare.cu",
            "awq_moe_sliced.cu", "awq_moe_tc.cu",
            "awq_moe_floor.cu", "awq_decoder_api.cu", "awq_norm.cu", "awq_rope.cu", "awq_attn.cu",
-           "awq_fp8_gemm.cu"]
+           "awq_fp8_gemm.cu", "awq_prompt_api.cu", "awq_qk_norm.cu", "awq_prompt_attn_f16.cu", "awq_prompt_attn_bf16.cu",
+           "awq_prompt_attn_f16_e4m3.cu", "awq_prompt_attn_bf16_e4m3.cu"]
 HEADERS = ["awq_ptx.cuh", "awq_moe_kernels.cuh", "awq_launch.cuh", "awq_dequant.cuh", "awq_route.cuh",
            "awq_router.cuh", "awq_split.cuh", "awq_tc.cuh", "awq_nvfp4.cuh",
-           "awq_decoder_kernels.cuh"]
+           "awq_decoder_kernels.cuh", "awq_decoder_checks.cuh", "awq_rope.cuh", "awq_prompt_kernels.cuh",
+           "awq_prompt_attn.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -99,6 +101,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     deps_common = [os.path.join(CSRC, h) for h in HEADERS] + [
         os.path.join(ROOT, "include", "awq_moe.h"), os.path.join(ROOT, "include", "awq_decoder.h"),
+        os.path.join(ROOT, "include", "awq_prompt.h"),
         os.path.abspath(__file__)]
     objs, jobs = [], []
     for src in SOURCES:

@@ -1,7 +1,7 @@
-// CPython module behind awq_int4_moe_gb300/decoder.py: takes the tensors of a
+// CPython module behind awq_int4_moe_gb300/decoder.py and prompt.py: takes the tensors of a
 // call apart, checks what the C call cannot see (types, shapes, devices,
-// dense rows), calls the entry point of include/awq_decoder.h on the current
-// stream and returns its status. No computation, no state. In Python alone
+// dense rows), calls the entry point of include/awq_decoder.h or awq_prompt.h on
+// the current stream and returns its status. No computation, no state. In Python alone
 // these checks cost several times what the smallest calls take on the device.
 #include <Python.h>
 
@@ -14,7 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "../../include/awq_decoder.h"
+#include "../../include/awq_prompt.h"
 
 namespace {
 
@@ -162,6 +162,24 @@ struct Call {
         return static_cast<int32_t *>(t.data_ptr());
     }
 
+    // Where the sequences of a packed batch begin, and the last one's end.
+    void *bounds(PyObject *o, int32_t *batch)
+    {
+        const at::Tensor &t = tensor(o, "cu_seqlens");
+        if (t.dim() != 1 || t.size(0) < 1 || t.size(0) > 0x7fffffff)
+            bad_value("cu_seqlens: expected shape (batch + 1,), got " + shape_text(t.sizes()));
+        *batch = static_cast<int32_t>(t.size(0) - 1);
+        return dense(o, "cu_seqlens", at::kInt, t.sizes());
+    }
+
+    const at::Tensor &scratch(PyObject *o)
+    {
+        const at::Tensor &t = tensor(o, "workspace");
+        check_device(t, "workspace");
+        if (!t.is_contiguous()) strides(t, "workspace");
+        return t;
+    }
+
     // A stream handle, or None for the device's current stream.
     void *stream(PyObject *o)
     {
@@ -191,6 +209,12 @@ bool truth(PyObject *o)
     const int v = PyObject_IsTrue(o);
     if (v < 0) throw Bad{nullptr, ""};
     return v;
+}
+
+// The factor of a score: 1 / sqrt(dim) for None.
+float score_scale(PyObject *o, int64_t dim)
+{
+    return static_cast<float>(o == Py_None ? 1.0 / std::sqrt(static_cast<double>(std::max<int64_t>(dim, 1))) : number(o));
 }
 
 // A size as the C ABI's int32.
@@ -303,6 +327,81 @@ awq_status fp8_gemm(PyObject *const *a)
                         c.stream(a[6]));
 }
 
+// q, k, v, cu_seqlens, out, workspace, dev_status, scale, lse, stream
+awq_status prompt_attention(PyObject *const *a)
+{
+    Call c;
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+    const int code = c.activation(q, "q", 3);
+    const at::ScalarType type = q.scalar_type();
+    const at::IntArrayRef shape = q.sizes();
+    if (k.dim() != 3) bad_value("k: expected 3 dimensions, got shape " + shape_text(k.sizes()));
+    const int64_t kv_shape[3] = {shape[0], k.size(1), shape[2]};
+    const awq_heads hq = c.heads(a[0], "q", type, shape), ho = c.heads(a[4], "out", type, shape);
+    const awq_heads hk = c.heads(a[1], "k", type, kv_shape), hv = c.heads(a[2], "v", type, kv_shape);
+    int32_t batch;
+    void *pc = c.bounds(a[3], &batch);
+    void *pl = c.dense(a[8], "lse", at::kFloat, {shape[0], shape[1]}, true);
+    const at::Tensor &ws = c.scratch(a[5]);
+    return awq_prompt_attention(&hq, &hk, &hv, static_cast<int32_t *>(pc), batch, size32(shape[0], "q"), size32(shape[1], "q"),
+                                size32(kv_shape[1], "k"), size32(shape[2], "q"), code, score_scale(a[7], shape[2]), &ho,
+                                static_cast<float *>(pl), ws.data_ptr(), ws.nbytes(), c.status(a[6]), c.stream(a[9]));
+}
+
+// q, k_cache, v_cache, page_table, cu_seqlens, seq_lens, out, workspace, dev_status, scale, lse, k_scale, v_scale, stream
+awq_status chunk_attention(PyObject *const *a)
+{
+    Call c;
+    const at::Tensor &q = tensor(a[0], "q");
+    const int code = c.activation(q, "q", 3);
+    const at::ScalarType type = q.scalar_type();
+    const at::IntArrayRef shape = q.sizes();
+    const awq_kv_cache cache = c.cache(a[1], a[2], number(a[11]), number(a[12]), type);
+    if (shape[2] != cache.head_dim)
+        bad_value("q: head size " + std::to_string(shape[2]) + ", the cache's is " + std::to_string(cache.head_dim));
+    const awq_heads hq = c.heads(a[0], "q", type, shape), ho = c.heads(a[6], "out", type, shape);
+    int32_t batch;
+    void *pc = c.bounds(a[4], &batch);
+    const at::Tensor &table = tensor(a[3], "page_table");
+    if (table.dim() != 2) bad_value("page_table: expected 2 dimensions, got shape " + shape_text(table.sizes()));
+    const int64_t pages = table.size(1);
+    int64_t ldt;
+    void *pt = c.rows(a[3], "page_table", at::kInt, {batch, pages}, &ldt);
+    void *pl = c.dense(a[5], "seq_lens", at::kInt, {batch});
+    void *ps = c.dense(a[10], "lse", at::kFloat, {shape[0], shape[1]}, true);
+    const at::Tensor &ws = c.scratch(a[7]);
+    return awq_chunk_attention(&hq, &cache, static_cast<int32_t *>(pt), ldt, size32(pages, "page_table"), static_cast<int32_t *>(pc),
+                               static_cast<int32_t *>(pl), batch, size32(shape[0], "q"), size32(shape[1], "q"), code,
+                               score_scale(a[9], shape[2]), &ho, static_cast<float *>(ps), ws.data_ptr(), ws.nbytes(),
+                               c.status(a[8]), c.stream(a[13]));
+}
+
+// q, k, v, q_weight, k_weight, eps, positions, cos_sin, slots, k_cache, v_cache, dev_status, q_out, interleaved, k_scale,
+// v_scale, stream
+awq_status qk_norm_rope_append(PyObject *const *a)
+{
+    Call c;
+    const at::Tensor &q = tensor(a[0], "q");
+    const int code = c.activation(q, "q", 3);
+    const at::ScalarType type = q.scalar_type();
+    const at::IntArrayRef shape = q.sizes();
+    const awq_kv_cache cache = c.cache(a[9], a[10], number(a[14]), number(a[15]), type);
+    if (shape[2] != cache.head_dim)
+        bad_value("q: head size " + std::to_string(shape[2]) + ", the cache's is " + std::to_string(cache.head_dim));
+    const awq_heads hq = c.heads(a[0], "q", type, shape), ho = a[12] == Py_None ? hq : c.heads(a[12], "q_out", type, shape);
+    const int64_t kv_shape[3] = {shape[0], cache.num_heads, shape[2]};
+    const awq_heads hk = c.heads(a[1], "k", type, kv_shape), hv = c.heads(a[2], "v", type, kv_shape);
+    void *pqw = c.dense(a[3], "q_weight", type, {shape[2]}), *pkw = c.dense(a[4], "k_weight", type, {shape[2]});
+    const at::Tensor &table = tensor(a[7], "cos_sin");
+    if (table.dim() != 2) bad_value("cos_sin: expected 2 dimensions, got shape " + shape_text(table.sizes()));
+    void *pt = c.dense(a[7], "cos_sin", at::kFloat, table.sizes());
+    void *pp = c.dense(a[6], "positions", at::kInt, {shape[0]}), *ps = c.dense(a[8], "slots", at::kLong, {shape[0]});
+    return awq_qk_norm_rope_append(&hq, &ho, &hk, &hv, pqw, pkw, static_cast<float>(number(a[5])), static_cast<int32_t *>(pp),
+                                   static_cast<float *>(pt), size32(table.size(0), "cos_sin"), size32(table.size(1), "cos_sin"),
+                                   truth(a[13]), static_cast<int64_t *>(ps), &cache, size32(shape[0], "q"),
+                                   size32(shape[1], "q"), code, c.status(a[11]), c.stream(a[16]));
+}
+
 // One entry of the module: N positional arguments in, the status out.
 template <awq_status (*F)(PyObject *const *), Py_ssize_t N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
@@ -329,7 +428,10 @@ constexpr PyMethodDef method(const char *name)
 
 PyMethodDef methods[] = {method<add_rmsnorm, 9>("add_rmsnorm"),       method<quantize_fp8, 4>("quantize_fp8"),
                          method<rope_append, 14>("rope_append"),      method<paged_attention, 13>("paged_attention"),
-                         method<fp8_gemm, 7>("fp8_gemm"),             {nullptr, nullptr, 0, nullptr}};
+                         method<fp8_gemm, 7>("fp8_gemm"),             method<prompt_attention, 10>("prompt_attention"),
+                         method<chunk_attention, 14>("chunk_attention"),
+                         method<qk_norm_rope_append, 17>("qk_norm_rope_append"),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

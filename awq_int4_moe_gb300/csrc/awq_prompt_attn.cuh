@@ -1,0 +1,1102 @@
+// awq_prompt_attention and awq_chunk_attention: causal attention of n new
+// tokens per sequence, over K and V packed like q or in the paged cache, on the
+// 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
+//
+// Rows. The G query heads of a KV head see the same keys, so a sequence's rows
+// are its (token, head of the group) pairs, token by token: row r is token r / G,
+// head r % G, and sees the keys before limit(r) = L - n + r / G + 1. A unit is
+// 256 consecutive rows of one sequence and KV head (128 where a head is larger
+// than 128): no row of a tile is padding but at a sequence's end, a key is
+// copied once for all heads that read it, and the diagonal cuts few tiles.
+//
+// One pass over the keys, 128 at a time (base-2 logarithms, all fp32):
+//   S = Q K'                                    tensor core, into tensor memory
+//   m' = max(m, S f), P = exp2(S f - m'), l = l 2^(m - m') + sum P      registers
+//   O = O 2^(m - m') + P V                      tensor core, P from tensor memory
+// m is raised only where a score passes it by more than 2^8, so that O is scaled
+// (a round trip through registers) for the first tiles of a row and then hardly
+// ever; P stays below 2^8 times the maximum's own weight.
+//
+// Steps. Two score tiles are in flight, one per softmax warpgroup ("slot"): while
+// one is turned into weights, the tensor core works for the other.
+//   wide (more than 128 rows): slot w has rows 128 w .. of every key tile;
+//   narrow (up to 128 rows, few new tokens over a long context): both have the
+//     same rows and every other key tile; their outputs are joined in tensor
+//     memory at the end;
+//   heads larger than 128: one warpgroup, its score tile double-buffered.
+// Tensor memory: S (and P over it, 16 bits) 2 x 128 columns, O 2 x 128 or 256.
+//
+// Warps: 0-7 softmax and output, a thread per row; 8-11 loader (Q, then K and V
+// tiles of 128 keys x 128 columns, 128-byte swizzle, five or ten in shared memory,
+// by cp.async, 16 bytes a thread, as keys of a page or of a packed batch need
+// no tensor map; e4m3 is expanded to fp16 in registers); 12 issues the MMAs. They
+// meet at mbarriers, every wait is bounded.
+//
+// Balance. Units are numbered sequence by sequence, head by head, tile by tile;
+// their costs (a unit's keys and a fixed part) have a closed form, and every
+// block takes an equal share of the sum, whatever units it belongs to. A unit
+// that is cut (in whole multiples of kPiece key tiles) leaves its parts in the
+// workspace; at the end the blocks that share it wait for the last one and each
+// join a part of its rows, in block order, so the same inputs give the same bits.
+#pragma once
+
+#include <type_traits>
+
+#include "awq_launch.cuh"
+#include "awq_prompt_kernels.cuh"
+#include "awq_tc.cuh"
+
+namespace awq {
+
+namespace {
+
+constexpr float kChunkLazy = 8.f;      // a score raises the maximum when it passes it by this (base 2)
+// fp16 weights are taken against 2^-7 of the maximum: they stay below 2^15 and
+// keep 31 bits below the maximum's own before they vanish.
+constexpr float kChunkRaiseF16 = 7.f;
+// Below every factor that turns a score into a base-2 logarithm: with a factor
+// of 0 a masked score of -infinity would be NaN.
+constexpr float kChunkMinFactor = 1.17549435e-38f;
+constexpr float kChunkLn2 = 0.6931471805599453f;
+constexpr int kPiece = 4;              // key tiles: cuts of a unit are multiples of it
+constexpr int kLoaderWarp = 8, kMmaWarp = 12, kChunkThreads = 512;
+constexpr int kAll256 = 1;             // named barrier of both softmax warpgroups
+
+template <int DP>
+struct ChunkGeo {
+    static constexpr int QT = DP <= 128 ? 2 : 1;            // row tiles of a unit
+    static constexpr int R = 128 * QT;
+    static constexpr int SC = DP < 128 ? DP : 128;          // columns of a stage
+    static constexpr int HV = DP / SC;                      // stages of a key tile
+    static constexpr int kStage = kChunkKeys * SC * 2;
+    static constexpr int kStages = 160 * 1024 / kStage;
+    static constexpr int kQTile = 128 * DP * 2;             // one row tile of Q
+    static constexpr int kQ = QT * kQTile;
+    // after Q and the stages: maxima and sums that two slots exchange, rows' powers of two, barriers
+    static constexpr int oStages = kQ, oMl = oStages + kStages * kStage, oExp = oMl + 2 * 128 * 8,
+                         oBars = oExp + 2 * 256, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 1, oMisc = oBars + kBars * 8,
+                         kSmem = oMisc + 64;
+    static constexpr uint32_t kTmemO = 256;                 // first column of O; S at 0 and 128
+    static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t pack_f2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 32 columns of the warp's 32 lanes; complete after tc_wait_ld32().
+#define AWQ_R32(r, i)                                                                                                            \
+    r[i], r[i + 1], r[i + 2], r[i + 3], r[i + 4], r[i + 5], r[i + 6], r[i + 7], r[i + 8], r[i + 9], r[i + 10], r[i + 11],          \
+        r[i + 12], r[i + 13], r[i + 14], r[i + 15], r[i + 16], r[i + 17], r[i + 18], r[i + 19], r[i + 20], r[i + 21], r[i + 22],   \
+        r[i + 23], r[i + 24], r[i + 25], r[i + 26], r[i + 27], r[i + 28], r[i + 29], r[i + 30], r[i + 31]
+__device__ __forceinline__ void tc_ld32_async(uint32_t taddr, float *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]),
+          "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]),
+          "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]),
+          "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr));
+}
+// Waits for the loads; the registers pass through so that no use of them is
+// moved above the wait.
+__device__ __forceinline__ void tc_wait_ld32(float *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
+                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]),
+                   "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]),
+                   "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31])
+        : "memory");
+}
+
+// Shared memory matrix descriptor of V as the B operand, MN-major: rows of 64
+// columns (128 bytes, 128-byte swizzle), 1024 bytes from 8 keys to the next 8,
+// 16 KB from 64 columns to the next 64.
+__device__ __forceinline__ uint64_t umma_desc_v(uint32_t addr)
+{
+    uint64_t d = static_cast<uint64_t>((addr & 0x3FFFF) >> 4);
+    d |= static_cast<uint64_t>((kChunkKeys * 128) >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= 1ull << 46;
+    d |= 2ull << 61;
+    return d;
+}
+// kind::f16, 128 rows, N columns, fp32 accumulator; bf16 operands; B MN-major.
+__device__ __forceinline__ uint32_t chunk_idesc(int N, bool bf16, bool b_mn)
+{
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (128u >> 4 << 24);
+}
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 16 bytes, or zeros where `bytes` is 0.
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Four e4m3 codes as two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t four, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+__device__ __forceinline__ int atomic_add_acq_rel(int32_t *p, int v)
+{
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
+// A pair of 16-bit values with those that are not finite made 0.
+template <typename C>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t v)
+{
+    constexpr uint32_t M = std::is_same<C, __half>::value ? 0x7C00u : 0x7F80u;
+    uint32_t r = v;
+    if ((v & M) == M) r &= 0xFFFF0000u;
+    if ((v & (M << 16)) == (M << 16)) r &= 0x0000FFFFu;
+    return r;
+}
+
+// ------------------------------------------------------------------ the units
+
+// What a block has of a unit: key tiles k0 .. k1 - 1.
+struct Unit {
+    int b, h;              // sequence, KV head
+    int q0, n, ctx;        // the sequence's first row of q, its new tokens, L - n
+    int row0, rows;        // packed rows
+    int keys, tiles;       // keys that its last row sees, and their tiles
+    int k0, k1;
+    int64_t at, cost;      // its place in the sum of costs
+    __device__ __forceinline__ bool cut() const { return k0 > 0 || k1 < tiles; }
+    __device__ __forceinline__ int limit(int row, int group) const      // keys that a row sees
+    {
+        const int v = ctx + static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(group)) + 1;
+        return v < 0 ? 0 : v;
+    }
+};
+
+// Key tiles of a unit before a cut at `y` of its cost.
+__device__ __forceinline__ int cut_at(int64_t y, int64_t cost, int tiles)
+{
+    if (y <= 0) return 0;
+    if (y >= cost) return tiles;
+    const int k = static_cast<int>(y * tiles / cost) / kPiece * kPiece;
+    return tiles - k < kPiece ? tiles : k;
+}
+
+struct Sequence {
+    int q0, n, len;
+};
+__device__ __forceinline__ Sequence sequence_at(const ChunkArgs &a, int b)
+{
+    const int c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1];
+    Sequence s;
+    s.q0 = min(max(c0, 0), a.tokens);
+    s.n = min(max(c1, s.q0), a.tokens) - s.q0;
+    s.len = a.seq_lens ? min(max(a.seq_lens[b], 0), a.max_len) : s.n;
+    return s;
+}
+__device__ __forceinline__ bool sequence_bad(const ChunkArgs &a, int b)
+{
+    const int c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1];
+    return c0 < 0 || c1 < c0 || c1 > a.tokens || (a.seq_lens && (a.seq_lens[b] < 0 || a.seq_lens[b] > a.max_len));
+}
+
+// Costs of a sequence's units for one KV head: unit i costs lin + R (i + 1), in
+// keys times G (so that all sequences count alike); a narrow one by itself half.
+template <int R>
+struct Costs {
+    int64_t lin, head;
+    int T;
+    bool half;
+    __device__ __forceinline__ Costs() {}
+    __device__ __forceinline__ Costs(const Sequence &s, int group)
+    {
+        const int64_t rows = static_cast<int64_t>(s.n) * group;
+        T = static_cast<int>((rows + R - 1) / R);
+        lin = group * (static_cast<int64_t>(max(s.len - s.n, 0)) + kChunkUnitCost);
+        half = R == 256 && rows <= 128;
+        head = before(T);
+    }
+    __device__ __forceinline__ int64_t before(int i) const
+    {
+        const int64_t c = i * lin + static_cast<int64_t>(R / 2) * i * (i + 1);
+        return half ? c / 2 : c;
+    }
+};
+
+template <int R>
+struct Cursor2 {
+    const ChunkArgs &a;
+    int64_t x0, x1, at;      // the block's share of the costs; where the unit begins
+    int b, h, t;
+    Sequence s;
+    Costs<R> c;
+
+    __device__ __forceinline__ Cursor2(const ChunkArgs &args, int64_t from, int64_t to, int first, int64_t first_at)
+        : a(args), x0(from), x1(to), at(first_at), b(first), h(0), t(0)
+    {
+        s.n = 0;
+        c.T = 0;
+        if (x0 >= x1) return;
+        s = sequence_at(a, b);
+        c = Costs<R>(s, a.group);
+        const int64_t in = x0 - at;
+        h = static_cast<int>(in / c.head);
+        at += h * c.head;
+        // the last unit that begins at or before x0
+        int lo = 0, hi = c.T - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (at + c.before(mid) <= x0) lo = mid;
+            else hi = mid - 1;
+        }
+        t = lo;
+        at += c.before(t);
+    }
+    // The block's next unit.
+    __device__ __forceinline__ bool next(Unit &u)
+    {
+        while (at < x1) {
+            while (t == c.T) {                          // (units remain, as costs do)
+                t = 0;
+                if (++h < a.cache.num_heads && c.T > 0) continue;
+                h = 0;
+                s = sequence_at(a, ++b);
+                c = Costs<R>(s, a.group);
+            }
+            u.b = b;
+            u.h = h;
+            u.q0 = s.q0;
+            u.n = s.n;
+            u.ctx = s.len - s.n;
+            u.row0 = t * R;
+            u.rows = min(R, s.n * a.group - u.row0);
+            u.keys = u.limit(u.row0 + u.rows - 1, a.group);
+            u.tiles = (u.keys + kChunkKeys - 1) / kChunkKeys;
+            u.at = at;
+            u.cost = c.before(t + 1) - c.before(t);
+            u.k0 = cut_at(x0 - at, u.cost, u.tiles);
+            u.k1 = cut_at(x1 - at, u.cost, u.tiles);
+            const bool mine = u.tiles ? u.k1 > u.k0 : x0 <= at;
+            at += u.cost;
+            ++t;
+            if (mine) return true;
+        }
+        return false;
+    }
+};
+
+// Which of the columns c .. c + 31 of V hold a value that is not finite at a key
+// that the row sees, among the tiles whose values were made finite on their way
+// to the tensor core. Reads them again: nothing of it runs on finite values.
+template <typename T, bool FP8>
+__device__ __forceinline__ uint32_t not_finite_seen(const ChunkArgs &a, const Unit &u, int limit, int c)
+{
+    const awq_kv_plane &pl = a.cache.v;
+    const int from = max(u.limit(u.row0, a.group) / kChunkKeys, u.k0) * kChunkKeys, to = min(limit, u.k1 * kChunkKeys);
+    uint32_t mask = 0;
+#pragma unroll 1
+    for (int key = from; key < to; ++key) {
+        int64_t off;
+        if (a.page_table) {
+            const int page = key / a.cache.page_size, id = a.page_table[u.b * a.table_stride + page];
+            if (id < 0 || id >= a.cache.num_pages) continue;
+            off = id * pl.page_stride + (key - page * a.cache.page_size) * pl.token_stride;
+        } else {
+            off = (static_cast<int64_t>(u.q0) + key) * pl.token_stride;
+        }
+        off += u.h * pl.head_stride;
+#pragma unroll 1
+        for (int i = 0; i < 32 && c + i < a.cache.head_dim; ++i) {
+            bool bad;
+            if constexpr (FP8) {
+                bad = (static_cast<const uint8_t *>(pl.data)[off + c + i] & 0x7F) == 0x7F;
+            } else {
+                const uint32_t v = static_cast<const uint16_t *>(pl.data)[off + c + i];
+                constexpr uint32_t M = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+                bad = (v & M) == M;
+            }
+            mask |= (bad ? 1u : 0u) << i;
+        }
+    }
+    return mask;
+}
+
+// The blocks that share a cut unit, for a whole warp: the first one, and where
+// `list` is given all of them, with this block's place and their number.
+__device__ __forceinline__ int sharing_blocks(const Unit &u, int64_t per, int lane, int16_t *list, int &me, int &count)
+{
+    const int c0 = static_cast<int>(u.at / per), c1 = static_cast<int>((u.at + u.cost - 1) / per);
+    int first = -1;
+    count = 0;
+    me = 0;
+    for (int base = c0; base <= c1; base += 32) {
+        const int c = base + lane;
+        const int ka = cut_at(c * per - u.at, u.cost, u.tiles), kb = cut_at((c + 1) * per - u.at, u.cost, u.tiles);
+        const bool in = c <= c1 && kb > ka;
+        const uint32_t all = __ballot_sync(~0u, in);
+        if (all == 0) continue;
+        if (first < 0) first = base + __ffs(all) - 1;
+        if (!list) break;
+        const int place = count + __popc(all & ((1u << lane) - 1));
+        if (in) list[place] = static_cast<int16_t>(c);
+        if (static_cast<int>(blockIdx.x) >= base && static_cast<int>(blockIdx.x) < base + 32)
+            me = count + __popc(all & ((1u << (blockIdx.x - base)) - 1));
+        count += __popc(all);
+    }
+    return first;
+}
+
+// ----------------------------------------------------------------- the kernel
+
+template <typename T, bool FP8, int DP>
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkArgs a)
+{
+    using G = ChunkGeo<DP>;
+    using C = typename std::conditional<FP8, __half, T>::type;      // the tensor core's type
+    constexpr bool kBf16 = std::is_same<C, __nv_bfloat16>::value;
+    constexpr bool kScaledQ = FP8 && !std::is_same<T, C>::value;    // bf16 q as fp16 with a power of two taken out
+    constexpr float kRaise = kBf16 ? 0.f : kChunkRaiseF16;
+    constexpr int NST = G::kStages, HV = G::HV, SC = G::SC, QT = G::QT, R = G::R;
+
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *const stages = smem + G::oStages;
+    float2 *const s_ml = reinterpret_cast<float2 *>(smem + G::oMl);          // [2][128]
+    uint8_t *const s_exp = smem + G::oExp;                                   // [2][256]
+    uint64_t *const full = reinterpret_cast<uint64_t *>(smem + G::oBars);
+    uint64_t *const empty = full + NST;
+    uint64_t *const q_full = empty + NST, *const q_empty = q_full + 1;
+    uint64_t *const s_full = q_empty + 1;        // [2]
+    uint64_t *const p_full = s_full + 2;         // [2]
+    uint64_t *const o_done = p_full + 2;         // [2]
+    uint64_t *const drain = o_done + 2;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + G::oMisc);
+    int *const s_bad = reinterpret_cast<int *>(smem + G::oMisc + 16);        // [4]
+    int *const s_first = s_bad + 4;
+    int64_t *const s_first_at = reinterpret_cast<int64_t *>(smem + G::oMisc + 40);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int D = a.cache.head_dim;
+    if (smem_u32(smem) & 1023) {                 // (the tiles' swizzle needs it)
+        if (tid == 0) set_status(a.status, AWQ_ERR_CUDA);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 128);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(q_full, 128);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_done[i], 1);
+        }
+        mbar_init(drain, 1);
+        for (int i = 0; i < 4; ++i) s_bad[i] = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) tc_alloc(tmem_slot, 512);
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- the sum of all costs, and the first unit of the block's share
+    int64_t x0, x1, per_cta;
+    {
+        int64_t *const scan = reinterpret_cast<int64_t *>(stages);           // [16], before any tile
+        const int per = (a.batch + kChunkThreads - 1) / kChunkThreads;
+        const int lo = min(a.batch, tid * per), hi = min(a.batch, lo + per);
+        int64_t mine = 0;
+        for (int b = lo; b < hi; ++b) {
+            if (blockIdx.x == 0 && sequence_bad(a, b)) set_status(a.status, AWQ_ERR_BAD_INDEX);
+            mine += Costs<R>(sequence_at(a, b), a.group).head * a.cache.num_heads;
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) scan[warp] = incl;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        int64_t before = incl - mine, total = 0;
+        for (int w = 0; w < kChunkThreads / 32; ++w) {
+            const int64_t v = scan[w];
+            if (w < warp) before += v;
+            total += v;
+        }
+        per_cta = (total + gridDim.x - 1) / gridDim.x;
+        x0 = min(total, per_cta * blockIdx.x);
+        x1 = min(total, x0 + per_cta);
+        if (x0 < x1 && x0 >= before && x0 < before + mine) {
+            int b = lo;
+            for (;; ++b) {
+                const int64_t c = Costs<R>(sequence_at(a, b), a.group).head * a.cache.num_heads;
+                if (x0 < before + c) break;
+                before += c;
+            }
+            *s_first = b;
+            *s_first_at = before;
+        }
+        __syncthreads();
+    }
+    const uint32_t tmem = *tmem_slot;
+    Cursor2<R> cursor(a, x0, x1, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0);
+    Unit u;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok && !mbar_wait_bounded(bar, parity, a.timeout_ns)) {
+            set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+            ok = false;
+        }
+    };
+    // Stages of a unit in the order that they are used up: K 0 .. ahead - 1, then
+    // V j, K j + ahead ... where `ahead` is 1 if both slots use a tile, else 2.
+    auto ahead_of = [&](const Unit &v) { return QT == 2 && v.rows > 128 ? 1 : min(2, v.k1 - v.k0); };
+    auto k_item = [](int j, int ahead) { return j + max(0, j - ahead + 1); };
+    auto v_item = [](int j, int ahead, int n) { return ahead + j + min(j, n - ahead); };
+
+    if (warp >= kLoaderWarp && warp < kMmaWarp) {
+        // ------------------------------------------------------- loader
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP8 ? 96 : 80));
+        const int lw = warp - kLoaderWarp;
+        uint32_t pos = 0;                                    // stages filled so far
+        int ordinal = 0;
+        while (cursor.next(u)) {
+            ++ordinal;
+            const int G_ = a.group;
+            // ---- Q: 128 rows a tile, lane i finds the row of its turn i / RP
+            {
+                constexpr int CH = DP / 8, RP = 32 / CH;
+                const int ch = lane % CH, sub = lane / CH;
+                const bool col = ch * 8 < D, pad = ch * 8 < (D + 15) / 16 * 16;
+                if (ordinal > 1) wait(q_empty, (ordinal - 2) & 1);
+                const T *const q = static_cast<const T *>(a.q.data);
+#pragma unroll 1
+                for (int w = 0; w < QT; ++w) {
+                    if (w * 128 >= u.rows) break;
+                    const int mine = w * 128 + (lane / RP) * 4 * RP + lw * RP + lane % RP;
+                    int64_t off = -1;
+                    if (mine < u.rows) {
+                        const uint32_t row = u.row0 + mine, tok = row / static_cast<uint32_t>(G_), g = row - tok * G_;
+                        off = (static_cast<int64_t>(u.q0) + tok) * a.q.token_stride + (static_cast<int64_t>(u.h) * G_ + g) * a.q.head_stride;
+                    }
+                    const uint32_t dst0 = smem_u32(smem) + w * G::kQTile + (ch >> 3) * (128 * 128);
+#pragma unroll 4
+                    for (int p = 0; p < 32 / RP; ++p) {
+                        const int64_t o = __shfl_sync(~0u, off, p * RP + sub);
+                        const int row = p * 4 * RP + lw * RP + sub;
+                        const uint32_t dst = dst0 + sw128_offset(row, ch & 7);
+                        if constexpr (kScaledQ) {
+                            // the row's largest magnitude to [2^14, 2^15)
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (o >= 0 && col) v = *reinterpret_cast<const uint4 *>(q + o + ch * 8);
+                            float f[8];
+                            const uint32_t raw[4] = {v.x, v.y, v.z, v.w};
+                            float top = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 x = unpack2<T>(raw[i]);
+                                f[2 * i] = x.x;
+                                f[2 * i + 1] = x.y;
+                                top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+                            }
+#pragma unroll
+                            for (int m = CH / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
+                            const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112);
+                            const float by = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+                            if (pad)
+                                sts_v4(dst, make_uint4(pack2<__half>(f[0] * by, f[1] * by), pack2<__half>(f[2] * by, f[3] * by),
+                                                       pack2<__half>(f[4] * by, f[5] * by), pack2<__half>(f[6] * by, f[7] * by)));
+                            if (ch == 0) s_exp[(ordinal & 1) * 256 + w * 128 + row] = static_cast<uint8_t>(e + 112);
+                        } else {
+                            if (pad) cp_async_16_or_zero(dst, o >= 0 && col ? q + o + ch * 8 : q, o >= 0 && col ? 16 : 0);
+                        }
+                    }
+                }
+                if constexpr (kScaledQ) {
+                    fence_proxy_async();
+                    mbar_arrive(q_full);
+                } else {
+                    cp_async_arrive_noinc(q_full);
+                }
+            }
+            // ---- K and V tiles
+            const int n = u.k1 - u.k0, ahead = n ? ahead_of(u) : 0;
+            const int seen_by_all = u.limit(u.row0, G_);                    // keys that every row sees
+            for (int item = 0; item < 2 * n; ++item) {
+                // the item's plane and tile (the inverse of k_item and v_item)
+                int j;
+                bool is_v;
+                if (item < ahead) {
+                    j = item;
+                    is_v = false;
+                } else if (item < ahead + 2 * (n - ahead)) {
+                    j = (item - ahead) >> 1;
+                    is_v = !((item - ahead) & 1);
+                    if (!is_v) j += ahead;
+                } else {
+                    j = item - n;
+                    is_v = true;
+                }
+                const int key0 = (u.k0 + j) * kChunkKeys;
+                const awq_kv_plane &pl = is_v ? a.cache.v : a.cache.k;
+                // lane i: where the row of its turn is
+                constexpr int kElem = FP8 ? 1 : 2;
+                constexpr int CH = SC * kElem / 16, RP = 32 / CH, TURNS = 32 / RP;
+                const int ch = lane % CH, sub = lane / CH;
+                int64_t off = -1;
+                {
+                    const int key = key0 + (lane / RP) * 4 * RP + lw * RP + lane % RP;
+                    if (key < u.keys) {
+                        if (a.page_table) {
+                            const uint32_t page = a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
+                            const int id = a.page_table[u.b * a.table_stride + page];
+                            if (id >= 0 && id < a.cache.num_pages)
+                                off = id * pl.page_stride + (key - static_cast<int>(page) * a.cache.page_size) * pl.token_stride;
+                            else
+                                set_status(a.status, AWQ_ERR_BAD_INDEX);
+                        } else {
+                            off = (static_cast<int64_t>(u.q0) + key) * pl.token_stride;
+                        }
+                        if (off >= 0) off += u.h * pl.head_stride;
+                    }
+                }
+                // a V tile that some row of the unit does not see in full: values
+                // that are not finite would reach it as 0 times themselves
+                const bool guard = is_v && key0 + kChunkKeys > seen_by_all;
+                for (int hh = 0; hh < HV; ++hh, ++pos) {
+                    const uint32_t st = pos % NST;
+                    const uint32_t base = smem_u32(stages) + st * G::kStage;
+                    const int d0 = hh * SC + ch * (16 / kElem);
+                    const bool col = d0 < D;
+                    bool bad = false;
+                    if constexpr (FP8) {
+                        const uint8_t *const src = static_cast<const uint8_t *>(pl.data);
+                        uint4 raw[TURNS];
+#pragma unroll
+                        for (int p = 0; p < TURNS; ++p) {
+                            const int64_t o = __shfl_sync(~0u, off, p * RP + sub);
+                            raw[p] = o >= 0 && col ? ld_v4(src + o + d0) : make_uint4(0, 0, 0, 0);
+                        }
+                        if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
+                        if (col) {
+#pragma unroll
+                            for (int p = 0; p < TURNS; ++p) {
+                                const int row = p * 4 * RP + lw * RP + sub;
+                                const uint32_t dst = base + (ch >> 2) * (kChunkKeys * 128);
+                                uint32_t w[8];
+                                e4m3x4_f16x4(raw[p].x, w[0], w[1]);
+                                e4m3x4_f16x4(raw[p].y, w[2], w[3]);
+                                e4m3x4_f16x4(raw[p].z, w[4], w[5]);
+                                e4m3x4_f16x4(raw[p].w, w[6], w[7]);
+                                if (guard) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const uint32_t f = finite_pair<C>(w[i]);
+                                        bad |= f != w[i];
+                                        w[i] = f;
+                                    }
+                                }
+                                sts_v4(dst + sw128_offset(row, (ch & 3) * 2), make_uint4(w[0], w[1], w[2], w[3]));
+                                sts_v4(dst + sw128_offset(row, (ch & 3) * 2 + 1), make_uint4(w[4], w[5], w[6], w[7]));
+                            }
+                        }
+                        if (bad) s_bad[ordinal & 3] = ordinal;
+                        fence_proxy_async();
+                        mbar_arrive(&full[st]);
+                    } else {
+                        const T *const src = static_cast<const T *>(pl.data);
+                        const bool pad = d0 < (D + 15) / 16 * 16;
+                        const uint32_t dst0 = base + (ch >> 3) * (kChunkKeys * 128) + sw128_offset(lw * RP + sub, ch & 7);
+                        constexpr int kStep = 4 * RP / 8 * 1024;                 // bytes from turn to turn
+                        if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
+#pragma unroll
+                        for (int p = 0; p < TURNS; ++p) {
+                            const int64_t o = __shfl_sync(~0u, off, p * RP + sub);
+                            if (pad) cp_async_16_or_zero(dst0 + p * kStep, o >= 0 && col ? src + o + d0 : src, o >= 0 && col ? 16 : 0);
+                        }
+                        if (guard) {
+                            cp_async_commit();
+                            cp_async_wait_group<0>();
+                            if (pad) {
+#pragma unroll 4
+                                for (int p = 0; p < TURNS; ++p) {
+                                    const uint4 v = lds_v4(dst0 + p * kStep);
+                                    const uint4 f = make_uint4(finite_pair<C>(v.x), finite_pair<C>(v.y), finite_pair<C>(v.z),
+                                                               finite_pair<C>(v.w));
+                                    if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
+                                        bad = true;
+                                        sts_v4(dst0 + p * kStep, f);
+                                    }
+                                }
+                            }
+                            if (bad) s_bad[ordinal & 3] = ordinal;
+                            fence_proxy_async();
+                            mbar_arrive(&full[st]);
+                        } else {
+                            cp_async_arrive_noinc(&full[st]);
+                        }
+                    }
+                }
+            }
+        }
+        cp_async_commit();
+        cp_async_wait_group<0>();
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------------- MMA issuer
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == kMmaWarp && lane == 0) {
+            const int k_steps = (D + 15) / 16;               // of Q K'; times 16: columns of P V
+            const uint32_t q_base = smem_u32(smem), st_base = smem_u32(stages);
+            uint32_t pos = 0;
+            uint32_t p_phase = 0;                            // bit per slot
+            int ordinal = 0;
+            while (cursor.next(u)) {
+                ++ordinal;
+                const int n = u.k1 - u.k0;
+                const bool wide = QT == 2 && u.rows > 128;
+                const int ahead = n ? ahead_of(u) : 0;
+                const int steps = wide ? 2 * n : n;
+                // the first slot's rows see fewer keys
+                const int n0 = wide ? min(n, max(0, (u.limit(u.row0 + 127, a.group) + kChunkKeys - 1) / kChunkKeys - u.k0)) : n;
+                wait(q_full, (ordinal - 1) & 1);
+                fence_proxy_async();
+                tc_fence_after();
+                uint32_t begun = 0;                          // accumulators that hold something
+                for (int s = 0; s < steps + 2; ++s) {
+                    if (s >= 2) {                            // P V of step s - 2
+                        const int slot = s & 1, j = wide ? (s - 2) >> 1 : s - 2;
+                        if (!(wide && slot == 0 && j >= n0)) {
+                            wait(&p_full[slot], p_phase >> slot & 1);
+                            p_phase ^= 1u << slot;
+                            const int at = v_item(j, ahead, n) * HV;
+                            const int acc = QT == 2 ? slot : 0;
+                            for (int hh = 0; hh < HV; ++hh) {
+                                const uint32_t item = pos + at + hh, st = item % NST;
+                                wait(&full[st], (item / NST) & 1);
+                                fence_proxy_async();
+                                tc_fence_after();
+                                const int cols = min(SC, k_steps * 16 - hh * SC);
+                                if (ok && cols > 0) {
+                                    const uint64_t db = umma_desc_v(st_base + st * G::kStage);
+                                    const uint32_t id = chunk_idesc(cols, kBf16, true);
+                                    const uint32_t d = tmem + G::kTmemO + acc * 128 + hh * 128;
+#pragma unroll
+                                    for (int k = 0; k < kChunkKeys / 16; ++k)
+                                        tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id,
+                                                          k > 0 || (begun >> acc & 1));
+                                }
+                                if (!wide || slot == 1) tc_commit(&empty[st]);
+                            }
+                            begun |= 1u << acc;
+                            tc_commit(&o_done[slot]);
+                        }
+                    }
+                    if (s < steps) {                         // Q K' of step s
+                        const int slot = s & 1, j = wide ? s >> 1 : s;
+                        if (!(wide && slot == 0 && j >= n0)) {
+                            const int at = k_item(j, ahead) * HV;
+                            const uint32_t id = chunk_idesc(kChunkKeys, kBf16, false);
+                            for (int hh = 0; hh < HV; ++hh) {
+                                const uint32_t item = pos + at + hh, st = item % NST;
+                                wait(&full[st], (item / NST) & 1);
+                                fence_proxy_async();
+                                tc_fence_after();
+                                const int ks = min(SC / 16, k_steps - hh * (SC / 16));
+                                if (ok) {
+                                    for (int k = 0; k < ks; ++k) {
+                                        const uint32_t in = (k >> 2) * (128 * 128) + (k & 3) * 32;
+                                        const uint64_t da = umma_desc_sw128(q_base + (wide ? slot : 0) * G::kQTile +
+                                                                            hh * (SC / 64) * (128 * 128) + in);
+                                        const uint64_t db = umma_desc_sw128(st_base + st * G::kStage + in);
+                                        tc_mma_f16(tmem + slot * 128, da, db, id, k > 0 || hh > 0);
+                                    }
+                                }
+                                if (!wide || slot == 1) tc_commit(&empty[st]);
+                            }
+                            tc_commit(&s_full[slot]);
+                        }
+                        if (s == steps - 1) tc_commit(q_empty);
+                    }
+                }
+                if (steps == 0) tc_commit(q_empty);
+                pos += 2 * n * HV;
+            }
+            // every MMA has completed before the block gives up its tensor memory
+            tc_commit(drain);
+            if (!mbar_wait_bounded(drain, 0, a.timeout_ns)) set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+        }
+    } else {
+        // ------------------------------------------------------- softmax and output
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP8 ? 184 : 192));
+        const int w = warp >> 2, row = (warp & 3) * 32 + lane;               // this thread's row of a tile
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        uint32_t s_phase = 0, o_phase = 0;                                   // a bit per slot: score tiles, products with V
+        int last = 0;                                                        // slot of the latest product
+        Unit shared_unit[2];                                                 // cut at its begin, at its end
+        uint32_t has_shared = 0;
+        int ordinal = 0;
+        float *const my_parts = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * chunk_piece_floats(DP);
+        while (cursor.next(u)) {
+            ++ordinal;
+            const int n = u.k1 - u.k0, G_ = a.group;
+            const bool wide = QT == 2 && u.rows > 128;
+            const int in_unit = wide ? w * 128 + row : row;                  // this thread's row of the unit
+            const bool valid = in_unit < u.rows;
+            const int my_row = u.row0 + (valid ? in_unit : u.rows - 1);
+            const int limit = u.limit(my_row, G_);
+            // its slot's key tiles: first, step, end
+            const int n0 = wide && w == 0 ? min(n, max(0, (u.limit(u.row0 + 127, G_) + kChunkKeys - 1) / kChunkKeys - u.k0)) : n;
+            const int j0 = QT == 2 && !wide ? w : 0, step = QT == 2 && !wide ? 2 : 1;
+            const bool idle = QT == 1 && w == 1;
+            const int all_see = u.limit(u.row0 + (wide ? w * 128 : 0), G_);  // keys that every row of the tile sees
+            float m = -INFINITY, l = 0.f, factor = 0.f;
+            bool first = true;
+            for (int j = idle ? n0 : j0; j < n0; j += step) {
+                const int slot = QT == 2 ? w : j & 1, acc = QT == 2 ? w : 0;
+                wait(&s_full[slot], s_phase >> slot & 1);
+                s_phase ^= 1u << slot;
+                ok = __all_sync(~0u, ok);
+                tc_fence_after();
+                const uint32_t s_addr = lanes + slot * 128;
+                if (first) {
+                    factor = a.factor;
+                    if constexpr (kScaledQ) factor *= __uint_as_float(static_cast<uint32_t>(
+                        max(1, s_exp[(ordinal & 1) * 256 + (wide ? w * 128 : 0) + row] - 112 - 14 + 127)) << 23);
+                    factor = fmaxf(factor, kChunkMinFactor);
+                }
+                float s[128];
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) tc_ld32_async(s_addr + c, s + c);
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) tc_wait_ld32(s + c);
+                }
+                if (a.negative) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = -s[c];
+                }
+                const int key0 = (u.k0 + j) * kChunkKeys;
+                if (key0 + kChunkKeys > all_see) {
+                    const int seen = limit - key0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c >= seen) s[c] = -INFINITY;
+                }
+                float top[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[i] = fmaxf(s[i], s[i + 4]);
+#pragma unroll
+                for (int c = 8; c < 128; c += 8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top[i] = max3(top[i], s[c + i], s[c + i + 4]);
+                const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+                // (row by row, so that a row's bits do not depend on its neighbours)
+                const bool raise = t > m + kChunkLazy || (m == -INFINITY && t > -INFINITY);
+                if (__any_sync(~0u, raise)) {
+                    const float by = raise ? ex2(m - t) : 1.f;
+                    m = raise ? t : m;
+                    l *= by;
+                    if (!first) {
+                        // O so far: behind the product of the step before
+                        wait(&o_done[last], (o_phase >> last & 1) ^ 1);
+                        ok = __all_sync(~0u, ok);
+                        tc_fence_after();
+                        if (ok) {
+                            for (int c = 0; c < (D + 31) / 32 * 32; c += 32) {
+                                float o[32];
+                                tc_ld32_async(lanes + G::kTmemO + acc * 128 + c, o);
+                                tc_wait_ld32(o);
+                                uint32_t r[32];
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * by);
+                                tc_st32(lanes + G::kTmemO + acc * 128 + c, r);
+                            }
+                        }
+                    }
+                }
+                first = false;
+                const float shift = m == -INFINITY ? 0.f : kRaise - m;
+                const uint64_t f2 = pack_f2(factor, factor), c2 = pack_f2(shift, shift);
+                uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x, y;
+                        unpack_f2(fma_f2(pack_f2(s[c + 2 * i], s[c + 2 * i + 1]), f2, c2), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        p[i] = pack2<C>(x, y);
+                        sum[i & 3] = add_f2(sum[i & 3], pack_f2(x, y));
+                    }
+                    if (ok) tc_st16(s_addr + c / 2, p);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[slot]);
+                o_phase ^= 1u << slot;
+                last = slot;
+                float x, y;
+                unpack_f2(add_f2(add_f2(sum[0], sum[1]), add_f2(sum[2], sum[3])), x, y);
+                l += x + y;
+            }
+            // ---- the unit's output, or this block's piece of it
+            const int acc = QT == 2 ? w : 0;
+            if (!first) {
+                wait(&o_done[last], (o_phase >> last & 1) ^ 1);
+                ok = __all_sync(~0u, ok);
+            }
+            tc_fence_after();
+            const bool merge = QT == 2 && !wide;
+            float w0 = 1.f, w1 = 0.f;                                        // weights of the two accumulators
+            if (merge) {
+                s_ml[w * 128 + row] = make_float2(m, l);
+                tc_fence_before();
+                named_barrier_sync(kAll256, 256);
+                tc_fence_after();
+                const float2 x = s_ml[row], y = s_ml[128 + row];
+                m = fmaxf(x.x, y.x);
+                const float ref = m == -INFINITY ? 0.f : m;
+                w0 = ex2(x.x - ref);
+                w1 = ex2(y.x - ref);
+                l = x.y * w0 + y.y * w1;
+            }
+            if (u.cut()) {
+                const int which = u.k0 > 0 ? 0 : 1;
+                shared_unit[which] = u;
+                has_shared |= 1u << which;
+            }
+            if (!idle && ok) {
+                const bool some = merge ? n > 0 : !first;                    // an accumulator holds something
+                float4 *const piece = reinterpret_cast<float4 *>(my_parts + (u.k0 > 0 ? 0 : 1) * chunk_piece_floats(DP) +
+                                                                 (wide ? w : 0) * static_cast<int64_t>(chunk_piece_floats(DP) / QT));
+                const float inv = l == 0.f ? 0.f : a.cache.v.scale / l;
+                const uint32_t tok = static_cast<uint32_t>(my_row) / static_cast<uint32_t>(G_), g = my_row - tok * G_;
+                const int64_t out_row = static_cast<int64_t>(u.q0) + tok, head = static_cast<int64_t>(u.h) * G_ + g;
+                T *const out = static_cast<T *>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride;
+                const bool guard = s_bad[ordinal & 3] == ordinal;            // values of V that are not finite were left out
+                // merged: each warpgroup takes half of the columns
+                const int c0 = merge ? w * (DP / 2) : 0, c1 = merge ? c0 + DP / 2 : DP;
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 32) {
+                    if (c >= D) break;
+                    float o[32];
+                    if (some) {
+                        tc_ld32_async(lanes + G::kTmemO + (merge ? 0 : acc * 128) + c, o);
+                        tc_wait_ld32(o);
+                        if (merge && n > 1) {
+                            float o1[32];
+                            tc_ld32_async(lanes + G::kTmemO + 128 + c, o1);
+                            tc_wait_ld32(o1);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                    }
+                    if (guard) {
+                        const uint32_t mask = valid ? not_finite_seen<T, FP8>(a, u, limit, c) : 0;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (mask >> i & 1) o[i] = __int_as_float(0x7FC00000);
+                        __syncwarp();
+                    }
+                    if (u.cut()) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            piece[((c + i) >> 2) * 128 + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    } else if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            if (c + i < D) {
+                                const float f[8] = {o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv,
+                                                    o[i + 4] * inv, o[i + 5] * inv, o[i + 6] * inv, o[i + 7] * inv};
+                                store_elems<T, 8>(out + c + i, f);
+                            }
+                    }
+                }
+                if (!merge || w == 0) {
+                    if (u.cut()) {
+                        float *const ml = reinterpret_cast<float *>(piece) + 128 * DP;
+                        ml[row] = m == -INFINITY ? m : m - kRaise;
+                        ml[128 + row] = l;
+                    } else if (valid && a.lse) {
+                        a.lse[out_row * a.q_heads + head] = l == 0.f ? -INFINITY : (m - kRaise + log2f(l)) * kChunkLn2;
+                    }
+                }
+            }
+            if (merge) {
+                tc_fence_before();
+                named_barrier_sync(kAll256, 256);
+                tc_fence_after();
+            }
+            if (u.cut()) {
+                __threadfence();
+                named_barrier_sync(kAll256, 256);
+                if (warp == 0) {
+                    int me, count;
+                    const int begun = sharing_blocks(u, per_cta, lane, nullptr, me, count);
+                    if (lane == 0) atomic_add_acq_rel(a.counters + 2 * begun, 1);
+                }
+            }
+        }
+        // ---- the cut units: each of the blocks that share one joins a part of it
+        for (int which = 0; which < 2; ++which) {
+            if (!(has_shared >> which & 1)) continue;
+            const Unit v = shared_unit[which];
+            int16_t *const list = reinterpret_cast<int16_t *>(s_ml);         // [kChunkMaxCtas], then place, number, first
+            named_barrier_sync(kAll256, 256);
+            if (warp == 0) {
+                int me, count;
+                const int begun = sharing_blocks(v, per_cta, lane, list, me, count);
+                if (lane == 0) {
+                    list[kChunkMaxCtas] = static_cast<int16_t>(me);
+                    list[kChunkMaxCtas + 1] = static_cast<int16_t>(count);
+                    list[kChunkMaxCtas + 2] = static_cast<int16_t>(begun);
+                    const uint64_t t0 = global_timer_ns();
+                    while (ok && ld_acquire_gpu(a.counters + 2 * begun) < count)
+                        if (global_timer_ns() - t0 > a.timeout_ns) {
+                            set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+                            ok = false;
+                        }
+                }
+                ok = __all_sync(~0u, ok);
+            }
+            ok = named_barrier_and(kAll256, 256, ok);
+            if (!ok) continue;
+            const int me = list[kChunkMaxCtas], count = list[kChunkMaxCtas + 1], begun = list[kChunkMaxCtas + 2];
+            const int rows = v.rows, items = rows * (D / 8);
+            const int lo = static_cast<int>(static_cast<int64_t>(items) * me / count);
+            const int hi = static_cast<int>(static_cast<int64_t>(items) * (me + 1) / count);
+            for (int item = lo + tid; item < hi; item += 256) {
+                const int chunk = item / rows, r = item - chunk * rows;
+                auto part = [&](int i) {                                     // of the i-th block: r's tile
+                    const int c = list[i];
+                    return a.parts + (static_cast<int64_t>(c) * 2 + (i == 0 ? 1 : 0)) * chunk_piece_floats(DP) +
+                           (r >> 7) * static_cast<int64_t>(chunk_piece_floats(DP) / QT);
+                };
+                float top = -INFINITY;
+                for (int i = 0; i < count; ++i) top = fmaxf(top, __ldcg(part(i) + 128 * DP + (r & 127)));
+                const float ref = top == -INFINITY ? 0.f : top;
+                float sum = 0.f, f[8] = {};
+#pragma unroll 2
+                for (int i = 0; i < count; ++i) {
+                    const float *const p = part(i);
+                    const float by = ex2(__ldcg(p + 128 * DP + (r & 127)) - ref);
+                    sum += __ldcg(p + 128 * DP + 128 + (r & 127)) * by;
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p) + 2 * chunk * 128 + (r & 127));
+                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(p) + (2 * chunk + 1) * 128 + (r & 127));
+                    f[0] += x.x * by;
+                    f[1] += x.y * by;
+                    f[2] += x.z * by;
+                    f[3] += x.w * by;
+                    f[4] += y.x * by;
+                    f[5] += y.y * by;
+                    f[6] += y.z * by;
+                    f[7] += y.w * by;
+                }
+                const float inv = sum == 0.f ? 0.f : a.cache.v.scale / sum;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] *= inv;
+                const uint32_t at = v.row0 + r, tok = at / static_cast<uint32_t>(a.group), g = at - tok * a.group;
+                const int64_t out_row = static_cast<int64_t>(v.q0) + tok, head = static_cast<int64_t>(v.h) * a.group + g;
+                store_elems<T, 8>(static_cast<T *>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride + 8 * chunk, f);
+                if (chunk == 0 && a.lse)
+                    a.lse[out_row * a.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kChunkLn2;
+            }
+            // the last block to leave makes the counters ready for the next call
+            named_barrier_sync(kAll256, 256);
+            if (tid == 0 && atomic_add_acq_rel(a.counters + 2 * begun + 1, 1) == count - 1) {
+                a.counters[2 * begun] = 0;
+                a.counters[2 * begun + 1] = 0;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tc_dealloc(tmem, 512);
+}
+
+template <typename T, bool FP8, int DP>
+awq_status launch_chunk_d(const ChunkArgs &a, int sms, cudaStream_t st)
+{
+    const awq_status r = set_smem(chunk_attn_kernel<T, FP8, DP>, ChunkGeo<DP>::kSmem);
+    if (r) return r;
+    const int grid = sms < kChunkMaxCtas ? sms : kChunkMaxCtas;
+    return launch_ex(chunk_attn_kernel<T, FP8, DP>, dim3(grid), dim3(kChunkThreads), ChunkGeo<DP>::kSmem, 1, true, st, a);
+}
+
+template <typename T, bool FP8>
+awq_status launch_chunk(const ChunkArgs &a, int sms, cudaStream_t st)
+{
+    const int dp = attn_padded_dim(a.cache.head_dim);
+    return dp == 64    ? launch_chunk_d<T, FP8, 64>(a, sms, st)
+           : dp == 128 ? launch_chunk_d<T, FP8, 128>(a, sms, st)
+                       : launch_chunk_d<T, FP8, 256>(a, sms, st);
+}
+
+}  // namespace
+
+}  // namespace awq

@@ -1,0 +1,8 @@
+// bf16 queries over a 16-bit cache, or packed K and V.
+#include "awq_prompt_attn.cuh"
+
+namespace awq {
+
+awq_status launch_chunk_bf16(const ChunkArgs &a, int sms, cudaStream_t st) { return launch_chunk<__nv_bfloat16, false>(a, sms, st); }
+
+}  // namespace awq

@@ -1,0 +1,62 @@
+// Kernel-side declarations of the prompt's operators (awq_prompt.h): argument
+// blocks, launchers and the sizes that the host and the kernels share.
+#pragma once
+
+#include "../../include/awq_prompt.h"
+#include "awq_decoder_kernels.cuh"
+
+namespace awq {
+
+// Attention of several new tokens per sequence; K and V packed like q
+// (page_table NULL) or in the paged cache.
+struct ChunkArgs {
+    awq_heads q, out;
+    awq_kv_cache cache;            // packed: its planes' token and head strides alone, and the head size
+    const int32_t *page_table;     // NULL: packed
+    const int32_t *cu_seqlens;     // [batch + 1]
+    const int32_t *seq_lens;       // [batch]; NULL: as many as are new
+    float *lse;
+    int32_t *counters;             // [2 * kChunkMaxCtas], zero between calls
+    float *parts;                  // pieces of cut units, see awq_prompt_attn.cuh
+    int32_t *status;
+    int64_t table_stride;
+    int32_t max_len, batch, tokens, q_heads, group;
+    uint32_t page_magic;           // as in AttnArgs
+    int32_t page_shift;
+    float factor;                  // |scale| * log2(e) * K's scale
+    int32_t negative;              // the scale is below 0
+    uint64_t timeout_ns;
+};
+
+struct HeadNormArgs {
+    RopeArgs rope;
+    const void *q_weight, *k_weight;
+    float eps;
+};
+
+// The grid never exceeds this many blocks (the workspace holds two counters and
+// two pieces for each).
+constexpr int kChunkMaxCtas = 160;
+constexpr size_t kChunkCounterBytes = (2 * kChunkMaxCtas * sizeof(int32_t) + 255) / 256 * 256;
+constexpr int kChunkKeys = 128;                                       // tokens of a K or V tile
+// Packed rows (a token's query heads of one KV head, token by token) of a unit:
+// two tiles of 128, one where a head is larger than 128.
+constexpr int chunk_rows(int padded_dim) { return padded_dim <= 128 ? 256 : 128; }
+constexpr int64_t kChunkUnitCost = 256;                               // a unit's fixed time, in tokens of its keys
+// Floats of a piece: output, maximum, sum of every row.
+constexpr size_t chunk_piece_floats(int padded_dim) { return static_cast<size_t>(chunk_rows(padded_dim)) * (padded_dim + 2); }
+constexpr size_t chunk_workspace_bytes(int dim)
+{
+    return kChunkCounterBytes + sizeof(float) * 2 * kChunkMaxCtas * chunk_piece_floats(attn_padded_dim(dim));
+}
+
+// One translation unit per pair of types.
+awq_status launch_chunk_f16(const ChunkArgs &a, int sms, cudaStream_t st);
+awq_status launch_chunk_bf16(const ChunkArgs &a, int sms, cudaStream_t st);
+awq_status launch_chunk_f16_e4m3(const ChunkArgs &a, int sms, cudaStream_t st);
+awq_status launch_chunk_bf16_e4m3(const ChunkArgs &a, int sms, cudaStream_t st);
+
+// vec: elements per access (8, 4 or 1).
+awq_status launch_head_norm(const HeadNormArgs &a, int dtype, int vec, int sms, cudaStream_t st);
+
+}  // namespace awq
