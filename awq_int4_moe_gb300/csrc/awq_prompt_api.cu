@@ -31,6 +31,17 @@ awq_status chunk_call(ChunkArgs &a, int32_t dtype, float scale, void *workspace,
     if (unit * (a.max_len / 128 + 1) > most || unit * (rows / R + 1) * a.cache.num_heads * a.batch > most)
         return AWQ_ERR_UNSUPPORTED_SHAPE;
     if (ws_bytes < chunk_workspace_bytes(dim)) return AWQ_ERR_WORKSPACE_TOO_SMALL;
+    // copies are boxes of keys that lie in one page wherever they begin
+    a.box = kChunkKeys;
+    while (a.page_table && a.cache.page_size % a.box) a.box /= 2;
+    const int64_t place = a.page_table ? a.cache.page_size : a.tokens, far = 1ll << 39;
+    for (int i = 0; i < 2; ++i) {
+        const awq_kv_plane &p = i ? a.cache.v : a.cache.k;
+        if ((place > 1 && p.token_stride == 0) || p.token_stride > far || p.head_stride > far || p.page_stride > far)
+            return AWQ_ERR_UNSUPPORTED_SHAPE;
+        a.head_step[i] = p.head_stride ? 1 : 0;
+        a.page_step[i] = p.page_stride ? 1 : 0;
+    }
     a.counters = static_cast<int32_t *>(workspace);
     a.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kChunkCounterBytes);
     a.negative = scale < 0.f;

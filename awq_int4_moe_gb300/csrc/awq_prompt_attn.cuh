@@ -26,11 +26,13 @@
 //   heads larger than 128: one warpgroup, its score tile double-buffered.
 // Tensor memory: S (and P over it, 16 bits) 2 x 128 columns, O 2 x 128 or 256.
 //
-// Warps: 0-7 softmax and output, a thread per row; 8-11 loader (Q, then K and V
-// tiles of 128 keys x 128 columns, 128-byte swizzle, five or ten in shared memory,
-// by cp.async, 16 bytes a thread, as keys of a page or of a packed batch need
-// no tensor map; e4m3 is expanded to fp16 in registers); 12 issues the MMAs. They
-// meet at mbarriers, every wait is bounded.
+// Warps: 0-7 softmax and output, a thread per row; 8 issues the MMAs; 9 finds the
+// units; 10-11 load (Q, then K and V tiles of 128 keys x 128 columns, 128-byte
+// swizzle, by cp.async, 16 bytes a thread, so that any page size and stride will
+// do; e4m3 tiles come as codes first and are expanded to fp16 in shared memory).
+// They meet at mbarriers, every wait is bounded. Registers go where the scores are
+// (208 a thread there): with 227 KB of shared memory in use what spills comes back
+// from L2.
 //
 // Balance. Units are numbered sequence by sequence, head by head, tile by tile;
 // their costs (a unit's keys and a fixed part) have a closed form, and every
@@ -59,23 +61,25 @@ constexpr float kChunkRaiseF16 = 7.f;
 constexpr float kChunkMinFactor = 1.17549435e-38f;
 constexpr float kChunkLn2 = 0.6931471805599453f;
 constexpr int kPiece = 4;              // key tiles: cuts of a unit are multiples of it
-constexpr int kLoaderWarp = 8, kMmaWarp = 12, kChunkThreads = 512;
-constexpr int kAll256 = 1;             // named barrier of both softmax warpgroups
+constexpr int kMmaWarp = 8, kUnitWarp = 9, kLoaderWarp = 10, kLoaders = 64, kChunkThreads = 384;
+constexpr int kUnits = 3;              // units in shared memory
 
-template <int DP>
+template <int DP, bool FP8>
 struct ChunkGeo {
     static constexpr int QT = DP <= 128 ? 2 : 1;            // row tiles of a unit
     static constexpr int R = 128 * QT;
     static constexpr int SC = DP < 128 ? DP : 128;          // columns of a stage
     static constexpr int HV = DP / SC;                      // stages of a key tile
     static constexpr int kStage = kChunkKeys * SC * 2;
-    static constexpr int kStages = 160 * 1024 / kStage;
+    static constexpr int kStages = (FP8 ? 96 : 160) * 1024 / kStage;
+    // e4m3 stages on their way to fp16
+    static constexpr int kRaw = FP8 ? 64 * 1024 / (kStage / 2) : 0;
     static constexpr int kQTile = 128 * DP * 2;             // one row tile of Q
     static constexpr int kQ = QT * kQTile;
     // after Q and the stages: maxima and sums that two slots exchange, rows' powers of two, barriers
-    static constexpr int oStages = kQ, oMl = oStages + kStages * kStage, oExp = oMl + 2 * 128 * 8,
-                         oBars = oExp + 2 * 256, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 1, oMisc = oBars + kBars * 8,
-                         kSmem = oMisc + 64;
+    static constexpr int oStages = kQ, oRaw = oStages + kStages * kStage, oMl = oRaw + kRaw * kStage / 2, oExp = oMl + 2 * 128 * 8,
+                         oUnits = oExp + 2 * 256, oBars = oUnits + kUnits * 64,
+                         kRawBars = FP8 ? kRaw : 1, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 2 * kUnits + 2 * kRawBars, oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
     static constexpr uint32_t kTmemO = 256;                 // first column of O; S at 0 and 128
     static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
@@ -165,10 +169,11 @@ __device__ __forceinline__ uint64_t umma_desc_v(uint32_t addr)
     d |= 2ull << 61;
     return d;
 }
-// kind::f16, 128 rows, N columns, fp32 accumulator; bf16 operands; B MN-major.
-__device__ __forceinline__ uint32_t chunk_idesc(int N, bool bf16, bool b_mn)
+// kind::f16, 128 rows, N columns, fp32 accumulator; bf16 operands; A negated (bit
+// 13); B MN-major.
+__device__ __forceinline__ uint32_t chunk_idesc(int N, bool bf16, bool negative, bool b_mn)
 {
-    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (negative ? 1u << 13 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
            (128u >> 4 << 24);
 }
 
@@ -178,6 +183,21 @@ __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, uint32_t bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// 4D TMA tile load (coordinates innermost first).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1, int c2, int c3)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void sts_v4(uint32_t addr, uint4 v)
 {
@@ -211,21 +231,26 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t v)
 
 // ------------------------------------------------------------------ the units
 
-// What a block has of a unit: key tiles k0 .. k1 - 1.
+// What a block has of a unit: key tiles k0 .. k1 - 1. 16 words, made by one warp
+// and read by the others from shared memory.
 struct Unit {
-    int b, h;              // sequence, KV head
-    int q0, n, ctx;        // the sequence's first row of q, its new tokens, L - n
-    int row0, rows;        // packed rows
-    int keys, tiles;       // keys that its last row sees, and their tiles
-    int k0, k1;
     int64_t at, cost;      // its place in the sum of costs
-    __device__ __forceinline__ bool cut() const { return k0 > 0 || k1 < tiles; }
-    __device__ __forceinline__ int limit(int row, int group) const      // keys that a row sees
-    {
-        const int v = ctx + static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(group)) + 1;
-        return v < 0 ? 0 : v;
-    }
+    int b, h;              // sequence, KV head; b < 0: no more units
+    int q0, ctx;           // the sequence's first row of q, its tokens before the new ones
+    int row0, rows;        // packed rows
+    int keys;              // keys that its last row sees
+    int k0, k1, n0;        // n0: tiles from k0 on that its first 128 rows see something of
+    int all0, all1;        // keys that every row of the unit and every row of its second tile sees
+    __device__ __forceinline__ int tiles() const { return (keys + kChunkKeys - 1) / kChunkKeys; }
+    __device__ __forceinline__ bool cut() const { return k0 > 0 || k1 < tiles(); }
 };
+static_assert(sizeof(Unit) == 64, "16 words");
+
+// Keys that packed row `row` sees, `ctx` tokens before the sequence's new ones.
+__device__ __forceinline__ int row_limit(int ctx, int row, int group)
+{
+    return max(0, ctx + static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(group)) + 1);
+}
 
 // Key tiles of a unit before a cut at `y` of its cost.
 __device__ __forceinline__ int cut_at(int64_t y, int64_t cost, int tiles)
@@ -290,7 +315,10 @@ struct Cursor2 {
     {
         s.n = 0;
         c.T = 0;
-        if (x0 >= x1) return;
+        if (x0 >= x1) {
+            at = x1;                                    // no share: no units
+            return;
+        }
         s = sequence_at(a, b);
         c = Costs<R>(s, a.group);
         const int64_t in = x0 - at;
@@ -317,20 +345,24 @@ struct Cursor2 {
                 s = sequence_at(a, ++b);
                 c = Costs<R>(s, a.group);
             }
+            const int row0 = t * R, rows = min(R, s.n * a.group - row0), ctx = s.len - s.n;
+            u.at = at;
+            u.cost = c.before(t + 1) - c.before(t);
             u.b = b;
             u.h = h;
             u.q0 = s.q0;
-            u.n = s.n;
-            u.ctx = s.len - s.n;
-            u.row0 = t * R;
-            u.rows = min(R, s.n * a.group - u.row0);
-            u.keys = u.limit(u.row0 + u.rows - 1, a.group);
-            u.tiles = (u.keys + kChunkKeys - 1) / kChunkKeys;
-            u.at = at;
-            u.cost = c.before(t + 1) - c.before(t);
-            u.k0 = cut_at(x0 - at, u.cost, u.tiles);
-            u.k1 = cut_at(x1 - at, u.cost, u.tiles);
-            const bool mine = u.tiles ? u.k1 > u.k0 : x0 <= at;
+            u.ctx = ctx;
+            u.row0 = row0;
+            u.rows = rows;
+            u.keys = row_limit(ctx, row0 + rows - 1, a.group);
+            const int tiles = u.tiles();
+            u.k0 = cut_at(x0 - at, u.cost, tiles);
+            u.k1 = cut_at(x1 - at, u.cost, tiles);
+            const int seen0 = row_limit(ctx, row0 + min(rows, 128) - 1, a.group);
+            u.n0 = min(u.k1 - u.k0, max(0, (seen0 + kChunkKeys - 1) / kChunkKeys - u.k0));
+            u.all0 = row_limit(ctx, row0, a.group);
+            u.all1 = row_limit(ctx, row0 + 128, a.group);
+            const bool mine = tiles ? u.k1 > u.k0 : x0 <= at;
             at += u.cost;
             ++t;
             if (mine) return true;
@@ -339,14 +371,14 @@ struct Cursor2 {
     }
 };
 
-// Which of the columns c .. c + 31 of V hold a value that is not finite at a key
+// Which of the columns c .. c + 15 of V hold a value that is not finite at a key
 // that the row sees, among the tiles whose values were made finite on their way
 // to the tensor core. Reads them again: nothing of it runs on finite values.
 template <typename T, bool FP8>
 __device__ __forceinline__ uint32_t not_finite_seen(const ChunkArgs &a, const Unit &u, int limit, int c)
 {
     const awq_kv_plane &pl = a.cache.v;
-    const int from = max(u.limit(u.row0, a.group) / kChunkKeys, u.k0) * kChunkKeys, to = min(limit, u.k1 * kChunkKeys);
+    const int from = max(u.all0 / kChunkKeys, u.k0) * kChunkKeys, to = min(limit, u.k1 * kChunkKeys);
     uint32_t mask = 0;
 #pragma unroll 1
     for (int key = from; key < to; ++key) {
@@ -360,7 +392,7 @@ __device__ __forceinline__ uint32_t not_finite_seen(const ChunkArgs &a, const Un
         }
         off += u.h * pl.head_stride;
 #pragma unroll 1
-        for (int i = 0; i < 32 && c + i < a.cache.head_dim; ++i) {
+        for (int i = 0; i < 16 && c + i < a.cache.head_dim; ++i) {
             bool bad;
             if constexpr (FP8) {
                 bad = (static_cast<const uint8_t *>(pl.data)[off + c + i] & 0x7F) == 0x7F;
@@ -385,7 +417,7 @@ __device__ __forceinline__ int sharing_blocks(const Unit &u, int64_t per, int la
     me = 0;
     for (int base = c0; base <= c1; base += 32) {
         const int c = base + lane;
-        const int ka = cut_at(c * per - u.at, u.cost, u.tiles), kb = cut_at((c + 1) * per - u.at, u.cost, u.tiles);
+        const int ka = cut_at(c * per - u.at, u.cost, u.tiles()), kb = cut_at((c + 1) * per - u.at, u.cost, u.tiles());
         const bool in = c <= c1 && kb > ka;
         const uint32_t all = __ballot_sync(~0u, in);
         if (all == 0) continue;
@@ -403,9 +435,10 @@ __device__ __forceinline__ int sharing_blocks(const Unit &u, int64_t per, int la
 // ----------------------------------------------------------------- the kernel
 
 template <typename T, bool FP8, int DP>
-__global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkArgs a)
+__global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                                                                      const __grid_constant__ ChunkArgs a)
 {
-    using G = ChunkGeo<DP>;
+    using G = ChunkGeo<DP, FP8>;
     using C = typename std::conditional<FP8, __half, T>::type;      // the tensor core's type
     constexpr bool kBf16 = std::is_same<C, __nv_bfloat16>::value;
     constexpr bool kScaledQ = FP8 && !std::is_same<T, C>::value;    // bf16 q as fp16 with a power of two taken out
@@ -423,10 +456,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     uint64_t *const p_full = s_full + 2;         // [2]
     uint64_t *const o_done = p_full + 2;         // [2]
     uint64_t *const drain = o_done + 2;
+    uint64_t *const both = drain + 1;                                        // both softmax warpgroups
+    uint64_t *const u_full = drain + 2, *const u_empty = u_full + kUnits;    // [kUnits]
+    uint64_t *const raw_full = u_empty + kUnits, *const raw_empty = raw_full + G::kRawBars;   // codes; one for guarded tiles
+    Unit *const s_unit = reinterpret_cast<Unit *>(smem + G::oUnits);
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + G::oMisc);
+    int *const s_first = reinterpret_cast<int *>(smem + G::oMisc + 4);
+    int64_t *const s_first_at = reinterpret_cast<int64_t *>(smem + G::oMisc + 8);
     int *const s_bad = reinterpret_cast<int *>(smem + G::oMisc + 16);        // [4]
-    int *const s_first = s_bad + 4;
-    int64_t *const s_first_at = reinterpret_cast<int64_t *>(smem + G::oMisc + 40);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.cache.head_dim;
@@ -436,10 +473,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     }
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&full[i], 128);
+            mbar_init(&full[i], 2);              // the loader's warps
             mbar_init(&empty[i], 1);
         }
-        mbar_init(q_full, 128);
+        mbar_init(q_full, kLoaders);
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -447,8 +484,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             mbar_init(&o_done[i], 1);
         }
         mbar_init(drain, 1);
+        mbar_init(both, 8);
+        for (int i = 0; i < G::kRawBars; ++i) {
+            mbar_init(&raw_full[i], FP8 ? 1 : 2);
+            mbar_init(&raw_empty[i], 2);
+        }
+        for (int i = 0; i < kUnits; ++i) {
+            mbar_init(&u_full[i], 1);
+            mbar_init(&u_empty[i], 11);      // 2 loader warps, the MMA issuer, 8 softmax warps
+        }
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         fence_barrier_init();
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
     }
     if (warp == kMmaWarp) tc_alloc(tmem_slot, 512);
     grid_dependency_wait();
@@ -497,8 +545,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         __syncthreads();
     }
     const uint32_t tmem = *tmem_slot;
-    Cursor2<R> cursor(a, x0, x1, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0);
-    Unit u;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (ok && !mbar_wait_bounded(bar, parity, a.timeout_ns)) {
@@ -506,307 +552,445 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             ok = false;
         }
     };
-    // Stages of a unit in the order that they are used up: K 0 .. ahead - 1, then
-    // V j, K j + ahead ... where `ahead` is 1 if both slots use a tile, else 2.
-    auto ahead_of = [&](const Unit &v) { return QT == 2 && v.rows > 128 ? 1 : min(2, v.k1 - v.k0); };
-    auto k_item = [](int j, int ahead) { return j + max(0, j - ahead + 1); };
-    auto v_item = [](int j, int ahead, int n) { return ahead + j + min(j, n - ahead); };
-
-    if (warp >= kLoaderWarp && warp < kMmaWarp) {
+    // The role's next unit (the ordinal-th, from 1) in shared memory; NULL after the
+    // last one. It is given back, by one thread of each warp, with done_with().
+    auto next_unit = [&](int ordinal) -> const Unit * {
+        const int i = (ordinal - 1) % kUnits;
+        wait(&u_full[i], (ordinal - 1) / kUnits & 1);
+        ok = __all_sync(~0u, ok);                    // (a warp gives up as one)
+        const Unit *const v = s_unit + i;
+        return ok && v->b >= 0 ? v : nullptr;
+    };
+    auto done_with = [&](int ordinal) { mbar_arrive(&u_empty[(ordinal - 1) % kUnits]); };
+    if (warp >= kLoaderWarp) {
         // ------------------------------------------------------- loader
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP8 ? 96 : 80));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         const int lw = warp - kLoaderWarp;
-        uint32_t pos = 0;                                    // stages filled so far
-        int ordinal = 0;
-        while (cursor.next(u)) {
-            ++ordinal;
-            const int G_ = a.group;
-            // ---- Q: 128 rows a tile, lane i finds the row of its turn i / RP
-            {
-                constexpr int CH = DP / 8, RP = 32 / CH;
-                const int ch = lane % CH, sub = lane / CH;
-                const bool col = ch * 8 < D, pad = ch * 8 < (D + 15) / 16 * 16;
-                if (ordinal > 1) wait(q_empty, (ordinal - 2) & 1);
-                const T *const q = static_cast<const T *>(a.q.data);
-#pragma unroll 1
-                for (int w = 0; w < QT; ++w) {
-                    if (w * 128 >= u.rows) break;
-                    const int mine = w * 128 + (lane / RP) * 4 * RP + lw * RP + lane % RP;
-                    int64_t off = -1;
-                    if (mine < u.rows) {
-                        const uint32_t row = u.row0 + mine, tok = row / static_cast<uint32_t>(G_), g = row - tok * G_;
-                        off = (static_cast<int64_t>(u.q0) + tok) * a.q.token_stride + (static_cast<int64_t>(u.h) * G_ + g) * a.q.head_stride;
-                    }
-                    const uint32_t dst0 = smem_u32(smem) + w * G::kQTile + (ch >> 3) * (128 * 128);
+        // ---- Q of a unit, 16 bytes a thread: RP rows of CH chunks a warp and turn, so a
+        // thread's rows are 2 RP apart and its token and head go on by additions.
+        auto load_q = [&](const Unit &u, int ordinal) {
+            constexpr int CH = DP / 8, RP = 32 / CH;
+            const int ch = lane % CH, first = lw * RP + lane / CH;
+            const bool col = ch * 8 < D, pad = ch * 8 < (D + 15) / 16 * 16;
+            const uint32_t group = a.group, row = u.row0 + first;
+            uint32_t g = row % group;
+            const T *src = static_cast<const T *>(a.q.data) + (u.q0 + static_cast<int64_t>(row / group)) * a.q.token_stride +
+                           (static_cast<int64_t>(u.h) * group + g) * a.q.head_stride + ch * 8;
+            const int64_t next_token = a.q.token_stride - static_cast<int64_t>(group) * a.q.head_stride;
+            const int64_t turn = (2 * RP / group) * a.q.token_stride + (2 * RP % group) * a.q.head_stride;
+            if (ordinal > 1) wait(q_empty, (ordinal - 2) & 1);
+            const int rows = u.rows > 128 ? R : 128;                 // (the rows of a tile are all written)
 #pragma unroll 4
-                    for (int p = 0; p < 32 / RP; ++p) {
-                        const int64_t o = __shfl_sync(~0u, off, p * RP + sub);
-                        const int row = p * 4 * RP + lw * RP + sub;
-                        const uint32_t dst = dst0 + sw128_offset(row, ch & 7);
-                        if constexpr (kScaledQ) {
-                            // the row's largest magnitude to [2^14, 2^15)
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (o >= 0 && col) v = *reinterpret_cast<const uint4 *>(q + o + ch * 8);
-                            float f[8];
-                            const uint32_t raw[4] = {v.x, v.y, v.z, v.w};
-                            float top = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 x = unpack2<T>(raw[i]);
-                                f[2 * i] = x.x;
-                                f[2 * i + 1] = x.y;
-                                top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-                            }
-#pragma unroll
-                            for (int m = CH / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
-                            const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112);
-                            const float by = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-                            if (pad)
-                                sts_v4(dst, make_uint4(pack2<__half>(f[0] * by, f[1] * by), pack2<__half>(f[2] * by, f[3] * by),
-                                                       pack2<__half>(f[4] * by, f[5] * by), pack2<__half>(f[6] * by, f[7] * by)));
-                            if (ch == 0) s_exp[(ordinal & 1) * 256 + w * 128 + row] = static_cast<uint8_t>(e + 112);
-                        } else {
-                            if (pad) cp_async_16_or_zero(dst, o >= 0 && col ? q + o + ch * 8 : q, o >= 0 && col ? 16 : 0);
-                        }
-                    }
-                }
+            for (int r = first; r < rows; r += 2 * RP) {
+                const bool in = r < u.rows && col;
+                const uint32_t dst = smem_u32(smem) + (r >> 7) * G::kQTile + (ch >> 3) * (128 * 128) + sw128_offset(r & 127, ch & 7);
                 if constexpr (kScaledQ) {
-                    fence_proxy_async();
-                    mbar_arrive(q_full);
+                    // the row's largest magnitude to [2^14, 2^15)
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (in) v = *reinterpret_cast<const uint4 *>(src);
+                    float f[8];
+                    const uint32_t raw[4] = {v.x, v.y, v.z, v.w};
+                    float top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 x = unpack2<T>(raw[i]);
+                        f[2 * i] = x.x;
+                        f[2 * i + 1] = x.y;
+                        top = max3(top, fabsf(x.x), fabsf(x.y));
+                    }
+#pragma unroll
+                    for (int m = CH / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
+                    const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112);
+                    const float by = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+                    if (pad)
+                        sts_v4(dst, make_uint4(pack2<__half>(f[0] * by, f[1] * by), pack2<__half>(f[2] * by, f[3] * by),
+                                               pack2<__half>(f[4] * by, f[5] * by), pack2<__half>(f[6] * by, f[7] * by)));
+                    if (ch == 0) s_exp[(ordinal & 1) * 256 + r] = static_cast<uint8_t>(e + 112);
                 } else {
-                    cp_async_arrive_noinc(q_full);
+                    if (pad) cp_async_16_or_zero(dst, in ? src : static_cast<const T *>(a.q.data), in ? 16 : 0);
+                }
+                src += turn;
+                g += 2 * RP % group;
+                if (g >= group) {
+                    g -= group;
+                    src += next_token;
                 }
             }
-            // ---- K and V tiles
-            const int n = u.k1 - u.k0, ahead = n ? ahead_of(u) : 0;
-            const int seen_by_all = u.limit(u.row0, G_);                    // keys that every row sees
-            for (int item = 0; item < 2 * n; ++item) {
-                // the item's plane and tile (the inverse of k_item and v_item)
-                int j;
-                bool is_v;
-                if (item < ahead) {
-                    j = item;
-                    is_v = false;
-                } else if (item < ahead + 2 * (n - ahead)) {
-                    j = (item - ahead) >> 1;
-                    is_v = !((item - ahead) & 1);
-                    if (!is_v) j += ahead;
+            if constexpr (kScaledQ) {
+                fence_proxy_async();
+                mbar_arrive(q_full);
+            } else {
+                cp_async_arrive_noinc(q_full);
+            }
+        };
+        // A place in the stages' order: of each unit K 0 .. ahead - 1, then V j, K j +
+        // ahead .. (`ahead` is 1 where both slots use a tile, else 2), a tile's stages
+        // one after another.
+        struct Walk {
+            const Unit *u = nullptr;
+            int ordinal = 0, item = 0, n = 0, ahead = 0;
+            // the tile's number in the unit, and whether it is V's
+            __device__ __forceinline__ int tile(bool &is_v) const
+            {
+                const int i = item / HV;
+                is_v = false;
+                if (i < ahead) return i;
+                is_v = true;
+                if (i >= ahead + 2 * (n - ahead)) return i - n;
+                const int j = (i - ahead) >> 1;
+                is_v = !((i - ahead) & 1);
+                return is_v ? j : j + ahead;
+            }
+        };
+        auto next_of = [&](Walk &w) {
+            w.u = next_unit(++w.ordinal);
+            w.item = 0;
+            w.n = w.u ? w.u->k1 - w.u->k0 : 0;
+            w.ahead = w.u ? min(QT == 2 && w.u->rows > 128 ? 1 : 2, w.n) : 0;
+        };
+        // Copies this warp's part of a stage: boxes of a.box keys (as many as lie in one
+        // page wherever they begin) by a row of the box, from column d0 on; nothing of
+        // boxes past the unit's keys. Its lane 0 arrives at `bar` with their bytes.
+        auto copy = [&](const Unit &u, int key0, bool is_v, int d0, uint32_t dst, int row_bytes, uint64_t *bar, bool part) {
+            const CUtensorMap *const map = is_v ? &map_v : &map_k;
+            const int box = a.box, boxes = kChunkKeys / box;
+            int page = -1, place = 0;
+            // (of more than 32 boxes, a lane has every 32nd)
+            int count = 0;
+            auto find = [&](int i) {
+                const int key = key0 + i * box;
+                page = -1;
+                if (!part || i >= boxes || key >= u.keys) return;
+                if (a.page_table) {
+                    const int at = a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
+                    page = a.page_table[u.b * a.table_stride + at];
+                    place = key - at * a.cache.page_size;
+                    if (page < 0 || page >= a.cache.num_pages) {
+                        set_status(a.status, AWQ_ERR_BAD_INDEX);
+                        page = -1;
+                    }
                 } else {
-                    j = item - n;
-                    is_v = true;
+                    page = 0;
+                    place = u.q0 + key;
                 }
-                const int key0 = (u.k0 + j) * kChunkKeys;
-                const awq_kv_plane &pl = is_v ? a.cache.v : a.cache.k;
-                // lane i: where the row of its turn is
-                constexpr int kElem = FP8 ? 1 : 2;
-                constexpr int CH = SC * kElem / 16, RP = 32 / CH, TURNS = 32 / RP;
-                const int ch = lane % CH, sub = lane / CH;
-                int64_t off = -1;
-                {
-                    const int key = key0 + (lane / RP) * 4 * RP + lw * RP + lane % RP;
-                    if (key < u.keys) {
-                        if (a.page_table) {
-                            const uint32_t page = a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
-                            const int id = a.page_table[u.b * a.table_stride + page];
-                            if (id >= 0 && id < a.cache.num_pages)
-                                off = id * pl.page_stride + (key - static_cast<int>(page) * a.cache.page_size) * pl.token_stride;
-                            else
-                                set_status(a.status, AWQ_ERR_BAD_INDEX);
-                        } else {
-                            off = (static_cast<int64_t>(u.q0) + key) * pl.token_stride;
-                        }
-                        if (off >= 0) off += u.h * pl.head_stride;
-                    }
+            };
+            for (int i = lane; i - lane < boxes; i += 32) {
+                find(i);
+                count += __popc(__ballot_sync(~0u, page >= 0));
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, count * box * row_bytes);
+            __syncwarp();
+            for (int i = lane; i - lane < boxes; i += 32) {
+                if (boxes > 32) find(i);
+                if (page >= 0)
+                    tma_load_4d(dst + i * box * row_bytes, map, bar, d0, place, a.head_step[is_v] * u.h, a.page_step[is_v] * page);
+            }
+        };
+
+        Walk to;                                             // the next stage to fill
+        uint32_t pos = 0;
+        next_of(to);
+        if constexpr (FP8) {
+            // Codes first, up to kRaw stages ahead and on into the next units; both warps
+            // expand them, a row's 16 codes a thread.
+            constexpr int CH = SC / 16, RP = 32 / CH;
+            const int ch = lane % CH, sub = lane / CH;
+            const uint32_t raw0 = smem_u32(smem + G::oRaw);
+            Walk from;                                       // the next stage to copy
+            uint32_t copied = 0;
+            if (lw == 0) next_of(from);
+            // (a unit that is as many ahead as there is room for units would wait for
+            // this thread itself)
+            auto copy_next = [&]() {
+                while (from.item == 2 * HV * from.n) {
+                    if (from.ordinal + 1 >= to.ordinal + kUnits) return false;
+                    next_of(from);
+                    if (!from.u) return false;
                 }
-                // a V tile that some row of the unit does not see in full: values
-                // that are not finite would reach it as 0 times themselves
-                const bool guard = is_v && key0 + kChunkKeys > seen_by_all;
-                for (int hh = 0; hh < HV; ++hh, ++pos) {
-                    const uint32_t st = pos % NST;
-                    const uint32_t base = smem_u32(stages) + st * G::kStage;
-                    const int d0 = hh * SC + ch * (16 / kElem);
-                    const bool col = d0 < D;
+                bool is_v;
+                const int key0 = (from.u->k0 + from.tile(is_v)) * kChunkKeys;
+                const uint32_t i = copied % G::kRaw;
+                if (copied >= G::kRaw) wait(&raw_empty[i], (copied / G::kRaw - 1) & 1);
+                copy(*from.u, key0, is_v, from.item % HV * SC, raw0 + i * (G::kStage / 2), SC, &raw_full[i], true);
+                ++from.item;
+                ++copied;
+                return true;
+            };
+            while (to.u) {
+                load_q(*to.u, to.ordinal);
+                for (; to.item < 2 * HV * to.n; ++to.item, ++pos) {
+                    if (lw == 0)
+                        while (from.u && copied - pos < G::kRaw && copy_next());
+                    bool is_v;
+                    const int key0 = (to.u->k0 + to.tile(is_v)) * kChunkKeys;
+                    // a V tile that some row of the unit does not see in full: values
+                    // that are not finite would reach it as 0 times themselves
+                    const bool guard = is_v && key0 + kChunkKeys > to.u->all0;
+                    const uint32_t st = pos % NST, tile = smem_u32(stages) + st * G::kStage + (ch >> 2) * (kChunkKeys * 128);
+                    const uint32_t ri = pos % G::kRaw, raw = raw0 + ri * (G::kStage / 2) + lane * 16 + lw * (64 * SC);
+                    if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
+                    wait(&raw_full[ri], pos / G::kRaw & 1);
                     bool bad = false;
-                    if constexpr (FP8) {
-                        const uint8_t *const src = static_cast<const uint8_t *>(pl.data);
-                        uint4 raw[TURNS];
 #pragma unroll
-                        for (int p = 0; p < TURNS; ++p) {
-                            const int64_t o = __shfl_sync(~0u, off, p * RP + sub);
-                            raw[p] = o >= 0 && col ? ld_v4(src + o + d0) : make_uint4(0, 0, 0, 0);
-                        }
-                        if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
-                        if (col) {
-#pragma unroll
-                            for (int p = 0; p < TURNS; ++p) {
-                                const int row = p * 4 * RP + lw * RP + sub;
-                                const uint32_t dst = base + (ch >> 2) * (kChunkKeys * 128);
-                                uint32_t w[8];
-                                e4m3x4_f16x4(raw[p].x, w[0], w[1]);
-                                e4m3x4_f16x4(raw[p].y, w[2], w[3]);
-                                e4m3x4_f16x4(raw[p].z, w[4], w[5]);
-                                e4m3x4_f16x4(raw[p].w, w[6], w[7]);
-                                if (guard) {
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const uint32_t f = finite_pair<C>(w[i]);
-                                        bad |= f != w[i];
-                                        w[i] = f;
-                                    }
-                                }
-                                sts_v4(dst + sw128_offset(row, (ch & 3) * 2), make_uint4(w[0], w[1], w[2], w[3]));
-                                sts_v4(dst + sw128_offset(row, (ch & 3) * 2 + 1), make_uint4(w[4], w[5], w[6], w[7]));
-                            }
-                        }
-                        if (bad) s_bad[ordinal & 3] = ordinal;
-                        fence_proxy_async();
-                        mbar_arrive(&full[st]);
-                    } else {
-                        const T *const src = static_cast<const T *>(pl.data);
-                        const bool pad = d0 < (D + 15) / 16 * 16;
-                        const uint32_t dst0 = base + (ch >> 3) * (kChunkKeys * 128) + sw128_offset(lw * RP + sub, ch & 7);
-                        constexpr int kStep = 4 * RP / 8 * 1024;                 // bytes from turn to turn
-                        if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
-#pragma unroll
-                        for (int p = 0; p < TURNS; ++p) {
-                            const int64_t o = __shfl_sync(~0u, off, p * RP + sub);
-                            if (pad) cp_async_16_or_zero(dst0 + p * kStep, o >= 0 && col ? src + o + d0 : src, o >= 0 && col ? 16 : 0);
-                        }
+                    for (int p = 0; p < 64 / RP; ++p) {
+                        const uint4 v = lds_v4(raw + p * 512);
+                        uint32_t w[8];
+                        e4m3x4_f16x4(v.x, w[0], w[1]);
+                        e4m3x4_f16x4(v.y, w[2], w[3]);
+                        e4m3x4_f16x4(v.z, w[4], w[5]);
+                        e4m3x4_f16x4(v.w, w[6], w[7]);
                         if (guard) {
-                            cp_async_commit();
-                            cp_async_wait_group<0>();
-                            if (pad) {
-#pragma unroll 4
-                                for (int p = 0; p < TURNS; ++p) {
-                                    const uint4 v = lds_v4(dst0 + p * kStep);
-                                    const uint4 f = make_uint4(finite_pair<C>(v.x), finite_pair<C>(v.y), finite_pair<C>(v.z),
-                                                               finite_pair<C>(v.w));
-                                    if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
-                                        bad = true;
-                                        sts_v4(dst0 + p * kStep, f);
-                                    }
-                                }
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t f = finite_pair<C>(w[k]);
+                                bad |= f != w[k];
+                                w[k] = f;
                             }
-                            if (bad) s_bad[ordinal & 3] = ordinal;
-                            fence_proxy_async();
-                            mbar_arrive(&full[st]);
-                        } else {
-                            cp_async_arrive_noinc(&full[st]);
                         }
+                        // lanes of the second 64 columns take their chunks the other way
+                        // round, so that no bank is hit twice
+                        const int r = lw * 64 + p * RP + sub;
+                        const bool turned = ch >> 2;
+                        const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+                        sts_v4(tile + sw128_offset(r, (ch & 3) * 2 + (turned ? 1 : 0)), turned ? hi : lo);
+                        sts_v4(tile + sw128_offset(r, (ch & 3) * 2 + (turned ? 0 : 1)), turned ? lo : hi);
+                    }
+                    if (bad) s_bad[to.ordinal & 3] = to.ordinal;
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&raw_empty[ri]);
+                        mbar_arrive(&full[st]);
                     }
                 }
+                __syncwarp();
+                if (lane == 0) done_with(to.ordinal);
+                next_of(to);
+            }
+            if (!ok)                                         // as below
+                for (uint32_t i = copied > G::kRaw ? copied - G::kRaw : 0; i < copied; ++i)
+                    mbar_wait_bounded(&raw_full[i % G::kRaw], i / G::kRaw & 1, a.timeout_ns);
+        } else {
+            uint32_t guarded = 0;
+            while (to.u) {
+                const Unit &u = *to.u;
+                if (to.n == 0) load_q(u, to.ordinal);
+                for (; to.item < 2 * HV * to.n; ++to.item, ++pos) {
+                    bool is_v;
+                    const int key0 = (u.k0 + to.tile(is_v)) * kChunkKeys, d0 = to.item % HV * SC + lw * 64;
+                    const bool guard = is_v && key0 + kChunkKeys > u.all0;               // as above
+                    const uint32_t st = pos % NST, tile = smem_u32(stages) + st * G::kStage;
+                    if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
+                    // a warp copies 64 columns
+                    copy(u, key0, is_v, d0, tile + lw * (kChunkKeys * 128), 128, guard ? raw_full : &full[st], lw * 64 < SC && d0 < D);
+                    if (guard) {
+                        wait(raw_full, guarded);
+                        guarded ^= 1;
+                        bool bad = false;
+                        if (lw * 64 < SC && d0 < D) {
+#pragma unroll 4
+                            for (int i = 0; i < kChunkKeys * 8 / 32; ++i) {
+                                const uint32_t at = tile + lw * (kChunkKeys * 128) + (i * 32 + lane) * 16;
+                                const uint4 v = lds_v4(at);
+                                const uint4 f = make_uint4(finite_pair<C>(v.x), finite_pair<C>(v.y), finite_pair<C>(v.z),
+                                                           finite_pair<C>(v.w));
+                                if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
+                                    bad = true;
+                                    sts_v4(at, f);
+                                }
+                            }
+                        }
+                        if (bad) s_bad[to.ordinal & 3] = to.ordinal;
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&full[st]);
+                    }
+                    if (to.item == HV - 1) load_q(u, to.ordinal);    // behind K's first tile, which has room earlier
+                }
+                __syncwarp();
+                if (lane == 0) done_with(to.ordinal);
+                next_of(to);
             }
         }
         cp_async_commit();
         cp_async_wait_group<0>();
+        // after a time-out: the copies in flight end before the block does
+        if (!ok)
+            for (uint32_t i = pos > NST ? pos - NST : 0; i < pos; ++i) mbar_wait_bounded(&full[i % NST], i / NST & 1, a.timeout_ns);
     } else if (warp >= kMmaWarp) {
-        // ------------------------------------------------------- MMA issuer
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == kMmaWarp && lane == 0) {
+        // ------------------------------------------------------- units, MMA issuer
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kUnitWarp && lane == 0) {
+            // ---- the units, one after another
+            Cursor2<R> cursor(a, x0, x1, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0);
+            bool more = true;
+            for (int i = 0; more; ++i) {
+                Unit u;
+                more = cursor.next(u);
+                if (!more) u.b = -1;
+                if (i >= kUnits) wait(&u_empty[i % kUnits], (i / kUnits - 1) & 1);
+                if (!ok) break;
+                s_unit[i % kUnits] = u;
+                mbar_arrive(&u_full[i % kUnits]);
+            }
+        }
+        if (warp == kMmaWarp) {
+            // The issuing warp's own instructions are on the path of every tile: all its
+            // lanes run them, so that descriptors stay in uniform registers (with one
+            // lane in a branch of its own an MMA took 90 cycles to issue), places in the
+            // ring advance without divisions, and one elected lane issues.
             const int k_steps = (D + 15) / 16;               // of Q K'; times 16: columns of P V
-            const uint32_t q_base = smem_u32(smem), st_base = smem_u32(stages);
-            uint32_t pos = 0;
-            uint32_t p_phase = 0;                            // bit per slot
+            const uint64_t q_desc = umma_desc_sw128(smem_u32(smem));
+            const uint64_t k_desc = umma_desc_sw128(smem_u32(stages)), v_desc = umma_desc_v(smem_u32(stages));
+            const uint32_t qk_id = chunk_idesc(kChunkKeys, kBf16, a.negative, false);
+            struct Place {
+                uint32_t st, phase;
+                __device__ __forceinline__ void advance(uint32_t by)
+                {
+                    st += by;
+                    while (st >= NST) {
+                        st -= NST;
+                        phase ^= 1;
+                    }
+                }
+            };
+            Place kp{0, 0}, vp{0, 0};                        // of the next K and V tile
+            uint32_t p_phase = 0, begun = 0;                 // bits per slot; accumulators that hold something
             int ordinal = 0;
-            while (cursor.next(u)) {
+            auto commit = [&](uint64_t *bar) {
+                if (elect_one()) tc_commit(bar);
+            };
+            // S[slot] = Q[tile] K', and P V for the slot; `release` gives the stages back
+            auto qk = [&](int slot, int tile, bool release) {
+                Place at = kp;
+#pragma unroll
+                for (int hh = 0; hh < HV; ++hh) {
+                    wait(&full[at.st], at.phase);
+                    tc_fence_after();
+                    const uint64_t da = q_desc + ((tile * G::kQTile + hh * (SC / 64) * (128 * 128)) >> 4);
+                    const uint64_t db = k_desc + (at.st * G::kStage >> 4);
+                    const int ks = k_steps - hh * (SC / 16);
+                    auto step = [&](int k) {
+                        constexpr uint32_t kSub = 128 * 128 >> 4;            // 64 columns on
+                        const uint32_t in = (k >> 2) * kSub + (k & 3) * 2;
+                        if (elect_one()) tc_mma_f16(tmem + slot * 128, da + in, db + in, qk_id, k > 0 || hh > 0);
+                    };
+                    if (ks >= SC / 16) {
+#pragma unroll
+                        for (int k = 0; k < SC / 16; ++k) step(k);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < ks; ++k) step(k);
+                    }
+                    if (release) commit(&empty[at.st]);
+                    at.advance(1);
+                }
+                commit(&s_full[slot]);
+            };
+            auto pv = [&](int slot, bool release) {
+                wait(&p_full[slot], p_phase >> slot & 1);
+                p_phase ^= 1u << slot;
+                const int acc = QT == 2 ? slot : 0;
+                Place at = vp;
+#pragma unroll
+                for (int hh = 0; hh < HV; ++hh) {
+                    wait(&full[at.st], at.phase);
+                    tc_fence_after();
+                    const int cols = min(SC, k_steps * 16 - hh * SC);
+                    const uint64_t db = v_desc + (at.st * G::kStage >> 4);
+                    const uint32_t id = chunk_idesc(cols, kBf16, false, true), d = tmem + G::kTmemO + acc * 128 + hh * 128;
+#pragma unroll
+                    for (int k = 0; k < kChunkKeys / 16; ++k)
+                        if (elect_one())
+                            tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id, k > 0 || (begun >> acc & 1));
+                    if (release) commit(&empty[at.st]);
+                    at.advance(1);
+                }
+                begun |= 1u << acc;
+                commit(&o_done[slot]);
+            };
+            while (const Unit *const next = next_unit(ordinal + 1)) {
+                const int n = __shfl_sync(~0u, next->k1 - next->k0, 0);
+                const int n0 = __shfl_sync(~0u, next->n0, 0);        // (the first slot's rows see fewer keys)
+                const bool wide = QT == 2 && __shfl_sync(~0u, next->rows, 0) > 128;
                 ++ordinal;
-                const int n = u.k1 - u.k0;
-                const bool wide = QT == 2 && u.rows > 128;
-                const int ahead = n ? ahead_of(u) : 0;
-                const int steps = wide ? 2 * n : n;
-                // the first slot's rows see fewer keys
-                const int n0 = wide ? min(n, max(0, (u.limit(u.row0 + 127, a.group) + kChunkKeys - 1) / kChunkKeys - u.k0)) : n;
+                if (lane == 0) done_with(ordinal);
+                const int ahead = wide ? min(1, n) : min(2, n);
+                vp = kp;                                     // the unit's first stage
+                vp.advance(ahead * HV);
+                begun = 0;
                 wait(q_full, (ordinal - 1) & 1);
                 fence_proxy_async();
                 tc_fence_after();
-                uint32_t begun = 0;                          // accumulators that hold something
-                for (int s = 0; s < steps + 2; ++s) {
-                    if (s >= 2) {                            // P V of step s - 2
-                        const int slot = s & 1, j = wide ? (s - 2) >> 1 : s - 2;
-                        if (!(wide && slot == 0 && j >= n0)) {
-                            wait(&p_full[slot], p_phase >> slot & 1);
-                            p_phase ^= 1u << slot;
-                            const int at = v_item(j, ahead, n) * HV;
-                            const int acc = QT == 2 ? slot : 0;
-                            for (int hh = 0; hh < HV; ++hh) {
-                                const uint32_t item = pos + at + hh, st = item % NST;
-                                wait(&full[st], (item / NST) & 1);
-                                fence_proxy_async();
-                                tc_fence_after();
-                                const int cols = min(SC, k_steps * 16 - hh * SC);
-                                if (ok && cols > 0) {
-                                    const uint64_t db = umma_desc_v(st_base + st * G::kStage);
-                                    const uint32_t id = chunk_idesc(cols, kBf16, true);
-                                    const uint32_t d = tmem + G::kTmemO + acc * 128 + hh * 128;
-#pragma unroll
-                                    for (int k = 0; k < kChunkKeys / 16; ++k)
-                                        tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id,
-                                                          k > 0 || (begun >> acc & 1));
-                                }
-                                if (!wide || slot == 1) tc_commit(&empty[st]);
-                            }
-                            begun |= 1u << acc;
-                            tc_commit(&o_done[slot]);
+                auto k_done = [&](int j) { kp.advance(j + 1 < ahead ? HV : 2 * HV); };
+                auto v_done = [&](int j) { vp.advance(j < n - ahead ? 2 * HV : HV); };
+                if (wide) {
+                    for (int j = -1; j < n; ++j) {
+                        if (j >= 0 && j < n0) pv(0, false);
+                        if (j + 1 < n0) qk(0, 0, false);
+                        if (j >= 0) {
+                            pv(1, true);
+                            v_done(j);
+                        }
+                        if (j + 1 < n) {
+                            qk(1, 1, true);
+                            k_done(j + 1);
+                            if (j + 2 == n) commit(q_empty);
                         }
                     }
-                    if (s < steps) {                         // Q K' of step s
-                        const int slot = s & 1, j = wide ? s >> 1 : s;
-                        if (!(wide && slot == 0 && j >= n0)) {
-                            const int at = k_item(j, ahead) * HV;
-                            const uint32_t id = chunk_idesc(kChunkKeys, kBf16, false);
-                            for (int hh = 0; hh < HV; ++hh) {
-                                const uint32_t item = pos + at + hh, st = item % NST;
-                                wait(&full[st], (item / NST) & 1);
-                                fence_proxy_async();
-                                tc_fence_after();
-                                const int ks = min(SC / 16, k_steps - hh * (SC / 16));
-                                if (ok) {
-                                    for (int k = 0; k < ks; ++k) {
-                                        const uint32_t in = (k >> 2) * (128 * 128) + (k & 3) * 32;
-                                        const uint64_t da = umma_desc_sw128(q_base + (wide ? slot : 0) * G::kQTile +
-                                                                            hh * (SC / 64) * (128 * 128) + in);
-                                        const uint64_t db = umma_desc_sw128(st_base + st * G::kStage + in);
-                                        tc_mma_f16(tmem + slot * 128, da, db, id, k > 0 || hh > 0);
-                                    }
-                                }
-                                if (!wide || slot == 1) tc_commit(&empty[st]);
-                            }
-                            tc_commit(&s_full[slot]);
+                } else {
+                    for (int j = 0; j < n + 2; ++j) {
+                        if (j >= 2) {
+                            pv(j & 1, true);
+                            v_done(j - 2);
                         }
-                        if (s == steps - 1) tc_commit(q_empty);
+                        if (j < n) {
+                            qk(j & 1, 0, true);
+                            k_done(j);
+                            if (j + 1 == n) commit(q_empty);
+                        }
                     }
                 }
-                if (steps == 0) tc_commit(q_empty);
-                pos += 2 * n * HV;
+                if (n == 0) commit(q_empty);
+                if (n > 0) kp = vp;                          // the next unit begins behind the last V
             }
             // every MMA has completed before the block gives up its tensor memory
-            tc_commit(drain);
+            commit(drain);
             if (!mbar_wait_bounded(drain, 0, a.timeout_ns)) set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
         }
     } else {
         // ------------------------------------------------------- softmax and output
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP8 ? 184 : 192));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int w = warp >> 2, row = (warp & 3) * 32 + lane;               // this thread's row of a tile
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         uint32_t s_phase = 0, o_phase = 0;                                   // a bit per slot: score tiles, products with V
         int last = 0;                                                        // slot of the latest product
-        Unit shared_unit[2];                                                 // cut at its begin, at its end
-        uint32_t has_shared = 0;
+        // Units that are cut at their begin and at their end: a lane's word of the
+        // first (lanes 0-15) and of the second.
+        uint32_t shared_unit = 0, has_shared = 0;
         int ordinal = 0;
         float *const my_parts = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * chunk_piece_floats(DP);
-        while (cursor.next(u)) {
+        // Both warpgroups meet.
+        uint32_t met = 0;
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(both);
+            wait(both, met);
+            met ^= 1;
+            ok = __all_sync(~0u, ok);
+        };
+        while (const Unit *const next = next_unit(ordinal + 1)) {
+            const Unit &u = *next;
             ++ordinal;
-            const int n = u.k1 - u.k0, G_ = a.group;
+            const int n = u.k1 - u.k0, k0 = u.k0;
             const bool wide = QT == 2 && u.rows > 128;
             const int in_unit = wide ? w * 128 + row : row;                  // this thread's row of the unit
-            const bool valid = in_unit < u.rows;
-            const int my_row = u.row0 + (valid ? in_unit : u.rows - 1);
-            const int limit = u.limit(my_row, G_);
+            const int limit = row_limit(u.ctx, u.row0 + min(in_unit, u.rows - 1), a.group);
             // its slot's key tiles: first, step, end
-            const int n0 = wide && w == 0 ? min(n, max(0, (u.limit(u.row0 + 127, G_) + kChunkKeys - 1) / kChunkKeys - u.k0)) : n;
+            const int n0 = wide && w == 0 ? u.n0 : n;
             const int j0 = QT == 2 && !wide ? w : 0, step = QT == 2 && !wide ? 2 : 1;
             const bool idle = QT == 1 && w == 1;
-            const int all_see = u.limit(u.row0 + (wide ? w * 128 : 0), G_);  // keys that every row of the tile sees
+            const int all_see = wide && w == 1 ? u.all1 : u.all0;            // keys that every row of the tile sees
             float m = -INFINITY, l = 0.f, factor = 0.f;
             bool first = true;
             for (int j = idle ? n0 : j0; j < n0; j += step) {
@@ -829,11 +1013,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) tc_wait_ld32(s + c);
                 }
-                if (a.negative) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = -s[c];
-                }
-                const int key0 = (u.k0 + j) * kChunkKeys;
+                const int key0 = (k0 + j) * kChunkKeys;
                 if (key0 + kChunkKeys > all_see) {
                     const int seen = limit - key0;
 #pragma unroll
@@ -860,14 +1040,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                         ok = __all_sync(~0u, ok);
                         tc_fence_after();
                         if (ok) {
-                            for (int c = 0; c < (D + 31) / 32 * 32; c += 32) {
-                                float o[32];
-                                tc_ld32_async(lanes + G::kTmemO + acc * 128 + c, o);
-                                tc_wait_ld32(o);
-                                uint32_t r[32];
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tc_ld16(lanes + G::kTmemO + acc * 128 + c, o);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * by);
-                                tc_st32(lanes + G::kTmemO + acc * 128 + c, r);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                                tc_st16(lanes + G::kTmemO + acc * 128 + c, o);
                             }
                         }
                     }
@@ -902,6 +1081,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             }
             // ---- the unit's output, or this block's piece of it
             const int acc = QT == 2 ? w : 0;
+            const bool valid = in_unit < u.rows, cut = u.cut();
+            const int my_row = u.row0 + (valid ? in_unit : u.rows - 1), G_ = a.group;
             if (!first) {
                 wait(&o_done[last], (o_phase >> last & 1) ^ 1);
                 ok = __all_sync(~0u, ok);
@@ -912,7 +1093,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             if (merge) {
                 s_ml[w * 128 + row] = make_float2(m, l);
                 tc_fence_before();
-                named_barrier_sync(kAll256, 256);
+                meet();
                 tc_fence_after();
                 const float2 x = s_ml[row], y = s_ml[128 + row];
                 m = fmaxf(x.x, y.x);
@@ -920,11 +1101,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 w0 = ex2(x.x - ref);
                 w1 = ex2(y.x - ref);
                 l = x.y * w0 + y.y * w1;
-            }
-            if (u.cut()) {
-                const int which = u.k0 > 0 ? 0 : 1;
-                shared_unit[which] = u;
-                has_shared |= 1u << which;
             }
             if (!idle && ok) {
                 const bool some = merge ? n > 0 : !first;                    // an accumulator holds something
@@ -938,46 +1114,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 // merged: each warpgroup takes half of the columns
                 const int c0 = merge ? w * (DP / 2) : 0, c1 = merge ? c0 + DP / 2 : DP;
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 32) {
+                for (int c = c0; c < c1; c += 16) {
                     if (c >= D) break;
-                    float o[32];
+                    uint32_t o[16];
                     if (some) {
-                        tc_ld32_async(lanes + G::kTmemO + (merge ? 0 : acc * 128) + c, o);
-                        tc_wait_ld32(o);
+                        tc_ld16(lanes + G::kTmemO + (merge ? 0 : acc * 128) + c, o);
                         if (merge && n > 1) {
-                            float o1[32];
-                            tc_ld32_async(lanes + G::kTmemO + 128 + c, o1);
-                            tc_wait_ld32(o1);
+                            uint32_t o1[16];
+                            tc_ld16(lanes + G::kTmemO + 128 + c, o1);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * w0 + __uint_as_float(o1[i]) * w1);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                        for (int i = 0; i < 16; ++i) o[i] = 0;
                     }
                     if (guard) {
                         const uint32_t mask = valid ? not_finite_seen<T, FP8>(a, u, limit, c) : 0;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (mask >> i & 1) o[i] = __int_as_float(0x7FC00000);
+                        for (int i = 0; i < 16; ++i)
+                            if (mask >> i & 1) o[i] = 0x7FC00000u;
                         __syncwarp();
                     }
-                    if (u.cut()) {
+                    if (cut) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            piece[((c + i) >> 2) * 128 + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int i = 0; i < 16; i += 4)
+                            piece[((c + i) >> 2) * 128 + row] = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
+                                                                            __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
                     } else if (valid) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
+                        for (int i = 0; i < 16; i += 8)
                             if (c + i < D) {
-                                const float f[8] = {o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv,
-                                                    o[i + 4] * inv, o[i + 5] * inv, o[i + 6] * inv, o[i + 7] * inv};
+                                float f[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(o[i + k]) * inv;
                                 store_elems<T, 8>(out + c + i, f);
                             }
                     }
                 }
                 if (!merge || w == 0) {
-                    if (u.cut()) {
+                    if (cut) {
                         float *const ml = reinterpret_cast<float *>(piece) + 128 * DP;
                         ml[row] = m == -INFINITY ? m : m - kRaise;
                         ml[128 + row] = l;
@@ -988,28 +1165,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             }
             if (merge) {
                 tc_fence_before();
-                named_barrier_sync(kAll256, 256);
+                meet();
                 tc_fence_after();
             }
-            if (u.cut()) {
+            if (cut) {
+                const int which = u.k0 > 0 ? 0 : 1;
+                if (lane >> 4 == which) shared_unit = reinterpret_cast<const uint32_t *>(&u)[lane & 15];
+                has_shared |= 1u << which;
                 __threadfence();
-                named_barrier_sync(kAll256, 256);
+                meet();
                 if (warp == 0) {
                     int me, count;
                     const int begun = sharing_blocks(u, per_cta, lane, nullptr, me, count);
-                    if (lane == 0) atomic_add_acq_rel(a.counters + 2 * begun, 1);
+                    if (lane == 0 && ok) atomic_add_acq_rel(a.counters + 2 * begun, 1);
                 }
             }
+            __syncwarp();
+            if (lane == 0) done_with(ordinal);
         }
         // ---- the cut units: each of the blocks that share one joins a part of it
         for (int which = 0; which < 2; ++which) {
             if (!(has_shared >> which & 1)) continue;
-            const Unit v = shared_unit[which];
             int16_t *const list = reinterpret_cast<int16_t *>(s_ml);         // [kChunkMaxCtas], then place, number, first
-            named_barrier_sync(kAll256, 256);
+            Unit *const kept = reinterpret_cast<Unit *>(smem + G::oMl + 1024);
+            meet();
             if (warp == 0) {
+                if (lane >> 4 == which) reinterpret_cast<uint32_t *>(kept)[lane & 15] = shared_unit;
+                __syncwarp();
                 int me, count;
-                const int begun = sharing_blocks(v, per_cta, lane, list, me, count);
+                const int begun = sharing_blocks(*kept, per_cta, lane, list, me, count);
                 if (lane == 0) {
                     list[kChunkMaxCtas] = static_cast<int16_t>(me);
                     list[kChunkMaxCtas + 1] = static_cast<int16_t>(count);
@@ -1020,11 +1204,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                             set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
                             ok = false;
                         }
+                    if (!ok) list[kChunkMaxCtas + 1] = 0;
                 }
-                ok = __all_sync(~0u, ok);
             }
-            ok = named_barrier_and(kAll256, 256, ok);
+            meet();
+            ok = ok && list[kChunkMaxCtas + 1] > 0;
             if (!ok) continue;
+            const Unit v = *kept;
             const int me = list[kChunkMaxCtas], count = list[kChunkMaxCtas + 1], begun = list[kChunkMaxCtas + 2];
             const int rows = v.rows, items = rows * (D / 8);
             const int lo = static_cast<int>(static_cast<int64_t>(items) * me / count);
@@ -1066,8 +1252,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     a.lse[out_row * a.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kChunkLn2;
             }
             // the last block to leave makes the counters ready for the next call
-            named_barrier_sync(kAll256, 256);
-            if (tid == 0 && atomic_add_acq_rel(a.counters + 2 * begun + 1, 1) == count - 1) {
+            meet();
+            if (tid == 0 && ok && atomic_add_acq_rel(a.counters + 2 * begun + 1, 1) == count - 1) {
                 a.counters[2 * begun] = 0;
                 a.counters[2 * begun + 1] = 0;
             }
@@ -1079,13 +1265,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     if (warp == kMmaWarp) tc_dealloc(tmem, 512);
 }
 
+// A plane as [page][head][token of a page][element], boxes of `box` tokens.
+template <bool FP8, int DP>
+bool plane_map(CUtensorMap *m, const ChunkArgs &a, const awq_kv_plane &p)
+{
+    const cuuint64_t elem = FP8 ? 1 : 2;
+    const bool paged = a.page_table;
+    // (a stride that is not used or 0 makes its dimension one)
+    const auto dim = [](int64_t n, int64_t stride) { return static_cast<cuuint64_t>(stride ? n : 1); };
+    const auto bytes = [&](int64_t stride) { return static_cast<cuuint64_t>(stride ? stride * elem : 16); };
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.cache.head_dim), dim(paged ? a.cache.page_size : a.tokens, p.token_stride),
+                                dim(a.cache.num_heads, p.head_stride), dim(paged ? a.cache.num_pages : 1, p.page_stride)};
+    const cuuint64_t strides[3] = {bytes(p.token_stride), bytes(p.head_stride), bytes(p.page_stride)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(FP8 ? ChunkGeo<DP, FP8>::SC : 64), static_cast<cuuint32_t>(a.box), 1, 1};
+    return encode_tensor_map(m, FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, p.data, dims, strides, box,
+                             FP8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 template <typename T, bool FP8, int DP>
 awq_status launch_chunk_d(const ChunkArgs &a, int sms, cudaStream_t st)
 {
-    const awq_status r = set_smem(chunk_attn_kernel<T, FP8, DP>, ChunkGeo<DP>::kSmem);
+    CUtensorMap map_k, map_v;
+    if (!plane_map<FP8, DP>(&map_k, a, a.cache.k) || !plane_map<FP8, DP>(&map_v, a, a.cache.v)) return AWQ_ERR_CUDA;
+    const awq_status r = set_smem(chunk_attn_kernel<T, FP8, DP>, ChunkGeo<DP, FP8>::kSmem);
     if (r) return r;
     const int grid = sms < kChunkMaxCtas ? sms : kChunkMaxCtas;
-    return launch_ex(chunk_attn_kernel<T, FP8, DP>, dim3(grid), dim3(kChunkThreads), ChunkGeo<DP>::kSmem, 1, true, st, a);
+    return launch_ex(chunk_attn_kernel<T, FP8, DP>, dim3(grid), dim3(kChunkThreads), ChunkGeo<DP, FP8>::kSmem, 1, true, st, map_k, map_v, a);
 }
 
 template <typename T, bool FP8>

@@ -23,6 +23,8 @@ struct ChunkArgs {
     int32_t max_len, batch, tokens, q_heads, group;
     uint32_t page_magic;           // as in AttnArgs
     int32_t page_shift;
+    int32_t box;                   // keys of one copy: the largest power of two up to 128 that divides a page
+    int32_t head_step[2], page_step[2];    // of K and V: 0 where the plane's stride is 0, else 1
     float factor;                  // |scale| * log2(e) * K's scale
     int32_t negative;              // the scale is below 0
     uint64_t timeout_ns;

@@ -33,8 +33,8 @@ extern "C" {
  * that fall, or leave [0, tokens], set AWQ_ERR_BAD_INDEX; nothing outside the
  * buffers is touched, and the sequences that they bound are undefined.
  * q, out: 16-bit [tokens][q_heads][head_dim]; k, v: [tokens][kv_heads]
- * [head_dim], all 16-byte aligned with strides that are multiples of 16 bytes;
- * cu_seqlens i32[batch + 1]; lse f32[tokens][q_heads], dense, or NULL.
+ * [head_dim], all 16-byte aligned with strides that are multiples of 16 bytes
+ * (k's and v's below 2^39 elements, between tokens not 0); cu_seqlens i32[batch + 1]; lse f32[tokens][q_heads], dense, or NULL.
  * batch, tokens >= 0 (0 launches nothing); q_heads a multiple of kv_heads;
  * head_dim a multiple of 8 up to AWQ_ATTN_MAX_HEAD_DIM; tokens * (q_heads /
  * kv_heads) below 2^31 and batch * kv_heads * (tokens * (q_heads / kv_heads) /
@@ -81,7 +81,9 @@ AWQ_API size_t awq_prompt_attention_workspace_bytes(int32_t head_dim);
  * i32[batch]; q, out, cu_seqlens, lse, workspace and limits as in
  * awq_prompt_attention, with max_pages * page_size in place of 2 * tokens; head_dim a
  * multiple of 16 for an e4m3 cache; both planes 16-byte aligned with strides
- * that are multiples of 16 bytes.
+ * that are multiples of 16 bytes, below 2^39 elements and between tokens not 0.
+ * The cache is copied in boxes of as many tokens as the largest power of two up
+ * to 128 that divides page_size: pages of an odd size are read token by token.
  */
 AWQ_API awq_status awq_chunk_attention(const awq_heads *q, const awq_kv_cache *cache,
                                        const int32_t *page_table, int64_t table_stride, int32_t max_pages,
