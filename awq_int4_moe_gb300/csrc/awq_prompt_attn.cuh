@@ -79,7 +79,7 @@ struct ChunkGeo {
     // after Q and the stages: maxima and sums that two slots exchange, rows' powers of two, barriers
     static constexpr int oStages = kQ, oRaw = oStages + kStages * kStage, oMl = oRaw + kRaw * kStage / 2, oExp = oMl + 2 * 128 * 8,
                          oUnits = oExp + 2 * 256, oBars = oUnits + kUnits * 64,
-                         kRawBars = FP8 ? kRaw : 1, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 2 * kUnits + 2 * kRawBars, oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
+                         kRawBars = FP8 ? kRaw : 1, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 2 + 2 * kUnits + 2 * kRawBars, oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
     static constexpr uint32_t kTmemO = 256;                 // first column of O; S at 0 and 128
     static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
@@ -218,6 +218,16 @@ __device__ __forceinline__ int atomic_add_acq_rel(int32_t *p, int v)
     return old;
 }
 
+// Whether one of four pairs of 16-bit values is not finite: an exponent of ones
+// carries into the sign's place.
+template <typename C>
+__device__ __forceinline__ uint32_t not_finite4(uint4 v)
+{
+    constexpr uint32_t M = std::is_same<C, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+    constexpr uint32_t one = std::is_same<C, __half>::value ? 0x04000400u : 0x00800080u;
+    return (((v.x & M) + one) | ((v.y & M) + one) | ((v.z & M) + one) | ((v.w & M) + one)) & 0x80008000u;
+}
+
 // A pair of 16-bit values with those that are not finite made 0.
 template <typename C>
 __device__ __forceinline__ uint32_t finite_pair(uint32_t v)
@@ -227,6 +237,31 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t v)
     if ((v & M) == M) r &= 0xFFFF0000u;
     if ((v & (M << 16)) == (M << 16)) r &= 0x0000FFFFu;
     return r;
+}
+
+// Of 4 neighbouring lanes l with chunks i (r[4 i] .. r[4 i + 3]): chunk l of lane
+// l ^ i comes to r[4 i].
+__device__ __forceinline__ void transpose_chunks(uint32_t (&r)[16], int lane)
+{
+    // chunk i ^ l to place i
+#pragma unroll
+    for (int d = 2; d > 0; d >>= 1) {
+        const bool swap = lane & d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t a = r[4 * i + k], b = r[4 * (i ^ d) + k];
+                r[4 * i + k] = swap ? b : a;
+                r[4 * (i ^ d) + k] = swap ? a : b;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[4 * i + k] = __shfl_xor_sync(~0u, r[4 * i + k], i);
 }
 
 // ------------------------------------------------------------------ the units
@@ -371,7 +406,7 @@ struct Cursor2 {
     }
 };
 
-// Which of the columns c .. c + 15 of V hold a value that is not finite at a key
+// Which of the columns c .. c + 31 of V hold a value that is not finite at a key
 // that the row sees, among the tiles whose values were made finite on their way
 // to the tensor core. Reads them again: nothing of it runs on finite values.
 template <typename T, bool FP8>
@@ -392,7 +427,7 @@ __device__ __forceinline__ uint32_t not_finite_seen(const ChunkArgs &a, const Un
         }
         off += u.h * pl.head_stride;
 #pragma unroll 1
-        for (int i = 0; i < 16 && c + i < a.cache.head_dim; ++i) {
+        for (int i = 0; i < 32 && c + i < a.cache.head_dim; ++i) {
             bool bad;
             if constexpr (FP8) {
                 bad = (static_cast<const uint8_t *>(pl.data)[off + c + i] & 0x7F) == 0x7F;
@@ -453,7 +488,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     uint64_t *const empty = full + NST;
     uint64_t *const q_full = empty + NST, *const q_empty = q_full + 1;
     uint64_t *const s_full = q_empty + 1;        // [2]
-    uint64_t *const p_full = s_full + 2;         // [2]
+    uint64_t *const p_half = s_full + 2;         // [2]: weights of 64 keys
+    uint64_t *const p_full = p_half + 2;         // [2]
     uint64_t *const o_done = p_full + 2;         // [2]
     uint64_t *const drain = o_done + 2;
     uint64_t *const both = drain + 1;                                        // both softmax warpgroups
@@ -480,6 +516,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
+            mbar_init(&p_half[i], 4);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
@@ -730,32 +767,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     const uint32_t ri = pos % G::kRaw, raw = raw0 + ri * (G::kStage / 2) + lane * 16 + lw * (64 * SC);
                     if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
                     wait(&raw_full[ri], pos / G::kRaw & 1);
-                    bool bad = false;
+                    constexpr int B = 8;                             // loads in flight
 #pragma unroll
-                    for (int p = 0; p < 64 / RP; ++p) {
-                        const uint4 v = lds_v4(raw + p * 512);
-                        uint32_t w[8];
-                        e4m3x4_f16x4(v.x, w[0], w[1]);
-                        e4m3x4_f16x4(v.y, w[2], w[3]);
-                        e4m3x4_f16x4(v.z, w[4], w[5]);
-                        e4m3x4_f16x4(v.w, w[6], w[7]);
-                        if (guard) {
+                    for (int p0 = 0; p0 < 64 / RP; p0 += B) {
+                        uint4 v[B];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const uint32_t f = finite_pair<C>(w[k]);
-                                bad |= f != w[k];
-                                w[k] = f;
+                        for (int i = 0; i < B; ++i) v[i] = lds_v4(raw + (p0 + i) * 512);
+#pragma unroll
+                        for (int i = 0; i < B; ++i) {
+                            uint32_t w[8];
+                            e4m3x4_f16x4(v[i].x, w[0], w[1]);
+                            e4m3x4_f16x4(v[i].y, w[2], w[3]);
+                            e4m3x4_f16x4(v[i].z, w[4], w[5]);
+                            e4m3x4_f16x4(v[i].w, w[6], w[7]);
+                            uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+                            if (guard && (not_finite4<C>(lo) | not_finite4<C>(hi))) {
+                                s_bad[to.ordinal & 3] = to.ordinal;
+                                lo = make_uint4(finite_pair<C>(w[0]), finite_pair<C>(w[1]), finite_pair<C>(w[2]), finite_pair<C>(w[3]));
+                                hi = make_uint4(finite_pair<C>(w[4]), finite_pair<C>(w[5]), finite_pair<C>(w[6]), finite_pair<C>(w[7]));
                             }
+                            // lanes of the second 64 columns take their chunks the other way
+                            // round, so that no bank is hit twice
+                            const int r = lw * 64 + (p0 + i) * RP + sub;
+                            const bool turned = ch >> 2;
+                            sts_v4(tile + sw128_offset(r, (ch & 3) * 2 + (turned ? 1 : 0)), turned ? hi : lo);
+                            sts_v4(tile + sw128_offset(r, (ch & 3) * 2 + (turned ? 0 : 1)), turned ? lo : hi);
                         }
-                        // lanes of the second 64 columns take their chunks the other way
-                        // round, so that no bank is hit twice
-                        const int r = lw * 64 + p * RP + sub;
-                        const bool turned = ch >> 2;
-                        const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
-                        sts_v4(tile + sw128_offset(r, (ch & 3) * 2 + (turned ? 1 : 0)), turned ? hi : lo);
-                        sts_v4(tile + sw128_offset(r, (ch & 3) * 2 + (turned ? 0 : 1)), turned ? lo : hi);
                     }
-                    if (bad) s_bad[to.ordinal & 3] = to.ordinal;
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
@@ -774,8 +812,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             uint32_t guarded = 0;
             while (to.u) {
                 const Unit &u = *to.u;
-                if (to.n == 0) load_q(u, to.ordinal);
-                for (; to.item < 2 * HV * to.n; ++to.item, ++pos) {
+                for (;; ++to.item, ++pos) {
+                    if (to.item == min(HV, 2 * HV * to.n)) load_q(u, to.ordinal);    // behind K's first tile, which has room earlier
+                    if (to.item == 2 * HV * to.n) break;
                     bool is_v;
                     const int key0 = (u.k0 + to.tile(is_v)) * kChunkKeys, d0 = to.item % HV * SC + lw * 64;
                     const bool guard = is_v && key0 + kChunkKeys > u.all0;               // as above
@@ -786,26 +825,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     if (guard) {
                         wait(raw_full, guarded);
                         guarded ^= 1;
-                        bool bad = false;
                         if (lw * 64 < SC && d0 < D) {
-#pragma unroll 4
-                            for (int i = 0; i < kChunkKeys * 8 / 32; ++i) {
-                                const uint32_t at = tile + lw * (kChunkKeys * 128) + (i * 32 + lane) * 16;
-                                const uint4 v = lds_v4(at);
-                                const uint4 f = make_uint4(finite_pair<C>(v.x), finite_pair<C>(v.y), finite_pair<C>(v.z),
-                                                           finite_pair<C>(v.w));
-                                if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
-                                    bad = true;
-                                    sts_v4(at, f);
+                            const uint32_t mine = tile + lw * (kChunkKeys * 128) + lane * 16;
+#pragma unroll 1
+                            for (int i = 0; i < kChunkKeys * 8 / 32; i += 8) {
+                                uint4 v[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) v[k] = lds_v4(mine + (i + k) * 512);
+                                uint32_t bad = 0;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) bad |= not_finite4<C>(v[k]);
+                                if (bad) {
+                                    s_bad[to.ordinal & 3] = to.ordinal;
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k)
+                                        sts_v4(mine + (i + k) * 512, make_uint4(finite_pair<C>(v[k].x), finite_pair<C>(v[k].y),
+                                                                                finite_pair<C>(v[k].z), finite_pair<C>(v[k].w)));
                                 }
                             }
                         }
-                        if (bad) s_bad[to.ordinal & 3] = to.ordinal;
                         fence_proxy_async();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&full[st]);
                     }
-                    if (to.item == HV - 1) load_q(u, to.ordinal);    // behind K's first tile, which has room earlier
                 }
                 __syncwarp();
                 if (lane == 0) done_with(to.ordinal);
@@ -855,59 +897,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 }
             };
             Place kp{0, 0}, vp{0, 0};                        // of the next K and V tile
-            uint32_t p_phase = 0, begun = 0;                 // bits per slot; accumulators that hold something
+            uint32_t p_phase = 0;                            // a bit per slot
             int ordinal = 0;
             auto commit = [&](uint64_t *bar) {
                 if (elect_one()) tc_commit(bar);
-            };
-            // S[slot] = Q[tile] K', and P V for the slot; `release` gives the stages back
-            auto qk = [&](int slot, int tile, bool release) {
-                Place at = kp;
-#pragma unroll
-                for (int hh = 0; hh < HV; ++hh) {
-                    wait(&full[at.st], at.phase);
-                    tc_fence_after();
-                    const uint64_t da = q_desc + ((tile * G::kQTile + hh * (SC / 64) * (128 * 128)) >> 4);
-                    const uint64_t db = k_desc + (at.st * G::kStage >> 4);
-                    const int ks = k_steps - hh * (SC / 16);
-                    auto step = [&](int k) {
-                        constexpr uint32_t kSub = 128 * 128 >> 4;            // 64 columns on
-                        const uint32_t in = (k >> 2) * kSub + (k & 3) * 2;
-                        if (elect_one()) tc_mma_f16(tmem + slot * 128, da + in, db + in, qk_id, k > 0 || hh > 0);
-                    };
-                    if (ks >= SC / 16) {
-#pragma unroll
-                        for (int k = 0; k < SC / 16; ++k) step(k);
-                    } else {
-#pragma unroll 1
-                        for (int k = 0; k < ks; ++k) step(k);
-                    }
-                    if (release) commit(&empty[at.st]);
-                    at.advance(1);
-                }
-                commit(&s_full[slot]);
-            };
-            auto pv = [&](int slot, bool release) {
-                wait(&p_full[slot], p_phase >> slot & 1);
-                p_phase ^= 1u << slot;
-                const int acc = QT == 2 ? slot : 0;
-                Place at = vp;
-#pragma unroll
-                for (int hh = 0; hh < HV; ++hh) {
-                    wait(&full[at.st], at.phase);
-                    tc_fence_after();
-                    const int cols = min(SC, k_steps * 16 - hh * SC);
-                    const uint64_t db = v_desc + (at.st * G::kStage >> 4);
-                    const uint32_t id = chunk_idesc(cols, kBf16, false, true), d = tmem + G::kTmemO + acc * 128 + hh * 128;
-#pragma unroll
-                    for (int k = 0; k < kChunkKeys / 16; ++k)
-                        if (elect_one())
-                            tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id, k > 0 || (begun >> acc & 1));
-                    if (release) commit(&empty[at.st]);
-                    at.advance(1);
-                }
-                begun |= 1u << acc;
-                commit(&o_done[slot]);
             };
             while (const Unit *const next = next_unit(ordinal + 1)) {
                 const int n = __shfl_sync(~0u, next->k1 - next->k0, 0);
@@ -915,43 +908,94 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 const bool wide = QT == 2 && __shfl_sync(~0u, next->rows, 0) > 128;
                 ++ordinal;
                 if (lane == 0) done_with(ordinal);
-                const int ahead = wide ? min(1, n) : min(2, n);
+                const int ahead = wide ? min(1, n) : min(2, n), steps = wide ? 2 * n : n;
                 vp = kp;                                     // the unit's first stage
                 vp.advance(ahead * HV);
-                begun = 0;
                 wait(q_full, (ordinal - 1) & 1);
                 fence_proxy_async();
                 tc_fence_after();
-                auto k_done = [&](int j) { kp.advance(j + 1 < ahead ? HV : 2 * HV); };
-                auto v_done = [&](int j) { vp.advance(j < n - ahead ? 2 * HV : HV); };
-                if (wide) {
-                    for (int j = -1; j < n; ++j) {
-                        if (j >= 0 && j < n0) pv(0, false);
-                        if (j + 1 < n0) qk(0, 0, false);
-                        if (j >= 0) {
-                            pv(1, true);
-                            v_done(j);
-                        }
-                        if (j + 1 < n) {
-                            qk(1, 1, true);
-                            k_done(j + 1);
-                            if (j + 2 == n) commit(q_empty);
-                        }
+                auto full_at = [&](Place at) {
+#pragma unroll
+                    for (int hh = 0; hh < HV; ++hh) {
+                        wait(&full[at.st], at.phase);
+                        at.advance(1);
                     }
-                } else {
-                    for (int j = 0; j < n + 2; ++j) {
-                        if (j >= 2) {
-                            pv(j & 1, true);
-                            v_done(j - 2);
+                };
+                // Step s: P V of step s - 2, then S = Q K' of step s, in slot s mod 2. (One
+                // loop and one copy of the code of each: code that does not stay in the
+                // instruction cache takes longer than what it does.)
+                uint32_t begun = 0;                          // accumulators that hold something
+#pragma unroll 1
+                for (int s = 0; s < steps + 2; ++s) {
+                    const int slot = s & 1, jv = wide ? (s - 2) >> 1 : s - 2, jk = wide ? s >> 1 : s;
+                    const bool skip_v = wide && slot == 0 && jv >= n0, skip_k = wide && slot == 0 && jk >= n0;
+                    const bool pv = s >= 2 && !skip_v, qk = s < steps && !skip_k;
+                    const bool release = !wide || slot;      // a tile's last use
+                    // Stages are waited for before the weights, so that the two products
+                    // follow each other without a pause; at a tile's first use.
+                    if (QT == 2 && pv && (!wide || slot == 0 || jv >= n0)) full_at(vp);
+                    if (QT == 2 && qk && (!wide || slot == 0 || jk >= n0)) full_at(kp);
+                    if (pv) {
+                        const uint32_t phase = p_phase >> slot & 1;
+                        p_phase ^= 1u << slot;
+                        const int acc = QT == 2 ? slot : 0;
+                        wait(&p_half[slot], phase);
+                        Place at = vp;
+#pragma unroll
+                        for (int hh = 0; hh < HV; ++hh) {
+                            if (QT == 1) wait(&full[at.st], at.phase);
+                            tc_fence_after();
+                            const int cols = min(SC, k_steps * 16 - hh * SC);
+                            const uint64_t db = v_desc + (at.st * G::kStage >> 4);
+                            const uint32_t id = chunk_idesc(cols, kBf16, false, true), d = tmem + G::kTmemO + acc * 128 + hh * 128;
+                            const uint32_t more = begun >> acc & 1;
+#pragma unroll
+                            for (int k = 0; k < kChunkKeys / 16; ++k) {
+                                if (k == kChunkKeys / 32 && hh == 0) {
+                                    wait(&p_full[slot], phase);
+                                    tc_fence_after();
+                                }
+                                if (elect_one())
+                                    tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id, k > 0 ? 1u : more);
+                            }
+                            if (release) commit(&empty[at.st]);
+                            at.advance(1);
                         }
-                        if (j < n) {
-                            qk(j & 1, 0, true);
-                            k_done(j);
-                            if (j + 1 == n) commit(q_empty);
-                        }
+                        begun |= 1u << acc;
+                        commit(&o_done[slot]);
                     }
+                    if (s >= 2 && release) vp.advance(jv < n - ahead ? 2 * HV : HV);
+                    if (qk) {
+                        Place at = kp;
+                        const int tile = wide ? slot : 0;
+#pragma unroll
+                        for (int hh = 0; hh < HV; ++hh) {
+                            if (QT == 1) wait(&full[at.st], at.phase);
+                            tc_fence_after();
+                            const uint64_t da = q_desc + ((tile * G::kQTile + hh * (SC / 64) * (128 * 128)) >> 4);
+                            const uint64_t db = k_desc + (at.st * G::kStage >> 4);
+                            const int ks = k_steps - hh * (SC / 16);
+                            auto step = [&](int k) {
+                                constexpr uint32_t kSub = 128 * 128 >> 4;    // 64 columns on
+                                const uint32_t in = (k >> 2) * kSub + (k & 3) * 2;
+                                if (elect_one()) tc_mma_f16(tmem + slot * 128, da + in, db + in, qk_id, k > 0 || hh > 0);
+                            };
+                            if (ks >= SC / 16) {
+#pragma unroll
+                                for (int k = 0; k < SC / 16; ++k) step(k);
+                            } else {
+#pragma unroll 1
+                                for (int k = 0; k < ks; ++k) step(k);
+                            }
+                            if (release) commit(&empty[at.st]);
+                            at.advance(1);
+                        }
+                        commit(&s_full[slot]);
+                    }
+                    if (s < steps && release) kp.advance(jk + 1 < ahead ? HV : 2 * HV);
+                    if (s + 1 == steps) commit(q_empty);
                 }
-                if (n == 0) commit(q_empty);
+                if (steps == 0) commit(q_empty);
                 if (n > 0) kp = vp;                          // the next unit begins behind the last V
             }
             // every MMA has completed before the block gives up its tensor memory
@@ -1007,18 +1051,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     factor = fmaxf(factor, kChunkMinFactor);
                 }
                 float s[128];
-                if (ok) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 32) tc_ld32_async(s_addr + c, s + c);
-#pragma unroll
-                    for (int c = 0; c < 128; c += 32) tc_wait_ld32(s + c);
-                }
+                for (int c = 0; c < 128; c += 32) tc_ld32_async(s_addr + c, s + c);
                 const int key0 = (k0 + j) * kChunkKeys;
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) tc_wait_ld32(s + c);
                 if (key0 + kChunkKeys > all_see) {
                     const int seen = limit - key0;
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= seen) s[c] = -INFINITY;
+                    for (int c = 0; c < 128; c += 32) {
+                        // a bit for each key of 32 that the row sees
+                        const uint32_t bits = seen >= c + 32 ? ~0u : seen <= c ? 0u : (1u << (seen - c)) - 1;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(bits >> i & 1)) s[c + i] = -INFINITY;
+                    }
                 }
                 float top[4];
 #pragma unroll
@@ -1056,23 +1103,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 const uint64_t f2 = pack_f2(factor, factor), c2 = pack_f2(shift, shift);
                 uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < 4; ++c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float x, y;
-                        unpack_f2(fma_f2(pack_f2(s[c + 2 * i], s[c + 2 * i + 1]), f2, c2), x, y);
+                        unpack_f2(fma_f2(pack_f2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), f2, c2), x, y);
                         x = ex2(x);
                         y = ex2(y);
                         p[i] = pack2<C>(x, y);
                         sum[i & 3] = add_f2(sum[i & 3], pack_f2(x, y));
                     }
-                    if (ok) tc_st16(s_addr + c / 2, p);
+                    tc_st16(s_addr + 16 * c, p);
+                    if (c & 1) {
+                        // the product may begin with the first half
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&(c == 1 ? p_half : p_full)[slot]);
+                    }
                 }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[slot]);
                 o_phase ^= 1u << slot;
                 last = slot;
                 float x, y;
@@ -1109,48 +1159,55 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 const float inv = l == 0.f ? 0.f : a.cache.v.scale / l;
                 const uint32_t tok = static_cast<uint32_t>(my_row) / static_cast<uint32_t>(G_), g = my_row - tok * G_;
                 const int64_t out_row = static_cast<int64_t>(u.q0) + tok, head = static_cast<int64_t>(u.h) * G_ + g;
-                T *const out = static_cast<T *>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride;
+                const int64_t place = valid ? out_row * a.out.token_stride + head * a.out.head_stride : -1;
                 const bool guard = s_bad[ordinal & 3] == ordinal;            // values of V that are not finite were left out
                 // merged: each warpgroup takes half of the columns
                 const int c0 = merge ? w * (DP / 2) : 0, c1 = merge ? c0 + DP / 2 : DP;
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 16) {
+                for (int c = c0; c < c1; c += 32) {
                     if (c >= D) break;
-                    uint32_t o[16];
+                    float o[32];
                     if (some) {
-                        tc_ld16(lanes + G::kTmemO + (merge ? 0 : acc * 128) + c, o);
+                        tc_ld32_async(lanes + G::kTmemO + (merge ? 0 : acc * 128) + c, o);
+                        tc_wait_ld32(o);
                         if (merge && n > 1) {
-                            uint32_t o1[16];
-                            tc_ld16(lanes + G::kTmemO + 128 + c, o1);
+                            float o1[32];
+                            tc_ld32_async(lanes + G::kTmemO + 128 + c, o1);
+                            tc_wait_ld32(o1);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * w0 + __uint_as_float(o1[i]) * w1);
+                            for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = 0;
+                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
                     }
                     if (guard) {
                         const uint32_t mask = valid ? not_finite_seen<T, FP8>(a, u, limit, c) : 0;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (mask >> i & 1) o[i] = 0x7FC00000u;
+                        for (int i = 0; i < 32; ++i)
+                            if (mask >> i & 1) o[i] = __int_as_float(0x7FC00000);
                         __syncwarp();
                     }
                     if (cut) {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            piece[((c + i) >> 2) * 128 + row] = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
-                                                                            __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-                    } else if (valid) {
+                        for (int i = 0; i < 32; i += 4)
+                            piece[((c + i) >> 2) * 128 + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    } else {
+                        // 4 chunks of 8 columns of 4 rows change places among 4 lanes, so that a
+                        // store of the warp touches 8 rows, not 32 (whose lines were what it
+                        // took its time with)
+                        uint32_t r[16];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 8)
-                            if (c + i < D) {
-                                float f[8];
+                        for (int i = 0; i < 16; ++i) r[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
+                        transpose_chunks(r, lane);
+                        const int col = c + 8 * (lane & 3);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(o[i + k]) * inv;
-                                store_elems<T, 8>(out + c + i, f);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const int64_t to = __shfl_xor_sync(~0u, place, i);
+                            if (to >= 0 && col < D)
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out.data) + to + col) =
+                                    make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                        }
                     }
                 }
                 if (!merge || w == 0) {
