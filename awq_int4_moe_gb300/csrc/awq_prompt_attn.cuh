@@ -63,6 +63,7 @@ constexpr float kChunkLn2 = 0.6931471805599453f;
 constexpr int kPiece = 4;              // key tiles: cuts of a unit are multiples of it
 constexpr int kMmaWarp = 8, kUnitWarp = 9, kLoaderWarp = 10, kLoaders = 64, kChunkThreads = 384;
 constexpr int kUnits = 3;              // units in shared memory
+constexpr int kWaitTries = 1 << 18;    // 1 to 2 s
 
 template <int DP, bool FP8>
 struct ChunkGeo {
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     int64_t *const s_first_at = reinterpret_cast<int64_t *>(smem + G::oMisc + 8);
     int *const s_bad = reinterpret_cast<int *>(smem + G::oMisc + 16);        // [4]
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
     const int D = a.cache.head_dim;
     if (smem_u32(smem) & 1023) {                 // (the tiles' swizzle needs it)
         if (tid == 0) set_status(a.status, AWQ_ERR_CUDA);
@@ -582,12 +583,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         __syncthreads();
     }
     const uint32_t tmem = *tmem_slot;
+    // Waits give up after kWaitTries suspensions of some microseconds each; what a
+    // role does after that is harmless and ends soon, as it waits no more. The status
+    // is set once, at the end.
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait_bounded(bar, parity, a.timeout_ns)) {
-            set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
-            ok = false;
-        }
+        if (!ok || mbar_try_wait(bar, parity)) return;
+        int left = kWaitTries;
+#pragma unroll 1
+        while (!mbar_try_wait_sleep(bar, parity, 20000))
+            if (--left == 0) {
+                ok = false;
+                break;
+            }
     };
     // The role's next unit (the ordinal-th, from 1) in shared memory; NULL after the
     // last one. It is given back, by one thread of each warp, with done_with().
@@ -914,37 +922,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 wait(q_full, (ordinal - 1) & 1);
                 fence_proxy_async();
                 tc_fence_after();
-                auto full_at = [&](Place at) {
-#pragma unroll
-                    for (int hh = 0; hh < HV; ++hh) {
-                        wait(&full[at.st], at.phase);
-                        at.advance(1);
-                    }
-                };
-                // Step s: P V of step s - 2, then S = Q K' of step s, in slot s mod 2. (One
-                // loop and one copy of the code of each: code that does not stay in the
-                // instruction cache takes longer than what it does.)
+                // Step s: P V of step s - 2, then S = Q K' of step s, in slot s mod 2. A
+                // barrier's answer takes 100 cycles, which only a few MMAs can wait behind
+                // the tensor core: each is asked some MMAs ahead, and waited for only where
+                // the answer was no. (One loop and one copy of the code of each product.)
                 uint32_t begun = 0;                          // accumulators that hold something
+                bool got_p = false, got_v = false, got_k = false;
 #pragma unroll 1
                 for (int s = 0; s < steps + 2; ++s) {
                     const int slot = s & 1, jv = wide ? (s - 2) >> 1 : s - 2, jk = wide ? s >> 1 : s;
                     const bool skip_v = wide && slot == 0 && jv >= n0, skip_k = wide && slot == 0 && jk >= n0;
                     const bool pv = s >= 2 && !skip_v, qk = s < steps && !skip_k;
                     const bool release = !wide || slot;      // a tile's last use
-                    // Stages are waited for before the weights, so that the two products
-                    // follow each other without a pause; at a tile's first use.
-                    if (QT == 2 && pv && (!wide || slot == 0 || jv >= n0)) full_at(vp);
-                    if (QT == 2 && qk && (!wide || slot == 0 || jk >= n0)) full_at(kp);
+                    const bool first_k = !wide || slot == 0 || jk >= n0;
                     if (pv) {
                         const uint32_t phase = p_phase >> slot & 1;
                         p_phase ^= 1u << slot;
                         const int acc = QT == 2 ? slot : 0;
-                        wait(&p_half[slot], phase);
+                        if (QT == 2 && !got_v && (!wide || slot == 0 || jv >= n0)) wait(&full[vp.st], vp.phase);
+                        if (!got_p) wait(&p_half[slot], phase);
+                        tc_fence_after();
+                        const bool got_full = mbar_try_wait(&p_full[slot], phase);
                         Place at = vp;
 #pragma unroll
                         for (int hh = 0; hh < HV; ++hh) {
                             if (QT == 1) wait(&full[at.st], at.phase);
-                            tc_fence_after();
                             const int cols = min(SC, k_steps * 16 - hh * SC);
                             const uint64_t db = v_desc + (at.st * G::kStage >> 4);
                             const uint32_t id = chunk_idesc(cols, kBf16, false, true), d = tmem + G::kTmemO + acc * 128 + hh * 128;
@@ -952,8 +954,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
 #pragma unroll
                             for (int k = 0; k < kChunkKeys / 16; ++k) {
                                 if (k == kChunkKeys / 32 && hh == 0) {
-                                    wait(&p_full[slot], phase);
+                                    if (!got_full) wait(&p_full[slot], phase);
                                     tc_fence_after();
+                                    if (QT == 2 && qk && first_k) got_k = mbar_try_wait(&full[kp.st], kp.phase);
                                 }
                                 if (elect_one())
                                     tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id, k > 0 ? 1u : more);
@@ -962,16 +965,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                             at.advance(1);
                         }
                         begun |= 1u << acc;
-                        commit(&o_done[slot]);
+                        // (with a slot for each accumulator, S of step s + 2 is behind it)
+                        if (QT == 1 || (wide ? jv + 1 == (slot ? n : n0) : s >= steps)) commit(&o_done[slot]);
                     }
                     if (s >= 2 && release) vp.advance(jv < n - ahead ? 2 * HV : HV);
+                    got_p = got_v = false;
+                    if (s >= 1 && s < steps + 1) {           // the next step's weights and V
+                        const bool skip = wide && slot == 1 && (s - 1) >> 1 >= n0;
+                        if (!skip) got_p = mbar_try_wait(&p_half[slot ^ 1], p_phase >> (slot ^ 1) & 1);
+                        if (QT == 2 && release) got_v = mbar_try_wait(&full[vp.st], vp.phase);
+                    }
                     if (qk) {
                         Place at = kp;
                         const int tile = wide ? slot : 0;
+                        if (QT == 2 && !got_k && first_k) wait(&full[at.st], at.phase);
 #pragma unroll
                         for (int hh = 0; hh < HV; ++hh) {
                             if (QT == 1) wait(&full[at.st], at.phase);
-                            tc_fence_after();
                             const uint64_t da = q_desc + ((tile * G::kQTile + hh * (SC / 64) * (128 * 128)) >> 4);
                             const uint64_t db = k_desc + (at.st * G::kStage >> 4);
                             const int ks = k_steps - hh * (SC / 16);
@@ -987,11 +997,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
 #pragma unroll 1
                                 for (int k = 0; k < ks; ++k) step(k);
                             }
+                            if (hh == HV - 1) commit(&s_full[slot]);
                             if (release) commit(&empty[at.st]);
                             at.advance(1);
                         }
-                        commit(&s_full[slot]);
                     }
+                    got_k = false;
                     if (s < steps && release) kp.advance(jk + 1 < ahead ? HV : 2 * HV);
                     if (s + 1 == steps) commit(q_empty);
                 }
@@ -1082,10 +1093,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     m = raise ? t : m;
                     l *= by;
                     if (!first) {
-                        // O so far: behind the product of the step before
-                        wait(&o_done[last], (o_phase >> last & 1) ^ 1);
-                        ok = __all_sync(~0u, ok);
-                        tc_fence_after();
+                        // O so far is behind the product of the step before
+                        if (QT == 1) {
+                            wait(&o_done[last], (o_phase >> last & 1) ^ 1);
+                            ok = __all_sync(~0u, ok);
+                            tc_fence_after();
+                        }
                         if (ok) {
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
@@ -1123,7 +1136,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                         if (lane == 0) mbar_arrive(&(c == 1 ? p_half : p_full)[slot]);
                     }
                 }
-                o_phase ^= 1u << slot;
+                if (QT == 1) o_phase ^= 1u << slot;
                 last = slot;
                 float x, y;
                 unpack_f2(add_f2(add_f2(sum[0], sum[1]), add_f2(sum[2], sum[3])), x, y);
@@ -1134,6 +1147,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             const bool valid = in_unit < u.rows, cut = u.cut();
             const int my_row = u.row0 + (valid ? in_unit : u.rows - 1), G_ = a.group;
             if (!first) {
+                if (QT == 2) o_phase ^= 1u << last;
                 wait(&o_done[last], (o_phase >> last & 1) ^ 1);
                 ok = __all_sync(~0u, ok);
             }
@@ -1316,6 +1330,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             }
         }
     }
+    if (!ok) set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
