@@ -26,8 +26,8 @@
 //   heads larger than 128: one warpgroup, its score tile double-buffered.
 // Tensor memory: S (and P over it, 16 bits) 2 x 128 columns, O 2 x 128 or 256.
 //
-// Warps: 0-7 softmax and output, a thread per row; 8 issues the MMAs; 9 finds the
-// units; 10-11 load (Q, then K and V tiles of 128 keys x 128 columns, 128-byte
+// Warps: 0-7 softmax and output, a thread per row; 8-9 issue the MMAs of a slot
+// each; 10-11 find the units and load (Q, then K and V tiles of 128 keys x 128 columns, 128-byte
 // swizzle, by cp.async, 16 bytes a thread, so that any page size and stride will
 // do; e4m3 tiles come as codes first and are expanded to fp16 in shared memory).
 // They meet at mbarriers, every wait is bounded. Registers go where the scores are
@@ -61,7 +61,7 @@ constexpr float kChunkRaiseF16 = 7.f;
 constexpr float kChunkMinFactor = 1.17549435e-38f;
 constexpr float kChunkLn2 = 0.6931471805599453f;
 constexpr int kPiece = 4;              // key tiles: cuts of a unit are multiples of it
-constexpr int kMmaWarp = 8, kUnitWarp = 9, kLoaderWarp = 10, kLoaders = 64, kChunkThreads = 384;
+constexpr int kMmaWarp = 8, kLoaderWarp = 10, kLoaders = 64, kChunkThreads = 384;
 constexpr int kUnits = 3;              // units in shared memory
 constexpr int kWaitTries = 1 << 18;    // 1 to 2 s
 
@@ -80,7 +80,7 @@ struct ChunkGeo {
     // after Q and the stages: maxima and sums that two slots exchange, rows' powers of two, barriers
     static constexpr int oStages = kQ, oRaw = oStages + kStages * kStage, oMl = oRaw + kRaw * kStage / 2, oExp = oMl + 2 * 128 * 8,
                          oUnits = oExp + 2 * 256, oBars = oUnits + kUnits * 64,
-                         kRawBars = FP8 ? kRaw : 1, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 2 + 2 * kUnits + 2 * kRawBars, oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
+                         kRawBars = FP8 ? kRaw : 1, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 3 + 2 * kUnits + 2 * kRawBars, oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
     static constexpr uint32_t kTmemO = 256;                 // first column of O; S at 0 and 128
     static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
@@ -493,8 +493,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     uint64_t *const p_full = p_half + 2;         // [2]
     uint64_t *const o_done = p_full + 2;         // [2]
     uint64_t *const drain = o_done + 2;
-    uint64_t *const both = drain + 1;                                        // both softmax warpgroups
-    uint64_t *const u_full = drain + 2, *const u_empty = u_full + kUnits;    // [kUnits]
+    uint64_t *const both = drain + 2;                                        // both softmax warpgroups
+    uint64_t *const u_full = drain + 3, *const u_empty = u_full + kUnits;    // [kUnits]
     uint64_t *const raw_full = u_empty + kUnits, *const raw_empty = raw_full + G::kRawBars;   // codes; one for guarded tiles
     Unit *const s_unit = reinterpret_cast<Unit *>(smem + G::oUnits);
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + G::oMisc);
@@ -511,17 +511,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 2);              // the loader's warps
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], QT);            // the issuers
         }
         mbar_init(q_full, kLoaders);
-        mbar_init(q_empty, 1);
+        mbar_init(q_empty, QT);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_half[i], 4);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
-        mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         mbar_init(both, 8);
         for (int i = 0; i < G::kRawBars; ++i) {
             mbar_init(&raw_full[i], FP8 ? 1 : 2);
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         }
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&u_full[i], 1);
-            mbar_init(&u_empty[i], 11);      // 2 loader warps, the MMA issuer, 8 softmax warps
+            mbar_init(&u_empty[i], 10 + QT);     // 2 loader warps, the issuers, 8 softmax warps
         }
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         fence_barrier_init();
@@ -687,8 +687,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 return is_v ? j : j + ahead;
             }
         };
+        // The first warp finds the units, each when it first needs one.
+        Cursor2<R> cursor(a, x0, lw == 0 ? x1 : x0, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0);
+        int made = 0;
         auto next_of = [&](Walk &w) {
-            w.u = next_unit(++w.ordinal);
+            ++w.ordinal;
+            if (lw == 0 && w.ordinal > made) {
+                Unit v;
+                if (!cursor.next(v)) v.b = -1;
+                const int i = made % kUnits;
+                if (made >= kUnits) wait(&u_empty[i], (made / kUnits - 1) & 1);
+                if (lane == 0) {
+                    s_unit[i] = v;
+                    mbar_arrive(&u_full[i]);
+                }
+                ++made;
+            }
+            w.u = next_unit(w.ordinal);
             w.item = 0;
             w.n = w.u ? w.u->k1 - w.u->k0 : 0;
             w.ahead = w.u ? min(QT == 2 && w.u->rows > 128 ? 1 : 2, w.n) : 0;
@@ -734,7 +749,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
 
         Walk to;                                             // the next stage to fill
         uint32_t pos = 0;
-        next_of(to);
         if constexpr (FP8) {
             // Codes first, up to kRaw stages ahead and on into the next units; both warps
             // expand them, a row's 16 codes a thread.
@@ -743,14 +757,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             const uint32_t raw0 = smem_u32(smem + G::oRaw);
             Walk from;                                       // the next stage to copy
             uint32_t copied = 0;
-            if (lw == 0) next_of(from);
+            bool more = true;                                // units to copy from
             // (a unit that is as many ahead as there is room for units would wait for
             // this thread itself)
             auto copy_next = [&]() {
                 while (from.item == 2 * HV * from.n) {
                     if (from.ordinal + 1 >= to.ordinal + kUnits) return false;
                     next_of(from);
-                    if (!from.u) return false;
+                    more = from.u;
+                    if (!more) return false;
                 }
                 bool is_v;
                 const int key0 = (from.u->k0 + from.tile(is_v)) * kChunkKeys;
@@ -761,11 +776,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 ++copied;
                 return true;
             };
-            while (to.u) {
+            while (true) {
+                next_of(to);
+                if (!to.u) break;
                 load_q(*to.u, to.ordinal);
                 for (; to.item < 2 * HV * to.n; ++to.item, ++pos) {
                     if (lw == 0)
-                        while (from.u && copied - pos < G::kRaw && copy_next());
+                        while (more && copied - pos < G::kRaw && copy_next());
                     bool is_v;
                     const int key0 = (to.u->k0 + to.tile(is_v)) * kChunkKeys;
                     // a V tile that some row of the unit does not see in full: values
@@ -811,14 +828,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 }
                 __syncwarp();
                 if (lane == 0) done_with(to.ordinal);
-                next_of(to);
             }
             if (!ok)                                         // as below
                 for (uint32_t i = copied > G::kRaw ? copied - G::kRaw : 0; i < copied; ++i)
                     mbar_wait_bounded(&raw_full[i % G::kRaw], i / G::kRaw & 1, a.timeout_ns);
         } else {
             uint32_t guarded = 0;
-            while (to.u) {
+            while (true) {
+                next_of(to);
+                if (!to.u) break;
                 const Unit &u = *to.u;
                 for (;; ++to.item, ++pos) {
                     if (to.item == min(HV, 2 * HV * to.n)) load_q(u, to.ordinal);    // behind K's first tile, which has room earlier
@@ -859,7 +877,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 }
                 __syncwarp();
                 if (lane == 0) done_with(to.ordinal);
-                next_of(to);
             }
         }
         cp_async_commit();
@@ -868,27 +885,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         if (!ok)
             for (uint32_t i = pos > NST ? pos - NST : 0; i < pos; ++i) mbar_wait_bounded(&full[i % NST], i / NST & 1, a.timeout_ns);
     } else if (warp >= kMmaWarp) {
-        // ------------------------------------------------------- units, MMA issuer
+        // ------------------------------------------------------- MMA issuers
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == kUnitWarp && lane == 0) {
-            // ---- the units, one after another
-            Cursor2<R> cursor(a, x0, x1, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0);
-            bool more = true;
-            for (int i = 0; more; ++i) {
-                Unit u;
-                more = cursor.next(u);
-                if (!more) u.b = -1;
-                if (i >= kUnits) wait(&u_empty[i % kUnits], (i / kUnits - 1) & 1);
-                if (!ok) break;
-                s_unit[i % kUnits] = u;
-                mbar_arrive(&u_full[i % kUnits]);
-            }
-        }
-        if (warp == kMmaWarp) {
-            // The issuing warp's own instructions are on the path of every tile: all its
-            // lanes run them, so that descriptors stay in uniform registers (with one
-            // lane in a branch of its own an MMA took 90 cycles to issue), places in the
-            // ring advance without divisions, and one elected lane issues.
+        // A warp for each slot: what a warp does between its MMAs (a barrier's answer
+        // takes 100 cycles, a commit 50) is hidden behind the other's. All lanes run
+        // the code, one elected lane issues, places in the ring advance without
+        // divisions.
+        const int me = warp - kMmaWarp;
+        if (me < QT) {
             const int k_steps = (D + 15) / 16;               // of Q K'; times 16: columns of P V
             const uint64_t q_desc = umma_desc_sw128(smem_u32(smem));
             const uint64_t k_desc = umma_desc_sw128(smem_u32(stages)), v_desc = umma_desc_v(smem_u32(stages));
@@ -898,120 +902,144 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 __device__ __forceinline__ void advance(uint32_t by)
                 {
                     st += by;
+#pragma unroll 1
                     while (st >= NST) {
                         st -= NST;
                         phase ^= 1;
                     }
                 }
             };
-            Place kp{0, 0}, vp{0, 0};                        // of the next K and V tile
-            uint32_t p_phase = 0;                            // a bit per slot
-            int ordinal = 0;
             auto commit = [&](uint64_t *bar) {
                 if (elect_one()) tc_commit(bar);
             };
+            Place kp, vp;                                    // of the next K and V tile
+            uint32_t pos = 0;                                // the unit's first stage
+            uint32_t p_phase = 0;                            // a bit per slot
+            // S[slot] = Q[tile] K' and O[acc] (+)= P[slot] V
+            auto qk = [&](int slot, int tile) {
+                Place at = kp;
+#pragma unroll
+                for (int hh = 0; hh < HV; ++hh) {
+                    if (HV > 1) wait(&full[at.st], at.phase);
+                    const uint64_t da = q_desc + ((tile * G::kQTile + hh * (SC / 64) * (128 * 128)) >> 4);
+                    const uint64_t db = k_desc + (at.st * G::kStage >> 4);
+                    const int ks = k_steps - hh * (SC / 16);
+                    auto step = [&](int k) {
+                        constexpr uint32_t kSub = 128 * 128 >> 4;            // 64 columns on
+                        const uint32_t in = (k >> 2) * kSub + (k & 3) * 2;
+                        if (elect_one()) tc_mma_f16(tmem + slot * 128, da + in, db + in, qk_id, k > 0 || hh > 0);
+                    };
+                    if (ks >= SC / 16) {
+#pragma unroll
+                        for (int k = 0; k < SC / 16; ++k) step(k);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < ks; ++k) step(k);
+                    }
+                    if (hh == HV - 1) commit(&s_full[slot]);
+                    commit(&empty[at.st]);
+                    at.advance(1);
+                }
+            };
+            auto pv = [&](int slot, int acc, bool more) {
+                const uint32_t phase = p_phase >> slot & 1;
+                p_phase ^= 1u << slot;
+                wait(&p_half[slot], phase);
+                tc_fence_after();
+                Place at = vp;
+#pragma unroll
+                for (int hh = 0; hh < HV; ++hh) {
+                    if (HV > 1) wait(&full[at.st], at.phase);
+                    const int cols = min(SC, k_steps * 16 - hh * SC);
+                    const uint64_t db = v_desc + (at.st * G::kStage >> 4);
+                    const uint32_t id = chunk_idesc(cols, kBf16, false, true), d = tmem + G::kTmemO + acc * 128 + hh * 128;
+#pragma unroll
+                    for (int k = 0; k < kChunkKeys / 16; ++k) {
+                        if (k == kChunkKeys / 32 && hh == 0) {
+                            wait(&p_full[slot], phase);
+                            tc_fence_after();
+                        }
+                        if (elect_one())
+                            tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id, k > 0 || more);
+                    }
+                    commit(&empty[at.st]);
+                    at.advance(1);
+                }
+            };
+            int ordinal = 0;
             while (const Unit *const next = next_unit(ordinal + 1)) {
                 const int n = __shfl_sync(~0u, next->k1 - next->k0, 0);
                 const int n0 = __shfl_sync(~0u, next->n0, 0);        // (the first slot's rows see fewer keys)
                 const bool wide = QT == 2 && __shfl_sync(~0u, next->rows, 0) > 128;
                 ++ordinal;
                 if (lane == 0) done_with(ordinal);
-                const int ahead = wide ? min(1, n) : min(2, n), steps = wide ? 2 * n : n;
-                vp = kp;                                     // the unit's first stage
+                const int ahead = wide ? min(1, n) : min(2, n);
+                kp.st = pos % NST;                           // the unit's first stage
+                kp.phase = pos / NST & 1;
+                vp = kp;
                 vp.advance(ahead * HV);
                 wait(q_full, (ordinal - 1) & 1);
                 fence_proxy_async();
-                tc_fence_after();
-                // Step s: P V of step s - 2, then S = Q K' of step s, in slot s mod 2. A
-                // barrier's answer takes 100 cycles, which only a few MMAs can wait behind
-                // the tensor core: each is asked some MMAs ahead, and waited for only where
-                // the answer was no. (One loop and one copy of the code of each product.)
-                uint32_t begun = 0;                          // accumulators that hold something
-                bool got_p = false, got_v = false, got_k = false;
+                if constexpr (QT == 2) {
+                    // Wide: every tile, the first slot up to n0; narrow: every other. A warp
+                    // waits for all stages in their order, and gives back at once those that
+                    // it has no use for (a stage that it passed over could be two fillings
+                    // ahead of the phase that it waits for).
+                    const int end = me == 0 ? n0 : n;
+                    auto mine = [&](int j) { return wide ? j < end : (j & 1) == me; };
+                    const int last = wide ? end - 1 : n - 1 - ((n - 1 - me) & 1);
+                    auto give_back = [&](Place at) {
+                        if (lane == 0) mbar_arrive(&empty[at.st]);
+                    };
+                    bool more = false;                       // the accumulator holds something
+                    if (last < 0) commit(q_empty);
 #pragma unroll 1
-                for (int s = 0; s < steps + 2; ++s) {
-                    const int slot = s & 1, jv = wide ? (s - 2) >> 1 : s - 2, jk = wide ? s >> 1 : s;
-                    const bool skip_v = wide && slot == 0 && jv >= n0, skip_k = wide && slot == 0 && jk >= n0;
-                    const bool pv = s >= 2 && !skip_v, qk = s < steps && !skip_k;
-                    const bool release = !wide || slot;      // a tile's last use
-                    const bool first_k = !wide || slot == 0 || jk >= n0;
-                    if (pv) {
-                        const uint32_t phase = p_phase >> slot & 1;
-                        p_phase ^= 1u << slot;
-                        const int acc = QT == 2 ? slot : 0;
-                        if (QT == 2 && !got_v && (!wide || slot == 0 || jv >= n0)) wait(&full[vp.st], vp.phase);
-                        if (!got_p) wait(&p_half[slot], phase);
-                        tc_fence_after();
-                        const bool got_full = mbar_try_wait(&p_full[slot], phase);
-                        Place at = vp;
-#pragma unroll
-                        for (int hh = 0; hh < HV; ++hh) {
-                            if (QT == 1) wait(&full[at.st], at.phase);
-                            const int cols = min(SC, k_steps * 16 - hh * SC);
-                            const uint64_t db = v_desc + (at.st * G::kStage >> 4);
-                            const uint32_t id = chunk_idesc(cols, kBf16, false, true), d = tmem + G::kTmemO + acc * 128 + hh * 128;
-                            const uint32_t more = begun >> acc & 1;
-#pragma unroll
-                            for (int k = 0; k < kChunkKeys / 16; ++k) {
-                                if (k == kChunkKeys / 32 && hh == 0) {
-                                    if (!got_full) wait(&p_full[slot], phase);
-                                    tc_fence_after();
-                                    if (QT == 2 && qk && first_k) got_k = mbar_try_wait(&full[kp.st], kp.phase);
-                                }
-                                if (elect_one())
-                                    tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id, k > 0 ? 1u : more);
-                            }
-                            if (release) commit(&empty[at.st]);
-                            at.advance(1);
-                        }
-                        begun |= 1u << acc;
-                        // (with a slot for each accumulator, S of step s + 2 is behind it)
-                        if (QT == 1 || (wide ? jv + 1 == (slot ? n : n0) : s >= steps)) commit(&o_done[slot]);
-                    }
-                    if (s >= 2 && release) vp.advance(jv < n - ahead ? 2 * HV : HV);
-                    got_p = got_v = false;
-                    if (s >= 1 && s < steps + 1) {           // the next step's weights and V
-                        const bool skip = wide && slot == 1 && (s - 1) >> 1 >= n0;
-                        if (!skip) got_p = mbar_try_wait(&p_half[slot ^ 1], p_phase >> (slot ^ 1) & 1);
-                        if (QT == 2 && release) got_v = mbar_try_wait(&full[vp.st], vp.phase);
-                    }
-                    if (qk) {
-                        Place at = kp;
-                        const int tile = wide ? slot : 0;
-                        if (QT == 2 && !got_k && first_k) wait(&full[at.st], at.phase);
-#pragma unroll
-                        for (int hh = 0; hh < HV; ++hh) {
-                            if (QT == 1) wait(&full[at.st], at.phase);
-                            const uint64_t da = q_desc + ((tile * G::kQTile + hh * (SC / 64) * (128 * 128)) >> 4);
-                            const uint64_t db = k_desc + (at.st * G::kStage >> 4);
-                            const int ks = k_steps - hh * (SC / 16);
-                            auto step = [&](int k) {
-                                constexpr uint32_t kSub = 128 * 128 >> 4;    // 64 columns on
-                                const uint32_t in = (k >> 2) * kSub + (k & 3) * 2;
-                                if (elect_one()) tc_mma_f16(tmem + slot * 128, da + in, db + in, qk_id, k > 0 || hh > 0);
-                            };
-                            if (ks >= SC / 16) {
-#pragma unroll
-                                for (int k = 0; k < SC / 16; ++k) step(k);
+                    for (int j = -ahead; j < n; ++j) {
+                        const bool next = j + ahead < n;
+                        if (next) wait(&full[kp.st], kp.phase);
+                        if (j >= 0) {
+                            wait(&full[vp.st], vp.phase);
+                            if (mine(j)) {
+                                pv(me, me, more);
+                                more = true;
+                                if (j == last) commit(&o_done[me]);
                             } else {
-#pragma unroll 1
-                                for (int k = 0; k < ks; ++k) step(k);
+                                give_back(vp);
                             }
-                            if (hh == HV - 1) commit(&s_full[slot]);
-                            if (release) commit(&empty[at.st]);
-                            at.advance(1);
+                            vp.advance(j < n - ahead ? 2 : 1);
+                        }
+                        if (next) {
+                            if (mine(j + ahead)) {
+                                qk(me, wide ? me : 0);
+                                if (j + ahead == last) commit(q_empty);
+                            } else {
+                                give_back(kp);
+                            }
+                            kp.advance(j + 1 < 0 ? 1 : 2);
                         }
                     }
-                    got_k = false;
-                    if (s < steps && release) kp.advance(jk + 1 < ahead ? HV : 2 * HV);
-                    if (s + 1 == steps) commit(q_empty);
+                } else {
+                    // S is double-buffered: P V of tile s - 2, then Q K' of tile s
+#pragma unroll 1
+                    for (int s = 0; s < n + 2; ++s) {
+                        if (s >= 2) {
+                            pv(s & 1, 0, s > 2);
+                            vp.advance(s - 2 < n - ahead ? 2 * HV : HV);
+                            commit(&o_done[s & 1]);
+                        }
+                        if (s < n) {
+                            qk(s & 1, 0);
+                            kp.advance(s + 1 < ahead ? HV : 2 * HV);
+                            if (s + 1 == n) commit(q_empty);
+                        }
+                    }
+                    if (n == 0) commit(q_empty);
                 }
-                if (steps == 0) commit(q_empty);
-                if (n > 0) kp = vp;                          // the next unit begins behind the last V
+                pos += 2 * n * HV;
             }
             // every MMA has completed before the block gives up its tensor memory
-            commit(drain);
-            if (!mbar_wait_bounded(drain, 0, a.timeout_ns)) set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+            commit(&drain[me]);
+            if (!mbar_wait_bounded(&drain[me], 0, a.timeout_ns)) ok = false;
         }
     } else {
         // ------------------------------------------------------- softmax and output
