@@ -2,6 +2,7 @@
 // (nothing is launched on a host-visible error) and the choice of the kernel.
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include "awq_decoder_checks.cuh"
@@ -24,8 +25,27 @@ awq_status chunk_call(ChunkArgs &a, int32_t dtype, float scale, void *workspace,
         !plane_aligned(a.cache.v, elem, 16) || !aligned(a.cu_seqlens, 4) || !aligned(a.seq_lens, 4) ||
         !aligned(a.page_table, 4) || !aligned(a.lse, 4) || !aligned(workspace, 256) || !aligned(a.status, 4))
         return AWQ_ERR_MISALIGNED;
+    // Units are of whole tokens where they can be, so that Q comes in boxes of a
+    // tensor map: of the numbers of tokens that nearly fill one, that with the
+    // fewest boxes of up to 64 rows.
+    const int most_rows = chunk_rows(attn_padded_dim(dim));
+    a.unit_rows = most_rows;
+    const int64_t far = 1ll << 39;
+    if (a.group <= most_rows && (a.q_heads == 1 || (a.q.head_stride > 0 && a.q.head_stride < far)) &&
+        (a.tokens == 1 || (a.q.token_stride > 0 && a.q.token_stride < far))) {
+        int best = INT_MAX;
+        for (int n = most_rows / a.group, least = n - n / 32; n >= least; --n) {
+            int d = std::max(1, 64 / a.group);
+            while (n % d) --d;
+            if (n / d < best) {
+                best = n / d;
+                a.unit_rows = n * a.group;
+                a.q_box = d;
+            }
+        }
+    }
     // rows of a KV head are counted in 32 bits, costs (and products of them) in 64
-    const double G = a.group, rows = static_cast<double>(a.tokens) * G, R = chunk_rows(attn_padded_dim(dim));
+    const double G = a.group, rows = static_cast<double>(a.tokens) * G, R = a.unit_rows;
     if (rows > 0x7fffff00) return AWQ_ERR_UNSUPPORTED_SHAPE;
     const double most = 4.6e18, unit = G * (static_cast<double>(a.max_len) + kChunkUnitCost + a.tokens) + 2 * R;
     if (unit * (a.max_len / 128 + 1) > most || unit * (rows / R + 1) * a.cache.num_heads * a.batch > most)
@@ -34,7 +54,7 @@ awq_status chunk_call(ChunkArgs &a, int32_t dtype, float scale, void *workspace,
     // copies are boxes of keys that lie in one page wherever they begin
     a.box = kChunkKeys;
     while (a.page_table && a.cache.page_size % a.box) a.box /= 2;
-    const int64_t place = a.page_table ? a.cache.page_size : a.tokens, far = 1ll << 39;
+    const int64_t place = a.page_table ? a.cache.page_size : a.tokens;
     for (int i = 0; i < 2; ++i) {
         const awq_kv_plane &p = i ? a.cache.v : a.cache.k;
         if ((place > 1 && p.token_stride == 0) || p.token_stride > far || p.head_stride > far || p.page_stride > far)

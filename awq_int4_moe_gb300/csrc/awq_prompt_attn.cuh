@@ -75,8 +75,8 @@ struct ChunkGeo {
     static constexpr int kStages = (FP8 ? 96 : 160) * 1024 / kStage;
     // e4m3 stages on their way to fp16
     static constexpr int kRaw = FP8 ? 64 * 1024 / (kStage / 2) : 0;
-    static constexpr int kQTile = 128 * DP * 2;             // one row tile of Q
-    static constexpr int kQ = QT * kQTile;
+    static constexpr int kQSub = R * 128;                   // 64 columns of Q
+    static constexpr int kQ = DP / 64 * kQSub;
     // after Q and the stages: maxima and sums that two slots exchange, rows' powers of two, barriers
     static constexpr int oStages = kQ, oRaw = oStages + kStages * kStage, oMl = oRaw + kRaw * kStage / 2, oExp = oMl + 2 * 128 * 8,
                          oUnits = oExp + 2 * 256, oBars = oUnits + kUnits * 64,
@@ -292,7 +292,7 @@ __device__ __forceinline__ int row_limit(int ctx, int row, int group)
 __device__ __forceinline__ int cut_at(int64_t y, int64_t cost, int tiles)
 {
     if (y <= 0) return 0;
-    if (y >= cost) return tiles;
+    if (y >= cost) return tiles;          // (most units are not cut)
     const int k = static_cast<int>(y * tiles / cost) / kPiece * kPiece;
     return tiles - k < kPiece ? tiles : k;
 }
@@ -317,51 +317,46 @@ __device__ __forceinline__ bool sequence_bad(const ChunkArgs &a, int b)
 
 // Costs of a sequence's units for one KV head: unit i costs lin + R (i + 1), in
 // keys times G (so that all sequences count alike); a narrow one by itself half.
-template <int R>
 struct Costs {
     int64_t lin, head;
-    int T;
+    int T, R;
     bool half;
     __device__ __forceinline__ Costs() {}
-    __device__ __forceinline__ Costs(const Sequence &s, int group)
+    __device__ __forceinline__ Costs(const Sequence &s, int group, int unit_rows, bool narrow) : R(unit_rows)
     {
         const int64_t rows = static_cast<int64_t>(s.n) * group;
         T = static_cast<int>((rows + R - 1) / R);
         lin = group * (static_cast<int64_t>(max(s.len - s.n, 0)) + kChunkUnitCost);
-        half = R == 256 && rows <= 128;
+        half = narrow && rows <= 128;
         head = before(T);
     }
     __device__ __forceinline__ int64_t before(int i) const
     {
-        const int64_t c = i * lin + static_cast<int64_t>(R / 2) * i * (i + 1);
+        const int64_t c = i * lin + static_cast<int64_t>(i) * (i + 1) / 2 * R;
         return half ? c / 2 : c;
     }
 };
 
-template <int R>
-struct Cursor2 {
-    const ChunkArgs &a;
-    int64_t x0, x1, at;      // the block's share of the costs; where the unit begins
+// Walks through the units of a block's share [x0, x1) of the costs. Only its place
+// is kept; the sequence is looked at again for each unit.
+template <bool NARROW>
+struct UnitWalk {
+    int64_t x0, x1, at;      // the share; where the next unit begins
     int b, h, t;
-    Sequence s;
-    Costs<R> c;
 
-    __device__ __forceinline__ Cursor2(const ChunkArgs &args, int64_t from, int64_t to, int first, int64_t first_at)
-        : a(args), x0(from), x1(to), at(first_at), b(first), h(0), t(0)
+    __device__ __forceinline__ UnitWalk(const ChunkArgs &a, int64_t from, int64_t to, int first, int64_t first_at)
+        : x0(from), x1(to), at(first_at), b(first), h(0), t(0)
     {
-        s.n = 0;
-        c.T = 0;
         if (x0 >= x1) {
             at = x1;                                    // no share: no units
             return;
         }
-        s = sequence_at(a, b);
-        c = Costs<R>(s, a.group);
-        const int64_t in = x0 - at;
-        h = static_cast<int>(in / c.head);
+        const Costs c(sequence_at(a, b), a.group, a.unit_rows, NARROW);
+        h = static_cast<int>((x0 - at) / c.head);
         at += h * c.head;
         // the last unit that begins at or before x0
         int lo = 0, hi = c.T - 1;
+#pragma unroll 1
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (at + c.before(mid) <= x0) lo = mid;
@@ -371,17 +366,21 @@ struct Cursor2 {
         at += c.before(t);
     }
     // The block's next unit.
-    __device__ __forceinline__ bool next(Unit &u)
+    __device__ __forceinline__ bool next(const ChunkArgs &a, Unit &u)
     {
+#pragma unroll 1
         while (at < x1) {
-            while (t == c.T) {                          // (units remain, as costs do)
+            const Sequence s = sequence_at(a, b);
+            const Costs c(s, a.group, a.unit_rows, NARROW);
+            if (t == c.T) {                             // (units remain, as costs do)
                 t = 0;
-                if (++h < a.cache.num_heads && c.T > 0) continue;
-                h = 0;
-                s = sequence_at(a, ++b);
-                c = Costs<R>(s, a.group);
+                if (++h == a.cache.num_heads || c.T == 0) {
+                    h = 0;
+                    ++b;
+                }
+                continue;
             }
-            const int row0 = t * R, rows = min(R, s.n * a.group - row0), ctx = s.len - s.n;
+            const int row0 = t * a.unit_rows, rows = min(a.unit_rows, s.n * a.group - row0), ctx = s.len - s.n;
             u.at = at;
             u.cost = c.before(t + 1) - c.before(t);
             u.b = b;
@@ -472,6 +471,7 @@ __device__ __forceinline__ int sharing_blocks(const Unit &u, int64_t per, int la
 
 template <typename T, bool FP8, int DP>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                                                                      const __grid_constant__ CUtensorMap map_q,
                                                                       const __grid_constant__ ChunkArgs a)
 {
     using G = ChunkGeo<DP, FP8>;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     constexpr bool kBf16 = std::is_same<C, __nv_bfloat16>::value;
     constexpr bool kScaledQ = FP8 && !std::is_same<T, C>::value;    // bf16 q as fp16 with a power of two taken out
     constexpr float kRaise = kBf16 ? 0.f : kChunkRaiseF16;
-    constexpr int NST = G::kStages, HV = G::HV, SC = G::SC, QT = G::QT, R = G::R;
+    constexpr int NST = G::kStages, HV = G::HV, SC = G::SC, QT = G::QT;
 
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *const stages = smem + G::oStages;
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             mbar_init(&full[i], 2);              // the loader's warps
             mbar_init(&empty[i], QT);            // the issuers
         }
-        mbar_init(q_full, kLoaders);
+        mbar_init(q_full, kScaledQ || !a.q_box ? kLoaders : 1);
         mbar_init(q_empty, QT);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         int64_t mine = 0;
         for (int b = lo; b < hi; ++b) {
             if (blockIdx.x == 0 && sequence_bad(a, b)) set_status(a.status, AWQ_ERR_BAD_INDEX);
-            mine += Costs<R>(sequence_at(a, b), a.group).head * a.cache.num_heads;
+            mine += Costs(sequence_at(a, b), a.group, a.unit_rows, QT == 2).head * a.cache.num_heads;
         }
         int64_t incl = mine;
 #pragma unroll
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         if (x0 < x1 && x0 >= before && x0 < before + mine) {
             int b = lo;
             for (;; ++b) {
-                const int64_t c = Costs<R>(sequence_at(a, b), a.group).head * a.cache.num_heads;
+                const int64_t c = Costs(sequence_at(a, b), a.group, a.unit_rows, QT == 2).head * a.cache.num_heads;
                 if (x0 < before + c) break;
                 before += c;
             }
@@ -614,6 +614,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         // ---- Q of a unit, 16 bytes a thread: RP rows of CH chunks a warp and turn, so a
         // thread's rows are 2 RP apart and its token and head go on by additions.
         auto load_q = [&](const Unit &u, int ordinal) {
+            if (!kScaledQ && a.q_box) {
+                // boxes of whole tokens: units begin with one
+                if (lw) return;
+                if (ordinal > 1) wait(q_empty, (ordinal - 2) & 1);
+                const int rows = a.q_box * a.group, boxes = (u.rows + rows - 1) / rows, all = boxes * ((D + 63) / 64);
+                if (lane == 0) mbar_arrive_expect_tx(q_full, all * rows * 128);
+                __syncwarp();
+                for (int i = lane; i < all; i += 32) {
+                    const int sub = i / boxes, box = i - sub * boxes;
+                    tma_load_3d(smem + sub * G::kQSub + box * rows * 128, &map_q, q_full, sub * 64, u.h * a.group,
+                                u.q0 + u.row0 / a.group + box * a.q_box);
+                }
+                return;
+            }
             constexpr int CH = DP / 8, RP = 32 / CH;
             const int ch = lane % CH, first = lw * RP + lane / CH;
             const bool col = ch * 8 < D, pad = ch * 8 < (D + 15) / 16 * 16;
@@ -624,11 +638,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             const int64_t next_token = a.q.token_stride - static_cast<int64_t>(group) * a.q.head_stride;
             const int64_t turn = (2 * RP / group) * a.q.token_stride + (2 * RP % group) * a.q.head_stride;
             if (ordinal > 1) wait(q_empty, (ordinal - 2) & 1);
-            const int rows = u.rows > 128 ? R : 128;                 // (the rows of a tile are all written)
+            const int rows = u.rows > 128 ? G::R : 128;                 // (the rows of a tile are all written)
 #pragma unroll 4
             for (int r = first; r < rows; r += 2 * RP) {
                 const bool in = r < u.rows && col;
-                const uint32_t dst = smem_u32(smem) + (r >> 7) * G::kQTile + (ch >> 3) * (128 * 128) + sw128_offset(r & 127, ch & 7);
+                const uint32_t dst = smem_u32(smem) + (ch >> 3) * G::kQSub + sw128_offset(r, ch & 7);
                 if constexpr (kScaledQ) {
                     // the row's largest magnitude to [2^14, 2^15)
                     uint4 v = make_uint4(0, 0, 0, 0);
@@ -687,22 +701,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 return is_v ? j : j + ahead;
             }
         };
-        // The first warp finds the units, each when it first needs one.
-        Cursor2<R> cursor(a, x0, lw == 0 ? x1 : x0, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0);
-        int made = 0;
         auto next_of = [&](Walk &w) {
             ++w.ordinal;
-            if (lw == 0 && w.ordinal > made) {
-                Unit v;
-                if (!cursor.next(v)) v.b = -1;
-                const int i = made % kUnits;
-                if (made >= kUnits) wait(&u_empty[i], (made / kUnits - 1) & 1);
-                if (lane == 0) {
-                    s_unit[i] = v;
-                    mbar_arrive(&u_full[i]);
-                }
-                ++made;
-            }
             w.u = next_unit(w.ordinal);
             w.item = 0;
             w.n = w.u ? w.u->k1 - w.u->k0 : 0;
@@ -710,43 +710,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         };
         // Copies this warp's part of a stage: boxes of a.box keys (as many as lie in one
         // page wherever they begin) by a row of the box, from column d0 on; nothing of
-        // boxes past the unit's keys. Its lane 0 arrives at `bar` with their bytes.
-        auto copy = [&](const Unit &u, int key0, bool is_v, int d0, uint32_t dst, int row_bytes, uint64_t *bar, bool part) {
+        // boxes past the unit's keys. Lane i has the i-th box (and every 32nd more); the
+        // page of its first is asked for a stage ahead. Lane 0 arrives at `bar` with the
+        // bytes.
+        const int box = a.box, boxes = kChunkKeys / box;
+        int ahead_page = 0;                                  // the page of the lane's box of the next stage
+        auto page_at = [&](const Unit &u, int key) {         // -1: nothing to copy
+            if (key >= u.keys) return -1;
+            if (!a.page_table) return 0;
+            const int at = a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
+            return a.page_table[u.b * a.table_stride + at];
+        };
+        auto ask = [&](const Walk &w) {
+            bool is_v;
+            ahead_page = lane < boxes ? page_at(*w.u, (w.u->k0 + w.tile(is_v)) * kChunkKeys + lane * box) : -1;
+        };
+        auto copy = [&](Walk &w, uint32_t dst, int row_bytes, int d0, uint64_t *bar, bool part) {
+            const Unit &u = *w.u;
+            bool is_v;
+            const int key0 = (u.k0 + w.tile(is_v)) * kChunkKeys;
             const CUtensorMap *const map = is_v ? &map_v : &map_k;
-            const int box = a.box, boxes = kChunkKeys / box;
-            int page = -1, place = 0;
-            // (of more than 32 boxes, a lane has every 32nd)
-            int count = 0;
-            auto find = [&](int i) {
-                const int key = key0 + i * box;
-                page = -1;
-                if (!part || i >= boxes || key >= u.keys) return;
-                if (a.page_table) {
-                    const int at = a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
-                    page = a.page_table[u.b * a.table_stride + at];
-                    place = key - at * a.cache.page_size;
-                    if (page < 0 || page >= a.cache.num_pages) {
-                        set_status(a.status, AWQ_ERR_BAD_INDEX);
-                        page = -1;
-                    }
-                } else {
-                    page = 0;
-                    place = u.q0 + key;
-                }
+            const int head = a.head_step[is_v] * u.h, step = a.page_step[is_v];
+            int page = ahead_page;
+            ++w.item;
+            if (w.item < 2 * HV * w.n) ask(w);
+            auto good = [&](int p, int key) {
+                if (p >= 0 && p < (a.page_table ? a.cache.num_pages : 1)) return true;
+                if (key < u.keys) set_status(a.status, AWQ_ERR_BAD_INDEX);
+                return false;
             };
-            for (int i = lane; i - lane < boxes; i += 32) {
-                find(i);
-                count += __popc(__ballot_sync(~0u, page >= 0));
-            }
+            bool in = part && lane < boxes && good(page, key0 + lane * box);
+            int count = __popc(__ballot_sync(~0u, in));
+            for (int i = lane + 32; i - lane < boxes; i += 32)
+                count += __popc(__ballot_sync(~0u, part && good(page_at(u, key0 + i * box), key0 + i * box)));
             if (lane == 0) mbar_arrive_expect_tx(bar, count * box * row_bytes);
             __syncwarp();
             for (int i = lane; i - lane < boxes; i += 32) {
-                if (boxes > 32) find(i);
-                if (page >= 0)
-                    tma_load_4d(dst + i * box * row_bytes, map, bar, d0, place, a.head_step[is_v] * u.h, a.page_step[is_v] * page);
+                const int key = key0 + i * box;
+                if (i >= 32) {
+                    page = page_at(u, key);
+                    in = part && good(page, key);
+                }
+                if (!in) continue;
+                const int at = !a.page_table ? 0 : a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
+                const int place = a.page_table ? key - at * a.cache.page_size : u.q0 + key;
+                tma_load_4d(dst + i * box * row_bytes, map, bar, d0, place, head, step * page);
             }
         };
-
         Walk to;                                             // the next stage to fill
         uint32_t pos = 0;
         if constexpr (FP8) {
@@ -758,21 +768,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             Walk from;                                       // the next stage to copy
             uint32_t copied = 0;
             bool more = true;                                // units to copy from
-            // (a unit that is as many ahead as there is room for units would wait for
-            // this thread itself)
+            // (no wait for the unit after: it is found once the stages of this one are there)
             auto copy_next = [&]() {
                 while (from.item == 2 * HV * from.n) {
-                    if (from.ordinal + 1 >= to.ordinal + kUnits) return false;
+                    if (from.ordinal > to.ordinal) return false;
+                    const int i = from.ordinal % kUnits;
+                    if (from.ordinal == to.ordinal && !__all_sync(~0u, mbar_try_wait(&u_full[i], from.ordinal / kUnits & 1))) return false;
                     next_of(from);
                     more = from.u;
                     if (!more) return false;
                 }
-                bool is_v;
-                const int key0 = (from.u->k0 + from.tile(is_v)) * kChunkKeys;
                 const uint32_t i = copied % G::kRaw;
+                if (from.item == 0) ask(from);
                 if (copied >= G::kRaw) wait(&raw_empty[i], (copied / G::kRaw - 1) & 1);
-                copy(*from.u, key0, is_v, from.item % HV * SC, raw0 + i * (G::kStage / 2), SC, &raw_full[i], true);
-                ++from.item;
+                copy(from, raw0 + i * (G::kStage / 2), SC, from.item % HV * SC, &raw_full[i], true);
                 ++copied;
                 return true;
             };
@@ -838,7 +847,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 next_of(to);
                 if (!to.u) break;
                 const Unit &u = *to.u;
-                for (;; ++to.item, ++pos) {
+                if (to.n) ask(to);
+                for (;; ++pos) {
                     if (to.item == min(HV, 2 * HV * to.n)) load_q(u, to.ordinal);    // behind K's first tile, which has room earlier
                     if (to.item == 2 * HV * to.n) break;
                     bool is_v;
@@ -847,7 +857,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     const uint32_t st = pos % NST, tile = smem_u32(stages) + st * G::kStage;
                     if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
                     // a warp copies 64 columns
-                    copy(u, key0, is_v, d0, tile + lw * (kChunkKeys * 128), 128, guard ? raw_full : &full[st], lw * 64 < SC && d0 < D);
+                    copy(to, tile + lw * (kChunkKeys * 128), 128, d0, guard ? raw_full : &full[st], lw * 64 < SC && d0 < D);
                     if (guard) {
                         wait(raw_full, guarded);
                         guarded ^= 1;
@@ -890,8 +900,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         // A warp for each slot: what a warp does between its MMAs (a barrier's answer
         // takes 100 cycles, a commit 50) is hidden behind the other's. All lanes run
         // the code, one elected lane issues, places in the ring advance without
-        // divisions.
+        // divisions. The second one finds the units as well, each while the one
+        // before is at work.
         const int me = warp - kMmaWarp;
+        UnitWalk<QT == 2> walk(a, x0, me ? x1 : x0, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0);
+        int made = 0;
+        bool all_made = me == 0;
+        auto make = [&]() {
+            if (made >= kUnits) wait(&u_empty[made % kUnits], (made / kUnits - 1) & 1);
+            Unit v;
+            if (!walk.next(a, v)) {
+                v.b = -1;
+                all_made = true;
+            }
+            if (lane == 0) {
+                s_unit[made % kUnits] = v;
+                mbar_arrive(&u_full[made % kUnits]);
+            }
+            ++made;
+        };
+#pragma unroll 1
+        while (!all_made && (QT == 1 ? ok : made == 0)) make();
         if (me < QT) {
             const int k_steps = (D + 15) / 16;               // of Q K'; times 16: columns of P V
             const uint64_t q_desc = umma_desc_sw128(smem_u32(smem));
@@ -921,23 +950,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
 #pragma unroll
                 for (int hh = 0; hh < HV; ++hh) {
                     if (HV > 1) wait(&full[at.st], at.phase);
-                    const uint64_t da = q_desc + ((tile * G::kQTile + hh * (SC / 64) * (128 * 128)) >> 4);
+                    const uint64_t da = q_desc + ((tile * (128 * 128) + hh * (SC / 64) * G::kQSub) >> 4);
                     const uint64_t db = k_desc + (at.st * G::kStage >> 4);
                     const int ks = k_steps - hh * (SC / 16);
                     auto step = [&](int k) {
-                        constexpr uint32_t kSub = 128 * 128 >> 4;            // 64 columns on
-                        const uint32_t in = (k >> 2) * kSub + (k & 3) * 2;
-                        if (elect_one()) tc_mma_f16(tmem + slot * 128, da + in, db + in, qk_id, k > 0 || hh > 0);
+                        const uint32_t in = (k & 3) * 2, sub = k >> 2;       // 16 columns on, 64 columns on
+                        tc_mma_f16(tmem + slot * 128, da + in + sub * (G::kQSub >> 4), db + in + sub * (128 * 128 >> 4), qk_id,
+                                   k > 0 || hh > 0);
                     };
-                    if (ks >= SC / 16) {
+                    if (elect_one()) {
+                        if (ks >= SC / 16) {
 #pragma unroll
-                        for (int k = 0; k < SC / 16; ++k) step(k);
-                    } else {
+                            for (int k = 0; k < SC / 16; ++k) step(k);
+                        } else {
 #pragma unroll 1
-                        for (int k = 0; k < ks; ++k) step(k);
+                            for (int k = 0; k < ks; ++k) step(k);
+                        }
+                        if (hh == HV - 1) tc_commit(&s_full[slot]);
+                        tc_commit(&empty[at.st]);
                     }
-                    if (hh == HV - 1) commit(&s_full[slot]);
-                    commit(&empty[at.st]);
                     at.advance(1);
                 }
             };
@@ -953,16 +984,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     const int cols = min(SC, k_steps * 16 - hh * SC);
                     const uint64_t db = v_desc + (at.st * G::kStage >> 4);
                     const uint32_t id = chunk_idesc(cols, kBf16, false, true), d = tmem + G::kTmemO + acc * 128 + hh * 128;
+                    constexpr int kHalf = kChunkKeys / 32;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kChunkKeys / 16; ++k) {
-                        if (k == kChunkKeys / 32 && hh == 0) {
-                            wait(&p_full[slot], phase);
-                            tc_fence_after();
-                        }
-                        if (elect_one())
+                        for (int k = 0; k < kHalf; ++k)
                             tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id, k > 0 || more);
                     }
-                    commit(&empty[at.st]);
+                    if (hh == 0) {
+                        wait(&p_full[slot], phase);
+                        tc_fence_after();
+                    }
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = kHalf; k < 2 * kHalf; ++k)
+                            tc_mma_f16_tmem_a(d, tmem + slot * 128 + k * 8, db + k * (2048 >> 4), id, 1);
+                        tc_commit(&empty[at.st]);
+                    }
                     at.advance(1);
                 }
             };
@@ -994,7 +1031,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     bool more = false;                       // the accumulator holds something
                     if (last < 0) commit(q_empty);
 #pragma unroll 1
-                    for (int j = -ahead; j < n; ++j) {
+                    for (int j = -ahead; j <= n; ++j) {
+                        // (the unit after the next would wait for this warp itself)
+                        if (j == min(0, n) && !all_made && made == ordinal) make();
+                        if (j == n) break;
                         const bool next = j + ahead < n;
                         if (next) wait(&full[kp.st], kp.phase);
                         if (j >= 0) {
@@ -1385,12 +1425,21 @@ bool plane_map(CUtensorMap *m, const ChunkArgs &a, const awq_kv_plane &p)
 template <typename T, bool FP8, int DP>
 awq_status launch_chunk_d(const ChunkArgs &a, int sms, cudaStream_t st)
 {
-    CUtensorMap map_k, map_v;
+    CUtensorMap map_k, map_v, map_q{};
     if (!plane_map<FP8, DP>(&map_k, a, a.cache.k) || !plane_map<FP8, DP>(&map_v, a, a.cache.v)) return AWQ_ERR_CUDA;
+    if (a.q_box && !(FP8 && !std::is_same<T, __half>::value)) {
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.cache.head_dim), static_cast<cuuint64_t>(a.q_heads), static_cast<cuuint64_t>(a.tokens)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.q_heads > 1 ? a.q.head_stride * 2 : 16),
+                                       static_cast<cuuint64_t>(a.tokens > 1 ? a.q.token_stride * 2 : 16)};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.group), static_cast<cuuint32_t>(a.q_box)};
+        if (!encode_tensor_map(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, a.q.data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+            return AWQ_ERR_CUDA;
+    }
     const awq_status r = set_smem(chunk_attn_kernel<T, FP8, DP>, ChunkGeo<DP, FP8>::kSmem);
     if (r) return r;
     const int grid = sms < kChunkMaxCtas ? sms : kChunkMaxCtas;
-    return launch_ex(chunk_attn_kernel<T, FP8, DP>, dim3(grid), dim3(kChunkThreads), ChunkGeo<DP, FP8>::kSmem, 1, true, st, map_k, map_v, a);
+    return launch_ex(chunk_attn_kernel<T, FP8, DP>, dim3(grid), dim3(kChunkThreads), ChunkGeo<DP, FP8>::kSmem, 1, true, st, map_k, map_v, map_q, a);
 }
 
 template <typename T, bool FP8>

@@ -24,6 +24,8 @@ struct ChunkArgs {
     uint32_t page_magic;           // as in AttnArgs
     int32_t page_shift;
     int32_t box;                   // keys of one copy: the largest power of two up to 128 that divides a page
+    int32_t unit_rows;             // packed rows of a unit: of whole tokens where one has no more
+    int32_t q_box;                 // tokens of one copy of Q; 0: Q is copied row by row
     int32_t head_step[2], page_step[2];    // of K and V: 0 where the plane's stride is 0, else 1
     float factor;                  // |scale| * log2(e) * K's scale
     int32_t negative;              // the scale is below 0
