@@ -61,12 +61,14 @@ constexpr float kChunkRaiseF16 = 7.f;
 constexpr float kChunkMinFactor = 1.17549435e-38f;
 constexpr float kChunkLn2 = 0.6931471805599453f;
 constexpr int kPiece = 4;              // key tiles: cuts of a unit are multiples of it
-constexpr int kMmaWarp = 8, kLoaderWarp = 10, kLoaders = 64, kChunkThreads = 384;
+constexpr int kMmaWarp = 8, kLoaderWarp = 10;
 constexpr int kUnits = 3;              // units in shared memory
 constexpr int kWaitTries = 1 << 18;    // 1 to 2 s
 
 template <int DP, bool FP8>
 struct ChunkGeo {
+    // e4m3: 10 copies codes, 11 finds the units, 12-15 expand the codes; else 10 and 11 copy
+    static constexpr int kThreads = FP8 ? 512 : 384, kFillWarp = FP8 ? 12 : 10, kFillWarps = FP8 ? 4 : 2;
     static constexpr int QT = DP <= 128 ? 2 : 1;            // row tiles of a unit
     static constexpr int R = 128 * QT;
     static constexpr int SC = DP < 128 ? DP : 128;          // columns of a stage
@@ -470,7 +472,7 @@ __device__ __forceinline__ int sharing_blocks(const Unit &u, int64_t per, int la
 // ----------------------------------------------------------------- the kernel
 
 template <typename T, bool FP8, int DP>
-__global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+__global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                                                       const __grid_constant__ CUtensorMap map_q,
                                                                       const __grid_constant__ ChunkArgs a)
 {
@@ -479,6 +481,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     constexpr bool kBf16 = std::is_same<C, __nv_bfloat16>::value;
     constexpr bool kScaledQ = FP8 && !std::is_same<T, C>::value;    // bf16 q as fp16 with a power of two taken out
     constexpr float kRaise = kBf16 ? 0.f : kChunkRaiseF16;
+    constexpr int kThreads = G::kThreads, FW = G::kFillWarps;
     constexpr int NST = G::kStages, HV = G::HV, SC = G::SC, QT = G::QT;
 
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -510,10 +513,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     }
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&full[i], 2);              // the loader's warps
+            mbar_init(&full[i], FW);
             mbar_init(&empty[i], QT);            // the issuers
         }
-        mbar_init(q_full, kScaledQ || !a.q_box ? kLoaders : 1);
+        mbar_init(q_full, kScaledQ || !a.q_box ? 32 * FW : 1);
         mbar_init(q_empty, QT);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -525,11 +528,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         mbar_init(both, 8);
         for (int i = 0; i < G::kRawBars; ++i) {
             mbar_init(&raw_full[i], FP8 ? 1 : 2);
-            mbar_init(&raw_empty[i], 2);
+            mbar_init(&raw_empty[i], FW);
         }
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&u_full[i], 1);
-            mbar_init(&u_empty[i], 10 + QT);     // 2 loader warps, the issuers, 8 softmax warps
+            mbar_init(&u_empty[i], (FP8 ? 5 : 2) + QT + 8);      // copying and filling, issuers, softmax
         }
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         fence_barrier_init();
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     int64_t x0, x1, per_cta;
     {
         int64_t *const scan = reinterpret_cast<int64_t *>(stages);           // [16], before any tile
-        const int per = (a.batch + kChunkThreads - 1) / kChunkThreads;
+        const int per = (a.batch + kThreads - 1) / kThreads;
         const int lo = min(a.batch, tid * per), hi = min(a.batch, lo + per);
         int64_t mine = 0;
         for (int b = lo; b < hi; ++b) {
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         __syncthreads();
         tc_fence_after();
         int64_t before = incl - mine, total = 0;
-        for (int w = 0; w < kChunkThreads / 32; ++w) {
+        for (int w = 0; w < kThreads / 32; ++w) {
             const int64_t v = scan[w];
             if (w < warp) before += v;
             total += v;
@@ -607,12 +610,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         return ok && v->b >= 0 ? v : nullptr;
     };
     auto done_with = [&](int ordinal) { mbar_arrive(&u_empty[(ordinal - 1) % kUnits]); };
-    if (warp >= kLoaderWarp) {
+    if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP8 ? 56 : 88));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP8 ? 200 : 208));
+    // The units, found one after another.
+    auto make_unit = [&](UnitWalk<QT == 2> &walk, int made) {
+        if (made >= kUnits) wait(&u_empty[made % kUnits], (made / kUnits - 1) & 1);
+        Unit v;
+        const bool found = walk.next(a, v);
+        if (!found) v.b = -1;
+        if (lane == 0) {
+            s_unit[made % kUnits] = v;
+            mbar_arrive(&u_full[made % kUnits]);
+        }
+        return found;
+    };
+    auto first_unit = [&]() { return UnitWalk<QT == 2>(a, x0, x1, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0); };
+
+    if (FP8 && warp == kLoaderWarp + 1) {
+        UnitWalk<QT == 2> walk = first_unit();
+        int made = 0;
+#pragma unroll 1
+        while (make_unit(walk, made) && ok) ++made;
+    } else if (warp >= kLoaderWarp) {
         // ------------------------------------------------------- loader
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        const int lw = warp - kLoaderWarp;
+        const int lw = warp - G::kFillWarp;
         // ---- Q of a unit, 16 bytes a thread: RP rows of CH chunks a warp and turn, so a
-        // thread's rows are 2 RP apart and its token and head go on by additions.
+        // thread's rows are as far apart as the warps reach and its token and head go on by additions.
         auto load_q = [&](const Unit &u, int ordinal) {
             if (!kScaledQ && a.q_box) {
                 // boxes of whole tokens: units begin with one
@@ -629,18 +652,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                 return;
             }
             constexpr int CH = DP / 8, RP = 32 / CH;
-            const int ch = lane % CH, first = lw * RP + lane / CH;
+            const int ch = lane % CH, first = lw * RP + lane / CH, turn_rows = FW * RP;
             const bool col = ch * 8 < D, pad = ch * 8 < (D + 15) / 16 * 16;
             const uint32_t group = a.group, row = u.row0 + first;
             uint32_t g = row % group;
             const T *src = static_cast<const T *>(a.q.data) + (u.q0 + static_cast<int64_t>(row / group)) * a.q.token_stride +
                            (static_cast<int64_t>(u.h) * group + g) * a.q.head_stride + ch * 8;
             const int64_t next_token = a.q.token_stride - static_cast<int64_t>(group) * a.q.head_stride;
-            const int64_t turn = (2 * RP / group) * a.q.token_stride + (2 * RP % group) * a.q.head_stride;
+            const int64_t turn = (turn_rows / group) * a.q.token_stride + (turn_rows % group) * a.q.head_stride;
             if (ordinal > 1) wait(q_empty, (ordinal - 2) & 1);
             const int rows = u.rows > 128 ? G::R : 128;                 // (the rows of a tile are all written)
 #pragma unroll 4
-            for (int r = first; r < rows; r += 2 * RP) {
+            for (int r = first; r < rows; r += turn_rows) {
                 const bool in = r < u.rows && col;
                 const uint32_t dst = smem_u32(smem) + (ch >> 3) * G::kQSub + sw128_offset(r, ch & 7);
                 if constexpr (kScaledQ) {
@@ -669,7 +692,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                     if (pad) cp_async_16_or_zero(dst, in ? src : static_cast<const T *>(a.q.data), in ? 16 : 0);
                 }
                 src += turn;
-                g += 2 * RP % group;
+                g += turn_rows % group;
                 if (g >= group) {
                     g -= group;
                     src += next_token;
@@ -760,87 +783,84 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         Walk to;                                             // the next stage to fill
         uint32_t pos = 0;
         if constexpr (FP8) {
-            // Codes first, up to kRaw stages ahead and on into the next units; both warps
-            // expand them, a row's 16 codes a thread.
+            // One warp copies codes, up to kRaw stages ahead; four expand them, a row's 16
+            // codes a thread.
             constexpr int CH = SC / 16, RP = 32 / CH;
-            const int ch = lane % CH, sub = lane / CH;
             const uint32_t raw0 = smem_u32(smem + G::oRaw);
-            Walk from;                                       // the next stage to copy
-            uint32_t copied = 0;
-            bool more = true;                                // units to copy from
-            // (no wait for the unit after: it is found once the stages of this one are there)
-            auto copy_next = [&]() {
-                while (from.item == 2 * HV * from.n) {
-                    if (from.ordinal > to.ordinal) return false;
-                    const int i = from.ordinal % kUnits;
-                    if (from.ordinal == to.ordinal && !__all_sync(~0u, mbar_try_wait(&u_full[i], from.ordinal / kUnits & 1))) return false;
-                    next_of(from);
-                    more = from.u;
-                    if (!more) return false;
+            if (warp == kLoaderWarp) {
+                while (true) {
+                    next_of(to);
+                    if (!to.u) break;
+                    if (to.n) ask(to);
+#pragma unroll 1
+                    for (; to.item < 2 * HV * to.n; ++pos) {
+                        const uint32_t i = pos % G::kRaw;
+                        if (pos >= G::kRaw) wait(&raw_empty[i], (pos / G::kRaw - 1) & 1);
+                        copy(to, raw0 + i * (G::kStage / 2), SC, to.item % HV * SC, &raw_full[i], true);
+                    }
+                    if (lane == 0) done_with(to.ordinal);
                 }
-                const uint32_t i = copied % G::kRaw;
-                if (from.item == 0) ask(from);
-                if (copied >= G::kRaw) wait(&raw_empty[i], (copied / G::kRaw - 1) & 1);
-                copy(from, raw0 + i * (G::kStage / 2), SC, from.item % HV * SC, &raw_full[i], true);
-                ++copied;
-                return true;
-            };
-            while (true) {
-                next_of(to);
-                if (!to.u) break;
-                load_q(*to.u, to.ordinal);
-                for (; to.item < 2 * HV * to.n; ++to.item, ++pos) {
-                    if (lw == 0)
-                        while (more && copied - pos < G::kRaw && copy_next());
-                    bool is_v;
-                    const int key0 = (to.u->k0 + to.tile(is_v)) * kChunkKeys;
-                    // a V tile that some row of the unit does not see in full: values
-                    // that are not finite would reach it as 0 times themselves
-                    const bool guard = is_v && key0 + kChunkKeys > to.u->all0;
-                    const uint32_t st = pos % NST, tile = smem_u32(stages) + st * G::kStage + (ch >> 2) * (kChunkKeys * 128);
-                    const uint32_t ri = pos % G::kRaw, raw = raw0 + ri * (G::kStage / 2) + lane * 16 + lw * (64 * SC);
-                    if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
-                    wait(&raw_full[ri], pos / G::kRaw & 1);
-                    constexpr int B = 8;                             // loads in flight
+                if (!ok)                                     // as below
+                    for (uint32_t i = pos > G::kRaw ? pos - G::kRaw : 0; i < pos; ++i)
+                        mbar_wait_bounded(&raw_full[i % G::kRaw], i / G::kRaw & 1, a.timeout_ns);
+                pos = 0;
+            } else {
+                const int ch = lane % CH, row = lw * 32 + lane / CH;
+                // Where a row's chunks go: RP rows on, the swizzle changes with their number's
+                // last bits alone. Lanes of the second 64 columns take their two chunks the
+                // other way round, so that no bank is hit twice.
+                const bool turned = ch >> 2;
+                const uint32_t at0 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row, (ch & 3) * 2 + (turned ? 1 : 0));
+                const uint32_t at1 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row + RP, (ch & 3) * 2 + (turned ? 1 : 0));
+                while (true) {
+                    next_of(to);
+                    if (!to.u) break;
+                    load_q(*to.u, to.ordinal);
+#pragma unroll 1
+                    for (; to.item < 2 * HV * to.n; ++to.item, ++pos) {
+                        bool is_v;
+                        const int key0 = (to.u->k0 + to.tile(is_v)) * kChunkKeys;
+                        // a V tile that some row of the unit does not see in full: values
+                        // that are not finite would reach it as 0 times themselves
+                        const bool guard = is_v && key0 + kChunkKeys > to.u->all0;
+                        const uint32_t st = pos % NST, tile = smem_u32(stages) + st * G::kStage;
+                        const uint32_t ri = pos % G::kRaw, raw = raw0 + ri * (G::kStage / 2) + lane * 16 + lw * (32 * SC);
+                        if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
+                        wait(&raw_full[ri], pos / G::kRaw & 1);
+                        constexpr int B = 4;                         // loads in flight
+#pragma unroll 1
+                        for (int p0 = 0; p0 < 32 / RP; p0 += B) {
+                            uint4 v[B];
 #pragma unroll
-                    for (int p0 = 0; p0 < 64 / RP; p0 += B) {
-                        uint4 v[B];
+                            for (int i = 0; i < B; ++i) v[i] = lds_v4(raw + (p0 + i) * 512);
 #pragma unroll
-                        for (int i = 0; i < B; ++i) v[i] = lds_v4(raw + (p0 + i) * 512);
-#pragma unroll
-                        for (int i = 0; i < B; ++i) {
-                            uint32_t w[8];
-                            e4m3x4_f16x4(v[i].x, w[0], w[1]);
-                            e4m3x4_f16x4(v[i].y, w[2], w[3]);
-                            e4m3x4_f16x4(v[i].z, w[4], w[5]);
-                            e4m3x4_f16x4(v[i].w, w[6], w[7]);
-                            uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
-                            if (guard && (not_finite4<C>(lo) | not_finite4<C>(hi))) {
-                                s_bad[to.ordinal & 3] = to.ordinal;
-                                lo = make_uint4(finite_pair<C>(w[0]), finite_pair<C>(w[1]), finite_pair<C>(w[2]), finite_pair<C>(w[3]));
-                                hi = make_uint4(finite_pair<C>(w[4]), finite_pair<C>(w[5]), finite_pair<C>(w[6]), finite_pair<C>(w[7]));
+                            for (int i = 0; i < B; ++i) {
+                                uint4 lo, hi;
+                                e4m3x4_f16x4(v[i].x, lo.x, lo.y);
+                                e4m3x4_f16x4(v[i].y, lo.z, lo.w);
+                                e4m3x4_f16x4(v[i].z, hi.x, hi.y);
+                                e4m3x4_f16x4(v[i].w, hi.z, hi.w);
+                                if (guard && (not_finite4<C>(lo) | not_finite4<C>(hi))) {
+                                    s_bad[to.ordinal & 3] = to.ordinal;
+                                    lo = make_uint4(finite_pair<C>(lo.x), finite_pair<C>(lo.y), finite_pair<C>(lo.z), finite_pair<C>(lo.w));
+                                    hi = make_uint4(finite_pair<C>(hi.x), finite_pair<C>(hi.y), finite_pair<C>(hi.z), finite_pair<C>(hi.w));
+                                }
+                                const uint32_t at = tile + (RP == 4 && i & 1 ? at1 + (p0 + i - 1) * (RP * 128) : at0 + (p0 + i) * (RP * 128));
+                                sts_v4(at, turned ? hi : lo);
+                                sts_v4(at ^ 16, turned ? lo : hi);
                             }
-                            // lanes of the second 64 columns take their chunks the other way
-                            // round, so that no bank is hit twice
-                            const int r = lw * 64 + (p0 + i) * RP + sub;
-                            const bool turned = ch >> 2;
-                            sts_v4(tile + sw128_offset(r, (ch & 3) * 2 + (turned ? 1 : 0)), turned ? hi : lo);
-                            sts_v4(tile + sw128_offset(r, (ch & 3) * 2 + (turned ? 0 : 1)), turned ? lo : hi);
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&raw_empty[ri]);
+                            mbar_arrive(&full[st]);
                         }
                     }
-                    fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&raw_empty[ri]);
-                        mbar_arrive(&full[st]);
-                    }
+                    if (lane == 0) done_with(to.ordinal);
                 }
-                __syncwarp();
-                if (lane == 0) done_with(to.ordinal);
             }
-            if (!ok)                                         // as below
-                for (uint32_t i = copied > G::kRaw ? copied - G::kRaw : 0; i < copied; ++i)
-                    mbar_wait_bounded(&raw_full[i % G::kRaw], i / G::kRaw & 1, a.timeout_ns);
         } else {
             uint32_t guarded = 0;
             while (true) {
@@ -896,31 +916,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             for (uint32_t i = pos > NST ? pos - NST : 0; i < pos; ++i) mbar_wait_bounded(&full[i % NST], i / NST & 1, a.timeout_ns);
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------- MMA issuers
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // A warp for each slot: what a warp does between its MMAs (a barrier's answer
         // takes 100 cycles, a commit 50) is hidden behind the other's. All lanes run
         // the code, one elected lane issues, places in the ring advance without
         // divisions. The second one finds the units as well, each while the one
         // before is at work.
         const int me = warp - kMmaWarp;
-        UnitWalk<QT == 2> walk(a, x0, me ? x1 : x0, x0 < x1 ? *s_first : 0, x0 < x1 ? *s_first_at : 0);
+        // (not with e4m3, where a warp of its own does)
+        constexpr bool kFinds = !FP8;
         int made = 0;
-        bool all_made = me == 0;
-        auto make = [&]() {
-            if (made >= kUnits) wait(&u_empty[made % kUnits], (made / kUnits - 1) & 1);
-            Unit v;
-            if (!walk.next(a, v)) {
-                v.b = -1;
-                all_made = true;
-            }
-            if (lane == 0) {
-                s_unit[made % kUnits] = v;
-                mbar_arrive(&u_full[made % kUnits]);
-            }
-            ++made;
-        };
+        bool all_made = !kFinds || me == 0;
+        UnitWalk<QT == 2> walk = all_made ? UnitWalk<QT == 2>(a, 0, 0, 0, 0) : first_unit();
 #pragma unroll 1
-        while (!all_made && (QT == 1 ? ok : made == 0)) make();
+        while (!all_made && (QT == 1 ? ok : made == 0)) all_made = !make_unit(walk, made++);
         if (me < QT) {
             const int k_steps = (D + 15) / 16;               // of Q K'; times 16: columns of P V
             const uint64_t q_desc = umma_desc_sw128(smem_u32(smem));
@@ -1033,7 +1041,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
 #pragma unroll 1
                     for (int j = -ahead; j <= n; ++j) {
                         // (the unit after the next would wait for this warp itself)
-                        if (j == min(0, n) && !all_made && made == ordinal) make();
+                        if (kFinds && j == min(0, n) && !all_made && made == ordinal) all_made = !make_unit(walk, made++);
                         if (j == n) break;
                         const bool next = j + ahead < n;
                         if (next) wait(&full[kp.st], kp.phase);
@@ -1083,7 +1091,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         }
     } else {
         // ------------------------------------------------------- softmax and output
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int w = warp >> 2, row = (warp & 3) * 32 + lane;               // this thread's row of a tile
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         uint32_t s_phase = 0, o_phase = 0;                                   // a bit per slot: score tiles, products with V
@@ -1439,7 +1446,7 @@ awq_status launch_chunk_d(const ChunkArgs &a, int sms, cudaStream_t st)
     const awq_status r = set_smem(chunk_attn_kernel<T, FP8, DP>, ChunkGeo<DP, FP8>::kSmem);
     if (r) return r;
     const int grid = sms < kChunkMaxCtas ? sms : kChunkMaxCtas;
-    return launch_ex(chunk_attn_kernel<T, FP8, DP>, dim3(grid), dim3(kChunkThreads), ChunkGeo<DP, FP8>::kSmem, 1, true, st, map_k, map_v, map_q, a);
+    return launch_ex(chunk_attn_kernel<T, FP8, DP>, dim3(grid), dim3(ChunkGeo<DP, FP8>::kThreads), ChunkGeo<DP, FP8>::kSmem, 1, true, st, map_k, map_v, map_q, a);
 }
 
 template <typename T, bool FP8>
