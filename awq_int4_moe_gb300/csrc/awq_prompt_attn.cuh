@@ -242,29 +242,15 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t v)
     return r;
 }
 
-// Of 4 neighbouring lanes l with chunks i (r[4 i] .. r[4 i + 3]): chunk l of lane
-// l ^ i comes to r[4 i].
-__device__ __forceinline__ void transpose_chunks(uint32_t (&r)[16], int lane)
+__device__ __forceinline__ void st_v8(void *p, const uint32_t *r)
 {
-    // chunk i ^ l to place i
-#pragma unroll
-    for (int d = 2; d > 0; d >>= 1) {
-        const bool swap = lane & d;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & d) continue;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t a = r[4 * i + k], b = r[4 * (i ^ d) + k];
-                r[4 * i + k] = swap ? b : a;
-                r[4 * (i ^ d) + k] = swap ? a : b;
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[4 * i + k] = __shfl_xor_sync(~0u, r[4 * i + k], i);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+                 "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void st_v4(void *p, const uint32_t *r)
+{
+    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
 // ------------------------------------------------------------------ the units
@@ -1248,7 +1234,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                 const float inv = l == 0.f ? 0.f : a.cache.v.scale / l;
                 const uint32_t tok = static_cast<uint32_t>(my_row) / static_cast<uint32_t>(G_), g = my_row - tok * G_;
                 const int64_t out_row = static_cast<int64_t>(u.q0) + tok, head = static_cast<int64_t>(u.h) * G_ + g;
-                const int64_t place = valid ? out_row * a.out.token_stride + head * a.out.head_stride : -1;
+                T *const out = static_cast<T *>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride;
+                const bool sectors = __all_sync(~0u, (reinterpret_cast<uintptr_t>(out) & 31) == 0);
                 const bool guard = s_bad[ordinal & 3] == ordinal;            // values of V that are not finite were left out
                 // merged: each warpgroup takes half of the columns
                 const int c0 = merge ? w * (DP / 2) : 0, c1 = merge ? c0 + DP / 2 : DP;
@@ -1282,20 +1269,21 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                         for (int i = 0; i < 32; i += 4)
                             piece[((c + i) >> 2) * 128 + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     } else {
-                        // 4 chunks of 8 columns of 4 rows change places among 4 lanes, so that a
-                        // store of the warp touches 8 rows, not 32 (whose lines were what it
-                        // took its time with)
+                        // 32 bytes of a row a lane: whole sectors, without the rows changing
+                        // lanes (a transposition by shuffles took longer than it saved)
                         uint32_t r[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) r[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
-                        transpose_chunks(r, lane);
-                        const int col = c + 8 * (lane & 3);
+                        if (valid) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int64_t to = __shfl_xor_sync(~0u, place, i);
-                            if (to >= 0 && col < D)
-                                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out.data) + to + col) =
-                                    make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                            for (int i = 0; i < 16; i += 8) {
+                                if (c + 2 * i + 16 <= D && sectors) {
+                                    st_v8(out + c + 2 * i, r + i);
+                                } else {
+                                    if (c + 2 * i < D) st_v4(out + c + 2 * i, r + i);
+                                    if (c + 2 * i + 8 < D) st_v4(out + c + 2 * i + 8, r + i + 4);
+                                }
+                            }
                         }
                     }
                 }
