@@ -60,7 +60,7 @@ constexpr float kChunkRaiseF16 = 7.f;
 // of 0 a masked score of -infinity would be NaN.
 constexpr float kChunkMinFactor = 1.17549435e-38f;
 constexpr float kChunkLn2 = 0.6931471805599453f;
-constexpr int kPiece = 4;              // key tiles: cuts of a unit are multiples of it
+constexpr int kPiece = 8;              // key tiles: cuts of a unit are multiples of it
 constexpr int kMmaWarp = 8, kLoaderWarp = 10;
 constexpr int kUnits = 3;              // units in shared memory
 constexpr int kWaitTries = 1 << 18;    // 1 to 2 s
@@ -1213,8 +1213,17 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                 ok = __all_sync(~0u, ok);
             }
             tc_fence_after();
-            const bool merge = QT == 2 && !wide;
+            const bool merge = QT == 2 && !wide, both_store = QT == 1 || merge;
             float w0 = 1.f, w1 = 0.f;                                        // weights of the two accumulators
+            if (QT == 1) {
+                // the other warpgroup stores half of the columns
+                if (w == 0) s_ml[row] = make_float2(m, l);
+                tc_fence_before();
+                meet();
+                tc_fence_after();
+                m = s_ml[row].x;
+                l = s_ml[row].y;
+            }
             if (merge) {
                 s_ml[w * 128 + row] = make_float2(m, l);
                 tc_fence_before();
@@ -1227,8 +1236,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                 w1 = ex2(y.x - ref);
                 l = x.y * w0 + y.y * w1;
             }
-            if (!idle && ok) {
-                const bool some = merge ? n > 0 : !first;                    // an accumulator holds something
+            if (ok) {
+                const bool some = both_store ? n > 0 : !first;                    // an accumulator holds something
                 float4 *const piece = reinterpret_cast<float4 *>(my_parts + (u.k0 > 0 ? 0 : 1) * chunk_piece_floats(DP) +
                                                                  (wide ? w : 0) * static_cast<int64_t>(chunk_piece_floats(DP) / QT));
                 const float inv = l == 0.f ? 0.f : a.cache.v.scale / l;
@@ -1237,14 +1246,14 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                 T *const out = static_cast<T *>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride;
                 const bool sectors = __all_sync(~0u, (reinterpret_cast<uintptr_t>(out) & 31) == 0);
                 const bool guard = s_bad[ordinal & 3] == ordinal;            // values of V that are not finite were left out
-                // merged: each warpgroup takes half of the columns
-                const int c0 = merge ? w * (DP / 2) : 0, c1 = merge ? c0 + DP / 2 : DP;
+                // one tile of rows: each warpgroup takes half of the columns
+                const int c0 = both_store ? w * (DP / 2) : 0, c1 = both_store ? c0 + DP / 2 : DP;
 #pragma unroll 1
                 for (int c = c0; c < c1; c += 32) {
                     if (c >= D) break;
                     float o[32];
                     if (some) {
-                        tc_ld32_async(lanes + G::kTmemO + (merge ? 0 : acc * 128) + c, o);
+                        tc_ld32_async(lanes + G::kTmemO + (both_store ? 0 : acc * 128) + c, o);
                         tc_wait_ld32(o);
                         if (merge && n > 1) {
                             float o1[32];
@@ -1287,7 +1296,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                         }
                     }
                 }
-                if (!merge || w == 0) {
+                if (!both_store || w == 0) {
                     if (cut) {
                         float *const ml = reinterpret_cast<float *>(piece) + 128 * DP;
                         ml[row] = m == -INFINITY ? m : m - kRaise;
@@ -1297,7 +1306,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                     }
                 }
             }
-            if (merge) {
+            if (both_store) {
                 tc_fence_before();
                 meet();
                 tc_fence_after();
@@ -1349,41 +1358,70 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
             const int rows = v.rows, items = rows * (D / 8);
             const int lo = static_cast<int>(static_cast<int64_t>(items) * me / count);
             const int hi = static_cast<int>(static_cast<int64_t>(items) * (me + 1) / count);
-            for (int item = lo + tid; item < hi; item += 256) {
-                const int chunk = item / rows, r = item - chunk * rows;
-                auto part = [&](int i) {                                     // of the i-th block: r's tile
-                    const int c = list[i];
-                    return a.parts + (static_cast<int64_t>(c) * 2 + (i == 0 ? 1 : 0)) * chunk_piece_floats(DP) +
-                           (r >> 7) * static_cast<int64_t>(chunk_piece_floats(DP) / QT);
-                };
-                float top = -INFINITY;
-                for (int i = 0; i < count; ++i) top = fmaxf(top, __ldcg(part(i) + 128 * DP + (r & 127)));
+            auto part = [&](int i, int r) {                                  // of the i-th block: row r's tile
+                return a.parts + (static_cast<int64_t>(list[i]) * 2 + (i == 0 ? 1 : 0)) * chunk_piece_floats(DP) +
+                       (r >> 7) * static_cast<int64_t>(chunk_piece_floats(DP) / QT);
+            };
+            // the parts' weights, a row a thread (the stages are free by now)
+            float *const weights = reinterpret_cast<float *>(stages);        // [part][256]
+            if (tid < rows) {
+                const int r = tid;
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < count; ++i) top = fmaxf(top, __ldcg(part(i, r) + 128 * DP + (r & 127)));
                 const float ref = top == -INFINITY ? 0.f : top;
-                float sum = 0.f, f[8] = {};
-#pragma unroll 2
+#pragma unroll 4
                 for (int i = 0; i < count; ++i) {
-                    const float *const p = part(i);
-                    const float by = ex2(__ldcg(p + 128 * DP + (r & 127)) - ref);
-                    sum += __ldcg(p + 128 * DP + 128 + (r & 127)) * by;
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p) + 2 * chunk * 128 + (r & 127));
-                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(p) + (2 * chunk + 1) * 128 + (r & 127));
-                    f[0] += x.x * by;
-                    f[1] += x.y * by;
-                    f[2] += x.z * by;
-                    f[3] += x.w * by;
-                    f[4] += y.x * by;
-                    f[5] += y.y * by;
-                    f[6] += y.z * by;
-                    f[7] += y.w * by;
+                    const float *const ml = part(i, r) + 128 * DP + (r & 127);
+                    const float w = ex2(__ldcg(ml) - ref);
+                    weights[i * 256 + r] = w;
+                    sum += __ldcg(ml + 128) * w;
                 }
                 const float inv = sum == 0.f ? 0.f : a.cache.v.scale / sum;
+                for (int i = 0; i < count; ++i) weights[i * 256 + r] *= inv;
+                if (me == 0 && a.lse) {
+                    const uint32_t at = v.row0 + r, tok = at / static_cast<uint32_t>(a.group), g = at - tok * a.group;
+                    a.lse[(static_cast<int64_t>(v.q0) + tok) * a.q_heads + static_cast<int64_t>(v.h) * a.group + g] =
+                        sum == 0.f ? -INFINITY : (top + log2f(sum)) * kChunkLn2;
+                }
+            }
+            meet();
+            constexpr int IT = 4;                                            // items of a thread at a time
+#pragma unroll 1
+            for (int base = lo + tid; base < hi; base += IT * 256) {
+                float f[IT][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] *= inv;
-                const uint32_t at = v.row0 + r, tok = at / static_cast<uint32_t>(a.group), g = at - tok * a.group;
-                const int64_t out_row = static_cast<int64_t>(v.q0) + tok, head = static_cast<int64_t>(v.h) * a.group + g;
-                store_elems<T, 8>(static_cast<T *>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride + 8 * chunk, f);
-                if (chunk == 0 && a.lse)
-                    a.lse[out_row * a.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kChunkLn2;
+                for (int k = 0; k < IT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[k][e] = 0.f;
+#pragma unroll 1
+                for (int i = 0; i < count; ++i) {
+                    float4 x[IT], y[IT];
+#pragma unroll
+                    for (int k = 0; k < IT; ++k) {
+                        const int item = min(base + k * 256, hi - 1), chunk = item / rows, r = item - chunk * rows;
+                        const float4 *const p = reinterpret_cast<const float4 *>(part(i, r)) + 2 * chunk * 128 + (r & 127);
+                        x[k] = __ldcg(p);
+                        y[k] = __ldcg(p + 128);
+                    }
+#pragma unroll
+                    for (int k = 0; k < IT; ++k) {
+                        const int item = min(base + k * 256, hi - 1), r = item % rows;
+                        const float by = weights[i * 256 + r];
+                        const float z[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[k][e] += z[e] * by;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < IT; ++k) {
+                    const int item = base + k * 256;
+                    if (item >= hi) break;
+                    const int chunk = item / rows, r = item - chunk * rows;
+                    const uint32_t at = v.row0 + r, tok = at / static_cast<uint32_t>(a.group), g = at - tok * a.group;
+                    const int64_t out_row = static_cast<int64_t>(v.q0) + tok, head = static_cast<int64_t>(v.h) * a.group + g;
+                    store_elems<T, 8>(static_cast<T *>(a.out.data) + out_row * a.out.token_stride + head * a.out.head_stride + 8 * chunk, f[k]);
+                }
             }
             // the last block to leave makes the counters ready for the next call
             meet();
