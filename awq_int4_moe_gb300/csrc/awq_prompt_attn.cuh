@@ -42,6 +42,7 @@
 // join a part of its rows, in block order, so the same inputs give the same bits.
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "awq_launch.cuh"
@@ -691,105 +692,122 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                 cp_async_arrive_noinc(q_full);
             }
         };
-        // A place in the stages' order: of each unit K 0 .. ahead - 1, then V j, K j +
-        // ahead .. (`ahead` is 1 where both slots use a tile, else 2), a tile's stages
-        // one after another.
-        struct Walk {
-            const Unit *u = nullptr;
-            int ordinal = 0, item = 0, n = 0, ahead = 0;
-            // the tile's number in the unit, and whether it is V's
-            __device__ __forceinline__ int tile(bool &is_v) const
+        // A unit's tiles in the order that they are used up: K 0 .. ahead - 1, then V j, K j
+        // + ahead .. (`ahead` is 1 where both slots use a tile, else 2).
+        struct Tiles {
+            int n, ahead, k, v;                              // tiles; K's and V's so far
+            __device__ __forceinline__ Tiles(const Unit &u)
+                : n(u.k1 - u.k0), ahead(QT == 2 && u.rows > 128 ? 1 : 2), k(0), v(0) {}
+            __device__ __forceinline__ bool more() const { return v < n; }
+            __device__ __forceinline__ bool is_v() const { return k - v == ahead || k == n; }
+            __device__ __forceinline__ int tile() const { return is_v() ? v : k; }
+            __device__ __forceinline__ void next()
             {
-                const int i = item / HV;
-                is_v = false;
-                if (i < ahead) return i;
-                is_v = true;
-                if (i >= ahead + 2 * (n - ahead)) return i - n;
-                const int j = (i - ahead) >> 1;
-                is_v = !((i - ahead) & 1);
-                return is_v ? j : j + ahead;
+                if (is_v()) ++v;
+                else ++k;
             }
         };
-        auto next_of = [&](Walk &w) {
-            ++w.ordinal;
-            w.u = next_unit(w.ordinal);
-            w.item = 0;
-            w.n = w.u ? w.u->k1 - w.u->k0 : 0;
-            w.ahead = w.u ? min(QT == 2 && w.u->rows > 128 ? 1 : 2, w.n) : 0;
+        // A place in a ring: stage and the parity of its filling.
+        struct Ring {
+            uint32_t i = 0, phase = 0;
+            __device__ __forceinline__ void next(uint32_t n)
+            {
+                if (++i == n) {
+                    i = 0;
+                    phase ^= 1;
+                }
+            }
         };
-        // Copies this warp's part of a stage: boxes of a.box keys (as many as lie in one
-        // page wherever they begin) by a row of the box, from column d0 on; nothing of
-        // boxes past the unit's keys. Lane i has the i-th box (and every 32nd more); the
-        // page of its first is asked for a stage ahead. Lane 0 arrives at `bar` with the
-        // bytes.
+        // Copies are boxes of a.box keys, as many as lie in one page wherever they begin;
+        // nothing of boxes past the unit's keys. Lane i has the i-th box of a tile (and
+        // every 32nd more); where it is, is asked for a tile ahead.
         const int box = a.box, boxes = kChunkKeys / box;
-        int ahead_page = 0;                                  // the page of the lane's box of the next stage
-        auto page_at = [&](const Unit &u, int key) {         // -1: nothing to copy
-            if (key >= u.keys) return -1;
-            if (!a.page_table) return 0;
+        auto find = [&](const Unit &u, int key, int &page, int &place) {
+            page = -1;
+            place = 0;
+            if (key >= u.keys) return;
+            if (!a.page_table) {
+                page = 0;
+                place = u.q0 + key;
+                return;
+            }
             const int at = a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
-            return a.page_table[u.b * a.table_stride + at];
+            place = key - at * a.cache.page_size;
+            page = a.page_table[u.b * a.table_stride + at];
+            if (page < 0) page = INT_MIN;                    // (told apart from nothing to copy)
         };
-        auto ask = [&](const Walk &w) {
-            bool is_v;
-            ahead_page = lane < boxes ? page_at(*w.u, (w.u->k0 + w.tile(is_v)) * kChunkKeys + lane * box) : -1;
+        auto usable = [&](int page) {
+            if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.page_table ? a.cache.num_pages : 1)) return true;
+            if (page != -1) set_status(a.status, AWQ_ERR_BAD_INDEX);
+            return false;
         };
-        auto copy = [&](Walk &w, uint32_t dst, int row_bytes, int d0, uint64_t *bar, bool part) {
-            const Unit &u = *w.u;
-            bool is_v;
-            const int key0 = (u.k0 + w.tile(is_v)) * kChunkKeys;
+        int page = -1, place = 0;                            // of the lane's box of the next tile
+        // One stage (from column d0 on) of the tile at key0, whose first boxes are at
+        // `page` and `place`, `in` where they are to be copied. Lane 0 arrives at `bar`
+        // with the bytes.
+        auto copy = [&](const Unit &u, bool is_v, int key0, int page, int place, bool in, int d0, uint32_t dst, int row_bytes, uint64_t *bar) {
             const CUtensorMap *const map = is_v ? &map_v : &map_k;
             const int head = a.head_step[is_v] * u.h, step = a.page_step[is_v];
-            int page = ahead_page;
-            ++w.item;
-            if (w.item < 2 * HV * w.n) ask(w);
-            auto good = [&](int p, int key) {
-                if (p >= 0 && p < (a.page_table ? a.cache.num_pages : 1)) return true;
-                if (key < u.keys) set_status(a.status, AWQ_ERR_BAD_INDEX);
-                return false;
-            };
-            bool in = part && lane < boxes && good(page, key0 + lane * box);
+            const int bytes = box * row_bytes;
             int count = __popc(__ballot_sync(~0u, in));
-            for (int i = lane + 32; i - lane < boxes; i += 32)
-                count += __popc(__ballot_sync(~0u, part && good(page_at(u, key0 + i * box), key0 + i * box)));
-            if (lane == 0) mbar_arrive_expect_tx(bar, count * box * row_bytes);
-            __syncwarp();
-            for (int i = lane; i - lane < boxes; i += 32) {
-                const int key = key0 + i * box;
-                if (i >= 32) {
-                    page = page_at(u, key);
-                    in = part && good(page, key);
+            if (boxes > 32) {                                // small and odd pages
+#pragma unroll 1
+                for (int i = lane + 32; i < boxes; i += 32) {
+                    int pg, pl;
+                    find(u, key0 + i * box, pg, pl);
+                    count += __popc(__ballot_sync(~0u, usable(pg)));
                 }
-                if (!in) continue;
-                const int at = !a.page_table ? 0 : a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
-                const int place = a.page_table ? key - at * a.cache.page_size : u.q0 + key;
-                tma_load_4d(dst + i * box * row_bytes, map, bar, d0, place, head, step * page);
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
+            __syncwarp();
+            if (in) tma_load_4d(dst + lane * bytes, map, bar, d0, place, head, step * page);
+            if (boxes > 32) {
+#pragma unroll 1
+                for (int i = lane + 32; i < boxes; i += 32) {
+                    int pg, pl;
+                    find(u, key0 + i * box, pg, pl);
+                    if (usable(pg)) tma_load_4d(dst + i * bytes, map, bar, d0, pl, head, step * pg);
+                }
             }
         };
-        Walk to;                                             // the next stage to fill
-        uint32_t pos = 0;
+        // a V tile that some row of the unit does not see in full: values that are not
+        // finite would reach it as 0 times themselves
+        auto guarded = [&](const Unit &u, bool is_v, int key0) { return is_v && key0 + kChunkKeys > u.all0; };
+
+        Ring to;                                             // the next stage to fill
+        int ordinal = 0;
         if constexpr (FP8) {
             // One warp copies codes, up to kRaw stages ahead; four expand them, a row's 16
             // codes a thread.
             constexpr int CH = SC / 16, RP = 32 / CH;
             const uint32_t raw0 = smem_u32(smem + G::oRaw);
+            Ring raw;
             if (warp == kLoaderWarp) {
-                while (true) {
-                    next_of(to);
-                    if (!to.u) break;
-                    if (to.n) ask(to);
+                uint32_t copied = 0;
+                while (const Unit *const next = next_unit(++ordinal)) {
+                    const Unit &u = *next;
+                    Tiles t(u);
+                    if (t.more()) find(u, (u.k0 + t.tile()) * kChunkKeys + lane * box, page, place);
 #pragma unroll 1
-                    for (; to.item < 2 * HV * to.n; ++pos) {
-                        const uint32_t i = pos % G::kRaw;
-                        if (pos >= G::kRaw) wait(&raw_empty[i], (pos / G::kRaw - 1) & 1);
-                        copy(to, raw0 + i * (G::kStage / 2), SC, to.item % HV * SC, &raw_full[i], true);
+                    while (t.more()) {
+                        const bool is_v = t.is_v(), in = lane < boxes && usable(page);
+                        const int key0 = (u.k0 + t.tile()) * kChunkKeys, pg = page, pl = place;
+                        t.next();
+                        if (t.more()) find(u, (u.k0 + t.tile()) * kChunkKeys + lane * box, page, place);
+#pragma unroll
+                        for (int hh = 0; hh < HV; ++hh) {
+                            wait(&raw_empty[raw.i], raw.phase ^ 1);
+                            copy(u, is_v, key0, pg, pl, in, hh * SC, raw0 + raw.i * (G::kStage / 2), SC, &raw_full[raw.i]);
+                            raw.next(G::kRaw);
+                            ++copied;
+                        }
                     }
-                    if (lane == 0) done_with(to.ordinal);
+                    __syncwarp();
+                    if (lane == 0) done_with(ordinal);
                 }
                 if (!ok)                                     // as below
-                    for (uint32_t i = pos > G::kRaw ? pos - G::kRaw : 0; i < pos; ++i)
+                    for (uint32_t i = copied > G::kRaw ? copied - G::kRaw : 0; i < copied; ++i)
                         mbar_wait_bounded(&raw_full[i % G::kRaw], i / G::kRaw & 1, a.timeout_ns);
-                pos = 0;
             } else {
                 const int ch = lane % CH, row = lw * 32 + lane / CH;
                 // Where a row's chunks go: RP rows on, the swizzle changes with their number's
@@ -798,108 +816,124 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                 const bool turned = ch >> 2;
                 const uint32_t at0 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row, (ch & 3) * 2 + (turned ? 1 : 0));
                 const uint32_t at1 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row + RP, (ch & 3) * 2 + (turned ? 1 : 0));
-                while (true) {
-                    next_of(to);
-                    if (!to.u) break;
-                    load_q(*to.u, to.ordinal);
+                while (const Unit *const next = next_unit(++ordinal)) {
+                    const Unit &u = *next;
+                    load_q(u, ordinal);
+                    Tiles t(u);
 #pragma unroll 1
-                    for (; to.item < 2 * HV * to.n; ++to.item, ++pos) {
-                        bool is_v;
-                        const int key0 = (to.u->k0 + to.tile(is_v)) * kChunkKeys;
-                        // a V tile that some row of the unit does not see in full: values
-                        // that are not finite would reach it as 0 times themselves
-                        const bool guard = is_v && key0 + kChunkKeys > to.u->all0;
-                        const uint32_t st = pos % NST, tile = smem_u32(stages) + st * G::kStage;
-                        const uint32_t ri = pos % G::kRaw, raw = raw0 + ri * (G::kStage / 2) + lane * 16 + lw * (32 * SC);
-                        if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
-                        wait(&raw_full[ri], pos / G::kRaw & 1);
-                        constexpr int B = 4;                         // loads in flight
+                    while (t.more()) {
+                        const bool guard = guarded(u, t.is_v(), (u.k0 + t.tile()) * kChunkKeys);
+                        t.next();
 #pragma unroll 1
-                        for (int p0 = 0; p0 < 32 / RP; p0 += B) {
-                            uint4 v[B];
+                        for (int hh = 0; hh < HV; ++hh) {
+                            const uint32_t tile = smem_u32(stages) + to.i * G::kStage;
+                            const uint32_t from = raw0 + raw.i * (G::kStage / 2) + lane * 16 + lw * (32 * SC);
+                            wait(&empty[to.i], to.phase ^ 1);
+                            wait(&raw_full[raw.i], raw.phase);
+                            constexpr int B = 4;                     // loads in flight
+#pragma unroll 1
+                            for (int p0 = 0; p0 < 32 / RP; p0 += B) {
+                                uint4 v[B];
 #pragma unroll
-                            for (int i = 0; i < B; ++i) v[i] = lds_v4(raw + (p0 + i) * 512);
+                                for (int i = 0; i < B; ++i) v[i] = lds_v4(from + (p0 + i) * 512);
 #pragma unroll
-                            for (int i = 0; i < B; ++i) {
-                                uint4 lo, hi;
-                                e4m3x4_f16x4(v[i].x, lo.x, lo.y);
-                                e4m3x4_f16x4(v[i].y, lo.z, lo.w);
-                                e4m3x4_f16x4(v[i].z, hi.x, hi.y);
-                                e4m3x4_f16x4(v[i].w, hi.z, hi.w);
-                                if (guard && (not_finite4<C>(lo) | not_finite4<C>(hi))) {
-                                    s_bad[to.ordinal & 3] = to.ordinal;
-                                    lo = make_uint4(finite_pair<C>(lo.x), finite_pair<C>(lo.y), finite_pair<C>(lo.z), finite_pair<C>(lo.w));
-                                    hi = make_uint4(finite_pair<C>(hi.x), finite_pair<C>(hi.y), finite_pair<C>(hi.z), finite_pair<C>(hi.w));
+                                for (int i = 0; i < B; ++i) {
+                                    uint4 lo, hi;
+                                    e4m3x4_f16x4(v[i].x, lo.x, lo.y);
+                                    e4m3x4_f16x4(v[i].y, lo.z, lo.w);
+                                    e4m3x4_f16x4(v[i].z, hi.x, hi.y);
+                                    e4m3x4_f16x4(v[i].w, hi.z, hi.w);
+                                    if (guard && (not_finite4<C>(lo) | not_finite4<C>(hi))) {
+                                        s_bad[ordinal & 3] = ordinal;
+                                        lo = make_uint4(finite_pair<C>(lo.x), finite_pair<C>(lo.y), finite_pair<C>(lo.z), finite_pair<C>(lo.w));
+                                        hi = make_uint4(finite_pair<C>(hi.x), finite_pair<C>(hi.y), finite_pair<C>(hi.z), finite_pair<C>(hi.w));
+                                    }
+                                    const uint32_t at = tile + (RP == 4 && i & 1 ? at1 + (p0 + i - 1) * (RP * 128) : at0 + (p0 + i) * (RP * 128));
+                                    sts_v4(at, turned ? hi : lo);
+                                    sts_v4(at ^ 16, turned ? lo : hi);
                                 }
-                                const uint32_t at = tile + (RP == 4 && i & 1 ? at1 + (p0 + i - 1) * (RP * 128) : at0 + (p0 + i) * (RP * 128));
-                                sts_v4(at, turned ? hi : lo);
-                                sts_v4(at ^ 16, turned ? lo : hi);
                             }
-                        }
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&raw_empty[ri]);
-                            mbar_arrive(&full[st]);
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(&raw_empty[raw.i]);
+                                mbar_arrive(&full[to.i]);
+                            }
+                            to.next(NST);
+                            raw.next(G::kRaw);
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) done_with(to.ordinal);
+                    if (lane == 0) done_with(ordinal);
                 }
             }
         } else {
-            uint32_t guarded = 0;
-            while (true) {
-                next_of(to);
-                if (!to.u) break;
-                const Unit &u = *to.u;
-                if (to.n) ask(to);
-                for (;; ++pos) {
-                    if (to.item == min(HV, 2 * HV * to.n)) load_q(u, to.ordinal);    // behind K's first tile, which has room earlier
-                    if (to.item == 2 * HV * to.n) break;
-                    bool is_v;
-                    const int key0 = (u.k0 + to.tile(is_v)) * kChunkKeys, d0 = to.item % HV * SC + lw * 64;
-                    const bool guard = is_v && key0 + kChunkKeys > u.all0;               // as above
-                    const uint32_t st = pos % NST, tile = smem_u32(stages) + st * G::kStage;
-                    if (pos >= NST) wait(&empty[st], (pos / NST - 1) & 1);
-                    // a warp copies 64 columns
-                    copy(to, tile + lw * (kChunkKeys * 128), 128, d0, guard ? raw_full : &full[st], lw * 64 < SC && d0 < D);
-                    if (guard) {
-                        wait(raw_full, guarded);
-                        guarded ^= 1;
-                        if (lw * 64 < SC && d0 < D) {
-                            const uint32_t mine = tile + lw * (kChunkKeys * 128) + lane * 16;
+            uint32_t guard_phase = 0, filled = 0;
+            while (const Unit *const next = next_unit(++ordinal)) {
+                const Unit &u = *next;
+                Tiles t(u);
+                if (t.more()) find(u, (u.k0 + t.tile()) * kChunkKeys + lane * box, page, place);
+                bool has_q = false;
 #pragma unroll 1
-                            for (int i = 0; i < kChunkKeys * 8 / 32; i += 8) {
-                                uint4 v[8];
+                while (true) {
+                    if (!has_q && (t.k == 1 || !t.more())) {
+                        load_q(u, ordinal);                  // behind K's first tile, which has room earlier
+                        has_q = true;
+                    }
+                    if (!t.more()) break;
+                    const bool is_v = t.is_v(), in = lane < boxes && usable(page);
+                    const int key0 = (u.k0 + t.tile()) * kChunkKeys, pg = page, pl = place;
+                    const bool guard = guarded(u, is_v, key0);
+                    t.next();
+                    if (t.more()) find(u, (u.k0 + t.tile()) * kChunkKeys + lane * box, page, place);
+#pragma unroll 1
+                    for (int hh = 0; hh < HV; ++hh) {
+                        // a warp copies 64 columns
+                        const int d0 = hh * SC + lw * 64;
+                        const bool part = lw * 64 < SC && d0 < D;
+                        const uint32_t dst = smem_u32(stages) + to.i * G::kStage + lw * (kChunkKeys * 128);
+                        wait(&empty[to.i], to.phase ^ 1);
+                        if (part) copy(u, is_v, key0, pg, pl, in, d0, dst, 128, guard ? raw_full : &full[to.i]);
+                        else if (lane == 0) mbar_arrive(guard ? raw_full : &full[to.i]);
+                        if (guard) {
+                            wait(raw_full, guard_phase);
+                            guard_phase ^= 1;
+                            if (part) {
+#pragma unroll 1
+                                for (int i = 0; i < kChunkKeys * 8 / 32; i += 8) {
+                                    uint4 v[8];
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) v[k] = lds_v4(mine + (i + k) * 512);
-                                uint32_t bad = 0;
+                                    for (int k = 0; k < 8; ++k) v[k] = lds_v4(dst + lane * 16 + (i + k) * 512);
+                                    uint32_t bad = 0;
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) bad |= not_finite4<C>(v[k]);
-                                if (bad) {
-                                    s_bad[to.ordinal & 3] = to.ordinal;
+                                    for (int k = 0; k < 8; ++k) bad |= not_finite4<C>(v[k]);
+                                    if (bad) {
+                                        s_bad[ordinal & 3] = ordinal;
 #pragma unroll
-                                    for (int k = 0; k < 8; ++k)
-                                        sts_v4(mine + (i + k) * 512, make_uint4(finite_pair<C>(v[k].x), finite_pair<C>(v[k].y),
-                                                                                finite_pair<C>(v[k].z), finite_pair<C>(v[k].w)));
+                                        for (int k = 0; k < 8; ++k)
+                                            sts_v4(dst + lane * 16 + (i + k) * 512, make_uint4(finite_pair<C>(v[k].x), finite_pair<C>(v[k].y),
+                                                                                              finite_pair<C>(v[k].z), finite_pair<C>(v[k].w)));
+                                    }
                                 }
                             }
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&full[to.i]);
                         }
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&full[st]);
+                        to.next(NST);
+                        ++filled;
                     }
                 }
                 __syncwarp();
-                if (lane == 0) done_with(to.ordinal);
+                if (lane == 0) done_with(ordinal);
             }
+            // after a time-out: the copies in flight end before the block does
+            if (!ok)
+                for (uint32_t i = filled > NST ? filled - NST : 0; i < filled; ++i)
+                    mbar_wait_bounded(&full[i % NST], i / NST & 1, a.timeout_ns);
         }
         cp_async_commit();
         cp_async_wait_group<0>();
-        // after a time-out: the copies in flight end before the block does
-        if (!ok)
-            for (uint32_t i = pos > NST ? pos - NST : 0; i < pos; ++i) mbar_wait_bounded(&full[i % NST], i / NST & 1, a.timeout_ns);
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------- MMA issuers
         // A warp for each slot: what a warp does between its MMAs (a barrier's answer
