@@ -809,13 +809,12 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                     for (uint32_t i = copied > G::kRaw ? copied - G::kRaw : 0; i < copied; ++i)
                         mbar_wait_bounded(&raw_full[i % G::kRaw], i / G::kRaw & 1, a.timeout_ns);
             } else {
-                const int ch = lane % CH, row = lw * 32 + lane / CH;
-                // Where a row's chunks go: RP rows on, the swizzle changes with their number's
-                // last bits alone. Lanes of the second 64 columns take their two chunks the
-                // other way round, so that no bank is hit twice.
-                const bool turned = ch >> 2;
-                const uint32_t at0 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row, (ch & 3) * 2 + (turned ? 1 : 0));
-                const uint32_t at1 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row + RP, (ch & 3) * 2 + (turned ? 1 : 0));
+                // Lanes of the second 64 columns take the row beside theirs, whose swizzle has
+                // the other parity, so that neither load nor store hits a bank twice. RP rows
+                // on, the swizzle changes with their number's last bits alone.
+                const int ch = lane % CH, row = lw * 32 + (lane / CH ^ ch >> 2);
+                const uint32_t at0 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row, (ch & 3) * 2);
+                const uint32_t at1 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row + RP, (ch & 3) * 2);
                 while (const Unit *const next = next_unit(++ordinal)) {
                     const Unit &u = *next;
                     load_q(u, ordinal);
@@ -827,7 +826,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
 #pragma unroll 1
                         for (int hh = 0; hh < HV; ++hh) {
                             const uint32_t tile = smem_u32(stages) + to.i * G::kStage;
-                            const uint32_t from = raw0 + raw.i * (G::kStage / 2) + lane * 16 + lw * (32 * SC);
+                            const uint32_t from = raw0 + raw.i * (G::kStage / 2) + row * SC + ch * 16;
                             wait(&empty[to.i], to.phase ^ 1);
                             wait(&raw_full[raw.i], raw.phase);
                             constexpr int B = 4;                     // loads in flight
@@ -849,8 +848,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
                                         hi = make_uint4(finite_pair<C>(hi.x), finite_pair<C>(hi.y), finite_pair<C>(hi.z), finite_pair<C>(hi.w));
                                     }
                                     const uint32_t at = tile + (RP == 4 && i & 1 ? at1 + (p0 + i - 1) * (RP * 128) : at0 + (p0 + i) * (RP * 128));
-                                    sts_v4(at, turned ? hi : lo);
-                                    sts_v4(at ^ 16, turned ? lo : hi);
+                                    sts_v4(at, lo);
+                                    sts_v4(at ^ 16, hi);
                                 }
                             }
                             fence_proxy_async();
