@@ -282,26 +282,23 @@ __device__ __forceinline__ int cut_at(int64_t y, int64_t cost, int tiles)
 {
     if (y <= 0) return 0;
     if (y >= cost) return tiles;          // (most units are not cut)
-    const int k = static_cast<int>(y * tiles / cost) / kPiece * kPiece;
+    const int k = static_cast<int>(div_up_to_64(y * tiles, cost)) / kPiece * kPiece;
     return tiles - k < kPiece ? tiles : k;
 }
 
 struct Sequence {
     int q0, n, len;
+    bool bad;                // its bounds or its length are not what they may be
 };
 __device__ __forceinline__ Sequence sequence_at(const ChunkArgs &a, int b)
 {
-    const int c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1];
+    const int c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1], len = a.seq_lens ? a.seq_lens[b] : 0;
     Sequence s;
     s.q0 = min(max(c0, 0), a.tokens);
     s.n = min(max(c1, s.q0), a.tokens) - s.q0;
-    s.len = a.seq_lens ? min(max(a.seq_lens[b], 0), a.max_len) : s.n;
+    s.len = a.seq_lens ? min(max(len, 0), a.max_len) : s.n;
+    s.bad = c0 != s.q0 || c1 != s.q0 + s.n || len < 0 || len > a.max_len;
     return s;
-}
-__device__ __forceinline__ bool sequence_bad(const ChunkArgs &a, int b)
-{
-    const int c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1];
-    return c0 < 0 || c1 < c0 || c1 > a.tokens || (a.seq_lens && (a.seq_lens[b] < 0 || a.seq_lens[b] > a.max_len));
 }
 
 // Costs of a sequence's units for one KV head: unit i costs lin + R (i + 1), in
@@ -315,8 +312,8 @@ struct Costs {
     __device__ __forceinline__ Costs() {}
     __device__ __forceinline__ Costs(const Sequence &s, int group, int unit_rows, bool two_slots) : R(unit_rows)
     {
-        const int64_t rows = static_cast<int64_t>(s.n) * group;
-        T = static_cast<int>((rows + R - 1) / R);
+        const uint32_t rows = static_cast<uint32_t>(s.n) * static_cast<uint32_t>(group);     // (below 2^31: the host has checked)
+        T = static_cast<int>((rows + static_cast<uint32_t>(R) - 1) / static_cast<uint32_t>(R));
         lin = group * (static_cast<int64_t>(max(s.len - s.n, 0)) + kChunkUnitCost);
         narrow = two_slots && rows <= 128;
         head = before(T);
@@ -343,7 +340,7 @@ struct UnitWalk {
             return;
         }
         const Costs c(sequence_at(a, b), a.group, a.unit_rows, NARROW);
-        h = static_cast<int>((x0 - at) / c.head);
+        h = static_cast<int>(div_up_to_64(x0 - at, c.head));
         at += h * c.head;
         // the last unit that begins at or before x0
         int lo = 0, hi = c.T - 1;
@@ -437,7 +434,7 @@ __device__ __forceinline__ uint32_t not_finite_seen(const ChunkArgs &a, const Un
 // `list` is given all of them, with this block's place and their number.
 __device__ __forceinline__ int sharing_blocks(const Unit &u, int64_t per, int lane, int16_t *list, int &me, int &count)
 {
-    const int c0 = static_cast<int>(u.at / per), c1 = static_cast<int>((u.at + u.cost - 1) / per);
+    const int c0 = static_cast<int>(div_up_to_64(u.at, per)), c1 = static_cast<int>(div_up_to_64(u.at + u.cost - 1, per));
     int first = -1;
     count = 0;
     me = 0;
@@ -540,8 +537,9 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
         const int lo = min(a.batch, tid * per), hi = min(a.batch, lo + per);
         int64_t mine = 0;
         for (int b = lo; b < hi; ++b) {
-            if (blockIdx.x == 0 && sequence_bad(a, b)) set_status(a.status, AWQ_ERR_BAD_INDEX);
-            mine += Costs(sequence_at(a, b), a.group, a.unit_rows, QT == 2).head * a.cache.num_heads;
+            const Sequence s = sequence_at(a, b);
+            if (s.bad && blockIdx.x == 0) set_status(a.status, AWQ_ERR_BAD_INDEX);
+            mine += Costs(s, a.group, a.unit_rows, QT == 2).head * a.cache.num_heads;
         }
         int64_t incl = mine;
 #pragma unroll
@@ -559,7 +557,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
             if (w < warp) before += v;
             total += v;
         }
-        per_cta = (total + gridDim.x - 1) / gridDim.x;
+        per_cta = div_up_to_64(total + gridDim.x - 1, gridDim.x);
         x0 = min(total, per_cta * blockIdx.x);
         x1 = min(total, x0 + per_cta);
         if (x0 < x1 && x0 >= before && x0 < before + mine) {
