@@ -46,7 +46,7 @@
 #include <type_traits>
 
 #include "awq_launch.cuh"
-#include "awq_prompt_kernels.cuh"
+#include "awq_prompt_units.cuh"
 #include "awq_tc.cuh"
 
 namespace awq {
@@ -61,7 +61,6 @@ constexpr float kChunkRaiseF16 = 7.f;
 // of 0 a masked score of -infinity would be NaN.
 constexpr float kChunkMinFactor = 1.17549435e-38f;
 constexpr float kChunkLn2 = 0.6931471805599453f;
-constexpr int kPiece = 8;              // key tiles: cuts of a unit are multiples of it
 constexpr int kMmaWarp = 8, kLoaderWarp = 10;
 constexpr int kUnits = 3;              // units in shared memory
 constexpr int kWaitTries = 1 << 18;    // 1 to 2 s
@@ -254,145 +253,6 @@ __device__ __forceinline__ void st_v4(void *p, const uint32_t *r)
     asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
-// ------------------------------------------------------------------ the units
-
-// What a block has of a unit: key tiles k0 .. k1 - 1. 16 words, made by one warp
-// and read by the others from shared memory.
-struct Unit {
-    int64_t at, cost;      // its place in the sum of costs
-    int b, h;              // sequence, KV head; b < 0: no more units
-    int q0, ctx;           // the sequence's first row of q, its tokens before the new ones
-    int row0, rows;        // packed rows
-    int keys;              // keys that its last row sees
-    int k0, k1, n0;        // n0: tiles from k0 on that its first 128 rows see something of
-    int all0, all1;        // keys that every row of the unit and every row of its second tile sees
-    __device__ __forceinline__ int tiles() const { return (keys + kChunkKeys - 1) / kChunkKeys; }
-    __device__ __forceinline__ bool cut() const { return k0 > 0 || k1 < tiles(); }
-};
-static_assert(sizeof(Unit) == 64, "16 words");
-
-// Keys that packed row `row` sees, `ctx` tokens before the sequence's new ones.
-__device__ __forceinline__ int row_limit(int ctx, int row, int group)
-{
-    return max(0, ctx + static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(group)) + 1);
-}
-
-// Key tiles of a unit before a cut at `y` of its cost.
-__device__ __forceinline__ int cut_at(int64_t y, int64_t cost, int tiles)
-{
-    if (y <= 0) return 0;
-    if (y >= cost) return tiles;          // (most units are not cut)
-    const int k = static_cast<int>(div_up_to_64(y * tiles, cost)) / kPiece * kPiece;
-    return tiles - k < kPiece ? tiles : k;
-}
-
-struct Sequence {
-    int q0, n, len;
-    bool bad;                // its bounds or its length are not what they may be
-};
-__device__ __forceinline__ Sequence sequence_at(const ChunkArgs &a, int b)
-{
-    const int c0 = a.cu_seqlens[b], c1 = a.cu_seqlens[b + 1], len = a.seq_lens ? a.seq_lens[b] : 0;
-    Sequence s;
-    s.q0 = min(max(c0, 0), a.tokens);
-    s.n = min(max(c1, s.q0), a.tokens) - s.q0;
-    s.len = a.seq_lens ? min(max(len, 0), a.max_len) : s.n;
-    s.bad = c0 != s.q0 || c1 != s.q0 + s.n || len < 0 || len > a.max_len;
-    return s;
-}
-
-// Costs of a sequence's units for one KV head: unit i costs lin + R (i + 1), in
-// keys times G (so that all sequences count alike); a narrow one by itself 7/8 of
-// that (half the products, but as many bytes: 16 sequences that decode beside three
-// chunks took 128 us with it, 134 with 1, 149 with 5/8, 170 with a half).
-struct Costs {
-    int64_t lin, head;
-    int T, R;
-    bool narrow;
-    __device__ __forceinline__ Costs() {}
-    __device__ __forceinline__ Costs(const Sequence &s, int group, int unit_rows, bool two_slots) : R(unit_rows)
-    {
-        const uint32_t rows = static_cast<uint32_t>(s.n) * static_cast<uint32_t>(group);     // (below 2^31: the host has checked)
-        T = static_cast<int>((rows + static_cast<uint32_t>(R) - 1) / static_cast<uint32_t>(R));
-        lin = group * (static_cast<int64_t>(max(s.len - s.n, 0)) + kChunkUnitCost);
-        narrow = two_slots && rows <= 128;
-        head = before(T);
-    }
-    __device__ __forceinline__ int64_t before(int i) const
-    {
-        const int64_t c = i * lin + static_cast<int64_t>(i) * (i + 1) / 2 * R;
-        return narrow ? c * 7 / 8 : c;
-    }
-};
-
-// Walks through the units of a block's share [x0, x1) of the costs. Only its place
-// is kept; the sequence is looked at again for each unit.
-template <bool NARROW>
-struct UnitWalk {
-    int64_t x0, x1, at;      // the share; where the next unit begins
-    int b, h, t;
-
-    __device__ __forceinline__ UnitWalk(const ChunkArgs &a, int64_t from, int64_t to, int first, int64_t first_at)
-        : x0(from), x1(to), at(first_at), b(first), h(0), t(0)
-    {
-        if (x0 >= x1) {
-            at = x1;                                    // no share: no units
-            return;
-        }
-        const Costs c(sequence_at(a, b), a.group, a.unit_rows, NARROW);
-        h = static_cast<int>(div_up_to_64(x0 - at, c.head));
-        at += h * c.head;
-        // the last unit that begins at or before x0
-        int lo = 0, hi = c.T - 1;
-#pragma unroll 1
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (at + c.before(mid) <= x0) lo = mid;
-            else hi = mid - 1;
-        }
-        t = lo;
-        at += c.before(t);
-    }
-    // The block's next unit.
-    __device__ __forceinline__ bool next(const ChunkArgs &a, Unit &u)
-    {
-#pragma unroll 1
-        while (at < x1) {
-            const Sequence s = sequence_at(a, b);
-            const Costs c(s, a.group, a.unit_rows, NARROW);
-            if (t == c.T) {                             // (units remain, as costs do)
-                t = 0;
-                if (++h == a.cache.num_heads || c.T == 0) {
-                    h = 0;
-                    ++b;
-                }
-                continue;
-            }
-            const int row0 = t * a.unit_rows, rows = min(a.unit_rows, s.n * a.group - row0), ctx = s.len - s.n;
-            u.at = at;
-            u.cost = c.before(t + 1) - c.before(t);
-            u.b = b;
-            u.h = h;
-            u.q0 = s.q0;
-            u.ctx = ctx;
-            u.row0 = row0;
-            u.rows = rows;
-            u.keys = row_limit(ctx, row0 + rows - 1, a.group);
-            const int tiles = u.tiles();
-            u.k0 = cut_at(x0 - at, u.cost, tiles);
-            u.k1 = cut_at(x1 - at, u.cost, tiles);
-            const int seen0 = row_limit(ctx, row0 + min(rows, 128) - 1, a.group);
-            u.n0 = min(u.k1 - u.k0, max(0, (seen0 + kChunkKeys - 1) / kChunkKeys - u.k0));
-            u.all0 = row_limit(ctx, row0, a.group);
-            u.all1 = row_limit(ctx, row0 + 128, a.group);
-            const bool mine = tiles ? u.k1 > u.k0 : x0 <= at;
-            at += u.cost;
-            ++t;
-            if (mine) return true;
-        }
-        return false;
-    }
-};
 
 // Which of the columns c .. c + 31 of V hold a value that is not finite at a key
 // that the row sees, among the tiles whose values were made finite on their way
@@ -434,14 +294,13 @@ __device__ __forceinline__ uint32_t not_finite_seen(const ChunkArgs &a, const Un
 // `list` is given all of them, with this block's place and their number.
 __device__ __forceinline__ int sharing_blocks(const Unit &u, int64_t per, int lane, int16_t *list, int &me, int &count)
 {
-    const int c0 = static_cast<int>(div_up_to_64(u.at, per)), c1 = static_cast<int>(div_up_to_64(u.at + u.cost - 1, per));
+    const int c0 = first_block(u, per), c1 = last_block(u, per);
     int first = -1;
     count = 0;
     me = 0;
     for (int base = c0; base <= c1; base += 32) {
         const int c = base + lane;
-        const int ka = cut_at(c * per - u.at, u.cost, u.tiles()), kb = cut_at((c + 1) * per - u.at, u.cost, u.tiles());
-        const bool in = c <= c1 && kb > ka;
+        const bool in = c <= c1 && shares(u, per, c);
         const uint32_t all = __ballot_sync(~0u, in);
         if (all == 0) continue;
         if (first < 0) first = base + __ffs(all) - 1;
@@ -557,7 +416,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_ker
             if (w < warp) before += v;
             total += v;
         }
-        per_cta = div_up_to_64(total + gridDim.x - 1, gridDim.x);
+        per_cta = share_of(total, gridDim.x);
         x0 = min(total, per_cta * blockIdx.x);
         x1 = min(total, x0 + per_cta);
         if (x0 < x1 && x0 >= before && x0 < before + mine) {
