@@ -34,11 +34,15 @@ extern "C" {
  * buffers is touched, and the sequences that they bound are undefined.
  * q, out: 16-bit [tokens][q_heads][head_dim]; k, v: [tokens][kv_heads]
  * [head_dim], all 16-byte aligned with strides that are multiples of 16 bytes
- * (k's and v's below 2^39 elements, between tokens not 0); cu_seqlens i32[batch + 1]; lse f32[tokens][q_heads], dense, or NULL.
+ * (k's and v's at most 2^39 elements, and not 0 between tokens if there are more
+ * than one); cu_seqlens i32[batch + 1]; lse f32[tokens][q_heads], dense, or
+ * NULL; outputs overlap no input.
  * batch, tokens >= 0 (0 launches nothing); q_heads a multiple of kv_heads;
- * head_dim a multiple of 8 up to AWQ_ATTN_MAX_HEAD_DIM; tokens * (q_heads /
- * kv_heads) below 2^31 and batch * kv_heads * (tokens * (q_heads / kv_heads) /
- * 128 + 1) * (q_heads / kv_heads) * (2 * tokens + 512) below 2^61.
+ * head_dim a multiple of 8 up to AWQ_ATTN_MAX_HEAD_DIM. Sizes that the 32-bit
+ * rows and 64-bit costs of the split cannot hold are refused: with G = q_heads /
+ * kv_heads, tokens * G has to be at most 2^31 - 256, and with the longest
+ * context L (here: tokens) and u = G * (L + tokens + 256) + 512, both u * (L /
+ * 128 + 1) and u * (tokens * G / 120 + 1) * kv_heads * batch at most 4 * 10^18.
  * Work is split over the rows, and over the keys where that alone does not fill
  * the card, by the lengths on the device; the parts are joined in the same
  * launch, which is cooperative (all blocks at once on the multiprocessors).
@@ -79,9 +83,10 @@ AWQ_API size_t awq_prompt_attention_workspace_bytes(int32_t head_dim);
  * AWQ_ERR_BAD_INDEX; that sequence's output is then undefined.
  * page_table i32[batch][max_pages], row stride table_stride; seq_lens
  * i32[batch]; q, out, cu_seqlens, lse, workspace and limits as in
- * awq_prompt_attention, with max_pages * page_size in place of 2 * tokens; head_dim a
- * multiple of 16 for an e4m3 cache; both planes 16-byte aligned with strides
- * that are multiples of 16 bytes, below 2^39 elements and between tokens not 0.
+ * awq_prompt_attention, with L = max_pages * page_size; head_dim a multiple of
+ * 16 for an e4m3 cache; both planes 16-byte aligned with strides that are
+ * multiples of 16 bytes, at most 2^39 elements, and not 0 between tokens if a
+ * page holds more than one.
  * The cache is copied in boxes of as many tokens as the largest power of two up
  * to 128 that divides page_size: pages of an odd size are read token by token.
  */
