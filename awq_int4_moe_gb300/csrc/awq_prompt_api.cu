@@ -30,7 +30,7 @@ awq_status chunk_call(ChunkArgs &a, int32_t dtype, float scale, void *workspace,
     // fewest boxes of up to 64 rows.
     const int most_rows = chunk_rows(attn_padded_dim(dim));
     a.unit_rows = most_rows;
-    const int64_t far = 1ll << 39;
+    const int64_t far = 1ll << 39;               // elements: a tensor map's strides end at 2^40 bytes
     if (a.group <= most_rows && (a.q_heads == 1 || (a.q.head_stride > 0 && a.q.head_stride < far)) &&
         (a.tokens == 1 || (a.q.token_stride > 0 && a.q.token_stride < far))) {
         int best = INT_MAX;
@@ -57,7 +57,7 @@ awq_status chunk_call(ChunkArgs &a, int32_t dtype, float scale, void *workspace,
     const int64_t place = a.page_table ? a.cache.page_size : a.tokens;
     for (int i = 0; i < 2; ++i) {
         const awq_kv_plane &p = i ? a.cache.v : a.cache.k;
-        if ((place > 1 && p.token_stride == 0) || p.token_stride > far || p.head_stride > far || p.page_stride > far)
+        if ((place > 1 && p.token_stride == 0) || p.token_stride >= far || p.head_stride >= far || p.page_stride >= far)
             return AWQ_ERR_UNSUPPORTED_SHAPE;
         a.head_step[i] = p.head_stride ? 1 : 0;
         a.page_step[i] = p.page_stride ? 1 : 0;

@@ -26,13 +26,18 @@
 //   heads larger than 128: one warpgroup, its score tile double-buffered.
 // Tensor memory: S (and P over it, 16 bits) 2 x 128 columns, O 2 x 128 or 256.
 //
-// Warps: 0-7 softmax and output, a thread per row; 8-9 issue the MMAs of a slot
-// each; 10-11 find the units and load (Q, then K and V tiles of 128 keys x 128 columns, 128-byte
-// swizzle, by cp.async, 16 bytes a thread, so that any page size and stride will
-// do; e4m3 tiles come as codes first and are expanded to fp16 in shared memory).
-// They meet at mbarriers, every wait is bounded. Registers go where the scores are
-// (208 a thread there): with 227 KB of shared memory in use what spills comes back
-// from L2.
+// Warps: 0-7 softmax and output, a thread per row (nothing crosses lanes in a
+// step); 8 and 9 issue the MMAs of a slot each; the rest load. Units are found one
+// ahead of their use, by warp 9, or over e4m3 by warp 11. All meet at mbarriers, every
+// wait is bounded. Registers go where the scores are (208 or 200 a thread there): with 227 KB
+// of shared memory in use what spills comes back from L2.
+//
+// Copies are TMA boxes into 128-byte swizzled stages of 128 keys x 128 columns: of K
+// and V as many keys as the largest power of two up to 128 that divides the page (any page
+// size and stride will do), of Q whole tokens, for which a unit has a whole number
+// of them. Where Q cannot come so (more than 256 heads of one, or fewer bits than
+// it has) threads copy it. e4m3 tiles come as codes and are expanded to fp16 in
+// shared memory by four warps: kind::f8f6f4 would want the weights and q in 8 bits.
 //
 // Balance. Units are numbered sequence by sequence, head by head, tile by tile;
 // their costs (a unit's keys and a fixed part) have a closed form, and every
@@ -40,6 +45,22 @@
 // that is cut (in whole multiples of kPiece key tiles) leaves its parts in the
 // workspace; at the end the blocks that share it wait for the last one and each
 // join a part of its rows, in block order, so the same inputs give the same bits.
+//
+// Bound. Wide units over 16-bit keys: per key tile and slot 4 x 2 x 128^3 / 8192
+// = 2048 cycles of the tensor core for both slots against some 2750 measured: the
+// chain scores, maximum, exponentials (128 a thread, 4 cycles a warp's
+// instruction) and product of a slot is not quite hidden by the other's. Then a unit's
+// turnaround (its last product, the stores, the next one's Q: 9000 cycles). Narrow
+// units: the bytes of K and V; over e4m3 their expansion (1650 cycles a tile, 32 KB
+// to shared memory). Small calls: launch, scan, and some ten dependent steps.
+// Device time: one prompt of 8192 tokens, 32 heads over 8 of 128, 414 us (1.33
+// PFLOP/s); 1024 tokens over 32768, 388 us; 13 ragged prompts up to 4096, 174 us; 4
+// prompts with heads of 256, 170 us; 4 new tokens for each of 32 sequences over an e4m3
+// cache, 201 us (2.7 TB/s of it); a prompt of 48, 12 us.
+// Tried, and slower: the scores read twice from tensor memory instead of kept in
+// registers, the first weights taken against the old maximum before the new one
+// is known (414 -> 456 us), one issuing warp for both slots (by a fifth),
+// rolled loops over the MMAs, outputs transposed by shuffles before their stores.
 #pragma once
 
 #include <climits>
@@ -82,7 +103,8 @@ struct ChunkGeo {
     // after Q and the stages: maxima and sums that two slots exchange, rows' powers of two, barriers
     static constexpr int oStages = kQ, oRaw = oStages + kStages * kStage, oMl = oRaw + kRaw * kStage / 2, oExp = oMl + 2 * 128 * 8,
                          oUnits = oExp + 2 * 256, oBars = oUnits + kUnits * 64,
-                         kRawBars = FP8 ? kRaw : 1, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 3 + 2 * kUnits + 2 * kRawBars, oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
+                         kRawBars = FP8 ? kRaw : 1, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 3 + 2 * kUnits + 2 * kRawBars,
+                         oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
     static constexpr uint32_t kTmemO = 256;                 // first column of O; S at 0 and 128
     static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
@@ -253,7 +275,6 @@ __device__ __forceinline__ void st_v4(void *p, const uint32_t *r)
     asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
-
 // Which of the columns c .. c + 31 of V hold a value that is not finite at a key
 // that the row sees, among the tiles whose values were made finite on their way
 // to the tensor core. Reads them again: nothing of it runs on finite values.
@@ -317,9 +338,9 @@ __device__ __forceinline__ int sharing_blocks(const Unit &u, int64_t per, int la
 // ----------------------------------------------------------------- the kernel
 
 template <typename T, bool FP8, int DP>
-__global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1) chunk_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                                                                      const __grid_constant__ CUtensorMap map_q,
-                                                                      const __grid_constant__ ChunkArgs a)
+__global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                      const __grid_constant__ CUtensorMap map_q, const __grid_constant__ ChunkArgs a)
 {
     using G = ChunkGeo<DP, FP8>;
     using C = typename std::conditional<FP8, __half, T>::type;      // the tensor core's type

@@ -46,7 +46,9 @@ constexpr int kChunkKeys = 128;                                       // tokens 
 // Packed rows (a token's query heads of one KV head, token by token) of a unit:
 // two tiles of 128, one where a head is larger than 128.
 constexpr int chunk_rows(int padded_dim) { return padded_dim <= 128 ? 256 : 128; }
-constexpr int64_t kChunkUnitCost = 256;                               // a unit's fixed time, in tokens of its keys
+// A unit's fixed time (Q, start, turnaround, stores) in tokens of its keys: some
+// 5000 cycles of the 2750 that a tile of 128 takes.
+constexpr int64_t kChunkUnitCost = 256;
 // Floats of a piece: output, maximum, sum of every row.
 constexpr size_t chunk_piece_floats(int padded_dim) { return static_cast<size_t>(chunk_rows(padded_dim)) * (padded_dim + 2); }
 constexpr size_t chunk_workspace_bytes(int dim)

@@ -34,7 +34,7 @@ extern "C" {
  * buffers is touched, and the sequences that they bound are undefined.
  * q, out: 16-bit [tokens][q_heads][head_dim]; k, v: [tokens][kv_heads]
  * [head_dim], all 16-byte aligned with strides that are multiples of 16 bytes
- * (k's and v's at most 2^39 elements, and not 0 between tokens if there are more
+ * (k's and v's below 2^39 elements, and not 0 between tokens if there are more
  * than one); cu_seqlens i32[batch + 1]; lse f32[tokens][q_heads], dense, or
  * NULL; outputs overlap no input.
  * batch, tokens >= 0 (0 launches nothing); q_heads a multiple of kv_heads;
@@ -85,7 +85,7 @@ AWQ_API size_t awq_prompt_attention_workspace_bytes(int32_t head_dim);
  * i32[batch]; q, out, cu_seqlens, lse, workspace and limits as in
  * awq_prompt_attention, with L = max_pages * page_size; head_dim a multiple of
  * 16 for an e4m3 cache; both planes 16-byte aligned with strides that are
- * multiples of 16 bytes, at most 2^39 elements, and not 0 between tokens if a
+ * multiples of 16 bytes, below 2^39 elements, and not 0 between tokens if a
  * page holds more than one.
  * The cache is copied in boxes of as many tokens as the largest power of two up
  * to 128 that divides page_size: pages of an odd size are read token by token.
@@ -102,8 +102,9 @@ AWQ_API awq_status awq_chunk_attention(const awq_heads *q, const awq_kv_cache *c
  * q and k in front of the rotation, in the same pass:
  *   y[d] = x[d] / sqrt(mean over the head of x^2 + eps) * weight[d]
  * in fp32; y is rotated (and copied past rotary_dim) without being rounded in
- * between. v is appended as it is. A head whose sum of squares passes fp32's
- * range (finite bf16 values can) has y = 0.
+ * between. v is appended as it is. The squares are added in fp32: a head whose
+ * sum passes its range (finite bf16 values can) has y = 0, and squares below its
+ * range count as 0.
  * q_weight, k_weight: 16-bit [head_dim] of the activations' type, 2-byte
  * aligned; eps >= 0 and finite. All else as in awq_rope_append.
  */

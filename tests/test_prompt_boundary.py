@@ -61,7 +61,8 @@ NAN, INF = float("nan"), float("inf")
     (dict(q=heads(data=P + 8)), ALIGN), (dict(k=heads(tok=516)), ALIGN), (dict(v=heads(head=68)), ALIGN), (dict(out=heads(data=P + 1)), ALIGN),
     (dict(cu=P + 2), ALIGN), (dict(lse=P + 2), ALIGN), (dict(ws=P + 128), ALIGN), (dict(status=P + 2), ALIGN), (dict(ws_bytes=1000), SMALL),
     (dict(ws_bytes=awq.prompt_attention_workspace_bytes(64) - 1), SMALL),
-    (dict(tokens=(1 << 31) - 1), SHAPE), (dict(tokens=1 << 30, batch=1 << 30), SHAPE)])
+    (dict(tokens=(1 << 31) - 1), SHAPE), (dict(tokens=1 << 30, batch=1 << 30), SHAPE),
+    (dict(k=heads(tok=0)), SHAPE), (dict(v=heads(tok=0)), SHAPE), (dict(k=heads(tok=1 << 39)), SHAPE), (dict(v=heads(head=1 << 39)), SHAPE)])
 def test_prompt_refusals(over, code):
     assert prompt(**over) == code
 
@@ -91,7 +92,8 @@ def chunk(**over):
     (dict(q=heads(tok=516)), ALIGN), (dict(out=heads(head=68)), ALIGN), (dict(cache=cache(k=plane(data=P + 2))), ALIGN),
     (dict(cache=cache(v=plane(page=2052))), ALIGN), (dict(cache=cache(dtype=2, k=plane(token=136))), ALIGN), (dict(table=P + 2), ALIGN),
     (dict(cu=P + 2), ALIGN), (dict(lens=P + 2), ALIGN), (dict(lse=P + 2), ALIGN), (dict(ws=P + 128), ALIGN), (dict(status=P + 2), ALIGN),
-    (dict(ws_bytes=1000), SMALL), (dict(tokens=(1 << 31) - 1), SHAPE), (dict(batch=1 << 30, tokens=1 << 20, pages=1 << 26, stride=1 << 26), SHAPE)])
+    (dict(ws_bytes=1000), SMALL), (dict(tokens=(1 << 31) - 1), SHAPE), (dict(batch=1 << 30, tokens=1 << 20, pages=1 << 26, stride=1 << 26), SHAPE),
+    (dict(cache=cache(k=plane(token=0))), SHAPE), (dict(cache=cache(v=plane(page=1 << 39))), SHAPE)])
 def test_chunk_refusals(over, code):
     assert chunk(**over) == code
 
