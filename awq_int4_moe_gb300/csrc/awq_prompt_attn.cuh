@@ -467,6 +467,12 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 break;
             }
     };
+    // Both (their answers, of 100 cycles each, come together).
+    auto wait_two = [&](uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1) {
+        const bool in0 = mbar_try_wait(bar0, parity0), in1 = mbar_try_wait(bar1, parity1);
+        if (!in0) wait(bar0, parity0);
+        if (!in1) wait(bar1, parity1);
+    };
     // The role's next unit (the ordinal-th, from 1) in shared memory; NULL after the
     // last one. It is given back, by one thread of each warp, with done_with().
     auto next_unit = [&](int ordinal) -> const Unit * {
@@ -599,29 +605,30 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             }
         };
         // Copies are boxes of a.box keys, as many as lie in one page wherever they begin;
-        // nothing of boxes past the unit's keys. Lane i has the i-th box of a tile (and
-        // every 32nd more); where it is, is asked for a tile ahead.
+        // nothing of boxes past the unit's keys (their place is -1). Lane i has the i-th
+        // box of a tile (and every 32nd more); where it is, is asked for a tile ahead, and
+        // the page's number looked at when it is needed (at once, it held the copies of
+        // each tile back for as long as the table takes to answer).
         const int box = a.box, boxes = kChunkKeys / box;
         auto find = [&](const Unit &u, int key, int &page, int &place) {
-            page = -1;
-            place = 0;
+            page = 0;
+            place = -1;
             if (key >= u.keys) return;
             if (!a.page_table) {
-                page = 0;
                 place = u.q0 + key;
                 return;
             }
             const int at = a.page_shift ? __umulhi(key, a.page_magic) >> (a.page_shift - 1) : key;
             place = key - at * a.cache.page_size;
             page = a.page_table[u.b * a.table_stride + at];
-            if (page < 0) page = INT_MIN;                    // (told apart from nothing to copy)
         };
-        auto usable = [&](int page) {
+        auto usable = [&](int page, int place) {
+            if (place < 0) return false;
             if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.page_table ? a.cache.num_pages : 1)) return true;
-            if (page != -1) set_status(a.status, AWQ_ERR_BAD_INDEX);
+            set_status(a.status, AWQ_ERR_BAD_INDEX);
             return false;
         };
-        int page = -1, place = 0;                            // of the lane's box of the next tile
+        int page = 0, place = -1;                            // of the lane's box of the next tile
         // One stage (from column d0 on) of the tile at key0, whose first boxes are at
         // `page` and `place`, `in` where they are to be copied. Lane 0 arrives at `bar`
         // with the bytes.
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 for (int i = lane + 32; i < boxes; i += 32) {
                     int pg, pl;
                     find(u, key0 + i * box, pg, pl);
-                    count += __popc(__ballot_sync(~0u, usable(pg)));
+                    count += __popc(__ballot_sync(~0u, usable(pg, pl)));
                 }
             }
             if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 for (int i = lane + 32; i < boxes; i += 32) {
                     int pg, pl;
                     find(u, key0 + i * box, pg, pl);
-                    if (usable(pg)) tma_load_4d(dst + i * bytes, map, bar, d0, pl, head, step * pg);
+                    if (usable(pg, pl)) tma_load_4d(dst + i * bytes, map, bar, d0, pl, head, step * pg);
                 }
             }
         };
@@ -670,7 +677,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     if (t.more()) find(u, (u.k0 + t.tile()) * kChunkKeys + lane * box, page, place);
 #pragma unroll 1
                     while (t.more()) {
-                        const bool is_v = t.is_v(), in = lane < boxes && usable(page);
+                        const bool is_v = t.is_v(), in = lane < boxes && usable(page, place);
                         const int key0 = (u.k0 + t.tile()) * kChunkKeys, pg = page, pl = place;
                         t.next();
                         if (t.more()) find(u, (u.k0 + t.tile()) * kChunkKeys + lane * box, page, place);
@@ -707,29 +714,40 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                         for (int hh = 0; hh < HV; ++hh) {
                             const uint32_t tile = smem_u32(stages) + to.i * G::kStage;
                             const uint32_t from = raw0 + raw.i * (G::kStage / 2) + row * SC + ch * 16;
-                            wait(&empty[to.i], to.phase ^ 1);
-                            wait(&raw_full[raw.i], raw.phase);
-                            constexpr int B = 4;                     // loads in flight
+                            wait_two(&empty[to.i], to.phase ^ 1, &raw_full[raw.i], raw.phase);
+                            // (unrolled where rows alternate between two offsets)
+                            auto place_of = [&](int i) { return tile + (RP == 4 && i & 1 ? at1 + (i - 1) * (RP * 128) : at0 + i * (RP * 128)); };
+                            auto expand = [&](const uint4 &v, uint4 &lo, uint4 &hi) {
+                                e4m3x4_f16x4(v.x, lo.x, lo.y);
+                                e4m3x4_f16x4(v.y, lo.z, lo.w);
+                                e4m3x4_f16x4(v.z, hi.x, hi.y);
+                                e4m3x4_f16x4(v.w, hi.z, hi.w);
+                            };
+                            if (guard) {
 #pragma unroll 1
-                            for (int p0 = 0; p0 < 32 / RP; p0 += B) {
-                                uint4 v[B];
-#pragma unroll
-                                for (int i = 0; i < B; ++i) v[i] = lds_v4(from + (p0 + i) * 512);
-#pragma unroll
-                                for (int i = 0; i < B; ++i) {
+                                for (int i = 0; i < 32 / RP; ++i) {
                                     uint4 lo, hi;
-                                    e4m3x4_f16x4(v[i].x, lo.x, lo.y);
-                                    e4m3x4_f16x4(v[i].y, lo.z, lo.w);
-                                    e4m3x4_f16x4(v[i].z, hi.x, hi.y);
-                                    e4m3x4_f16x4(v[i].w, hi.z, hi.w);
-                                    if (guard && (not_finite4<C>(lo) | not_finite4<C>(hi))) {
+                                    expand(lds_v4(from + i * 512), lo, hi);
+                                    if (not_finite4<C>(lo) | not_finite4<C>(hi)) {
                                         s_bad[ordinal & 3] = ordinal;
                                         lo = make_uint4(finite_pair<C>(lo.x), finite_pair<C>(lo.y), finite_pair<C>(lo.z), finite_pair<C>(lo.w));
                                         hi = make_uint4(finite_pair<C>(hi.x), finite_pair<C>(hi.y), finite_pair<C>(hi.z), finite_pair<C>(hi.w));
                                     }
-                                    const uint32_t at = tile + (RP == 4 && i & 1 ? at1 + (p0 + i - 1) * (RP * 128) : at0 + (p0 + i) * (RP * 128));
-                                    sts_v4(at, lo);
-                                    sts_v4(at ^ 16, hi);
+                                    sts_v4(place_of(i), lo);
+                                    sts_v4(place_of(i) ^ 16, hi);
+                                }
+                            } else {
+                                constexpr int B = 4;                 // loads in flight
+                                uint4 v[B];
+#pragma unroll
+                                for (int i = 0; i < B; ++i) v[i] = lds_v4(from + i * 512);
+#pragma unroll
+                                for (int i = 0; i < 32 / RP; ++i) {
+                                    uint4 lo, hi;
+                                    expand(v[i % B], lo, hi);
+                                    if (i + B < 32 / RP) v[i % B] = lds_v4(from + (i + B) * 512);
+                                    sts_v4(place_of(i), lo);
+                                    sts_v4(place_of(i) ^ 16, hi);
                                 }
                             }
                             fence_proxy_async();
@@ -760,7 +778,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                         has_q = true;
                     }
                     if (!t.more()) break;
-                    const bool is_v = t.is_v(), in = lane < boxes && usable(page);
+                    const bool is_v = t.is_v(), in = lane < boxes && usable(page, place);
                     const int key0 = (u.k0 + t.tile()) * kChunkKeys, pg = page, pl = place;
                     const bool guard = guarded(u, is_v, key0);
                     t.next();
@@ -943,9 +961,10 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                         if (kFinds && j == min(0, n) && !all_made && made == ordinal) all_made = !make_unit(walk, made++);
                         if (j == n) break;
                         const bool next = j + ahead < n;
-                        if (next) wait(&full[kp.st], kp.phase);
+                        if (next && j >= 0) wait_two(&full[kp.st], kp.phase, &full[vp.st], vp.phase);
+                        else if (next) wait(&full[kp.st], kp.phase);
+                        else wait(&full[vp.st], vp.phase);
                         if (j >= 0) {
-                            wait(&full[vp.st], vp.phase);
                             if (mine(j)) {
                                 pv(me, me, more);
                                 more = true;

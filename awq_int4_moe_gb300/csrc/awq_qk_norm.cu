@@ -9,11 +9,11 @@
 // x' the other element of the pair (from the lane half a rotation away, or the
 // neighbour in the chunk), the token's products of weights, cosines and signed
 // sines are formed once and a row costs four products and a sum per element.
-// From 8 tokens per multiprocessor on a token is one warp's, which forms those
-// products once for all its rows and has two rows on their way (8191 tokens of 32 + 2
-// x 8 heads of 128: 41 us; with 256 threads a token, 58). Below that a token's q, k and
-// v are blocks of their own, of as many threads as they have chunks (16 such tokens:
-// 2.1 us, with a warp each 5).
+// From 3 tokens per multiprocessor on a token is one warp's, which forms those
+// products once for all its rows and has two rows on their way; below that a token's q, k
+// and v are blocks of their own, of as many threads as they have chunks. 32 + 2 x 8 heads
+// of 128, a warp against blocks: 64 tokens 7.2 / 3.0 us, 300 7.4 / 5.8, 600 7.5 / 9.0,
+// 1200 8.4 / 16, 8191 40 / 109.
 //
 // Any other shape (head_norm_kernel): a row is dealt in items to 1 to 32
 // neighbouring lanes: an item is VEC pairs half a rotation apart (two accesses
@@ -403,7 +403,7 @@ template <typename T, bool FP8>
 awq_status launch_head_rows(const HeadNormArgs &n, int sms, cudaStream_t st)
 {
     const bool inter = n.rope.interleaved;
-    if (n.rope.tokens >= 8 * sms)
+    if (n.rope.tokens >= 3 * sms)
         return inter ? launch_head_rows_i<T, FP8, true, 32>(n, st) : launch_head_rows_i<T, FP8, false, 32>(n, st);
     return inter ? launch_head_rows_i<T, FP8, true, 256>(n, st) : launch_head_rows_i<T, FP8, false, 256>(n, st);
 }
