@@ -605,15 +605,13 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             }
         };
         // Copies are boxes of a.box keys, as many as lie in one page wherever they begin;
-        // nothing of boxes past the unit's keys (their place is -1). Lane i has the i-th
-        // box of a tile (and every 32nd more); where it is, is asked for a tile ahead, and
-        // the page's number looked at when it is needed (at once, it held the copies of
-        // each tile back for as long as the table takes to answer).
+        // nothing of boxes past the unit's keys (their place is -1). Boxes of less than 4
+        // keys: lane i has the i-th box of a tile, every 32nd more is found late.
         const int box = a.box, boxes = kChunkKeys / box;
-        auto find = [&](const Unit &u, int key, int &page, int &place) {
+        auto find = [&](const Unit &u, uint32_t key, int &page, int &place) {
             page = 0;
             place = -1;
-            if (key >= u.keys) return;
+            if (key >= static_cast<uint32_t>(u.keys)) return;
             if (!a.page_table) {
                 place = u.q0 + key;
                 return;
@@ -628,11 +626,11 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             set_status(a.status, AWQ_ERR_BAD_INDEX);
             return false;
         };
-        int page = 0, place = -1;                            // of the lane's box of the next tile
-        // One stage (from column d0 on) of the tile at key0, whose first boxes are at
-        // `page` and `place`, `in` where they are to be copied. Lane 0 arrives at `bar`
-        // with the bytes.
-        auto copy = [&](const Unit &u, bool is_v, int key0, int page, int place, bool in, int d0, uint32_t dst, int row_bytes, uint64_t *bar) {
+        // One stage (from column d0 on) of the tile at key0, of which the lane has the
+        // lane_box-th box, at `page` and `place`, `in` where it is to be copied. Lane 0
+        // arrives at `bar` with the bytes.
+        auto copy = [&](const Unit &u, bool is_v, int key0, int lane_box, int page, int place, bool in, int d0, uint32_t dst,
+                        int row_bytes, uint64_t *bar) {
             const CUtensorMap *const map = is_v ? &map_v : &map_k;
             const int head = a.head_step[is_v] * u.h, step = a.page_step[is_v];
             const int bytes = box * row_bytes;
@@ -647,7 +645,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             }
             if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
             __syncwarp();
-            if (in) tma_load_4d(dst + lane * bytes, map, bar, d0, place, head, step * page);
+            if (in) tma_load_4d(dst + lane_box * bytes, map, bar, d0, place, head, step * page);
             if (boxes > 32) {
 #pragma unroll 1
                 for (int i = lane + 32; i < boxes; i += 32) {
@@ -670,21 +668,48 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             const uint32_t raw0 = smem_u32(smem + G::oRaw);
             Ring raw;
             if (warp == kLoaderWarp) {
+                // A lane has a box of one of the next tiles, and the one as many tiles on: a
+                // page's number is asked for well before it is used (asked for one tile
+                // ahead, as with 16 bits, it held every tile back: 201 -> 187 us for 4 new
+                // tokens of 32 sequences; there, registers are short and it lost 4 %).
+                const int per = min(boxes, 32), tiles = 32 / per, lane_box = lane & (per - 1), lane_tile = lane / per;
+                struct Places {
+                    int page, place, page1, place1;          // of the lane's box, and of its next one
+                } of_k, of_v;
+                auto look = [&](const Unit &u, int tile, int &page, int &place) {
+                    find(u, static_cast<uint32_t>(u.k0 + tile) * kChunkKeys + lane * box, page, place);
+                };
+                // The page and place of the lane's box if it is one of the tile's, else place
+                // -1; on to the next tile.
+                auto take = [&](const Unit &u, Places &p, int tile, int &page, int &place) {
+                    page = p.page;
+                    place = (tile & (tiles - 1)) == lane_tile ? p.place : -1;
+                    if (((tile + 1) & (tiles - 1)) == 0) {
+                        p.page = p.page1;
+                        p.place = p.place1;
+                        look(u, tile + 1 + tiles, p.page1, p.place1);
+                    }
+                };
                 uint32_t copied = 0;
                 while (const Unit *const next = next_unit(++ordinal)) {
-                    const Unit &u = *next;
+                    const Unit u = *next;               // (in registers: not read again behind every barrier)
                     Tiles t(u);
-                    if (t.more()) find(u, (u.k0 + t.tile()) * kChunkKeys + lane * box, page, place);
+                    look(u, 0, of_k.page, of_k.place);
+                    look(u, tiles, of_k.page1, of_k.place1);
+                    of_v = of_k;
 #pragma unroll 1
                     while (t.more()) {
-                        const bool is_v = t.is_v(), in = lane < boxes && usable(page, place);
-                        const int key0 = (u.k0 + t.tile()) * kChunkKeys, pg = page, pl = place;
+                        const bool is_v = t.is_v();
+                        const int tile = t.tile(), key0 = (u.k0 + tile) * kChunkKeys;
+                        int page, place;
+                        if (is_v) take(u, of_v, tile, page, place);
+                        else take(u, of_k, tile, page, place);
+                        const bool in = usable(page, place);
                         t.next();
-                        if (t.more()) find(u, (u.k0 + t.tile()) * kChunkKeys + lane * box, page, place);
 #pragma unroll
                         for (int hh = 0; hh < HV; ++hh) {
                             wait(&raw_empty[raw.i], raw.phase ^ 1);
-                            copy(u, is_v, key0, pg, pl, in, hh * SC, raw0 + raw.i * (G::kStage / 2), SC, &raw_full[raw.i]);
+                            copy(u, is_v, key0, lane_box, page, place, in, hh * SC, raw0 + raw.i * (G::kStage / 2), SC, &raw_full[raw.i]);
                             raw.next(G::kRaw);
                             ++copied;
                         }
@@ -703,7 +728,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 const uint32_t at0 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row, (ch & 3) * 2);
                 const uint32_t at1 = (ch >> 2) * (kChunkKeys * 128) + sw128_offset(row + RP, (ch & 3) * 2);
                 while (const Unit *const next = next_unit(++ordinal)) {
-                    const Unit &u = *next;
+                    const Unit u = *next;
                     load_q(u, ordinal);
                     Tiles t(u);
 #pragma unroll 1
@@ -766,6 +791,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             }
         } else {
             uint32_t guard_phase = 0, filled = 0;
+            int page = 0, place = -1;                        // of the lane's box of the next tile
             while (const Unit *const next = next_unit(++ordinal)) {
                 const Unit &u = *next;
                 Tiles t(u);
@@ -790,7 +816,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                         const bool part = lw * 64 < SC && d0 < D;
                         const uint32_t dst = smem_u32(stages) + to.i * G::kStage + lw * (kChunkKeys * 128);
                         wait(&empty[to.i], to.phase ^ 1);
-                        if (part) copy(u, is_v, key0, pg, pl, in, d0, dst, 128, guard ? raw_full : &full[to.i]);
+                        if (part) copy(u, is_v, key0, lane, pg, pl, in, d0, dst, 128, guard ? raw_full : &full[to.i]);
                         else if (lane == 0) mbar_arrive(guard ? raw_full : &full[to.i]);
                         if (guard) {
                             wait(raw_full, guard_phase);

@@ -49,6 +49,7 @@ constexpr int chunk_rows(int padded_dim) { return padded_dim <= 128 ? 256 : 128;
 // A unit's fixed time (Q, start, turnaround, stores) in tokens of its keys: some
 // 5000 cycles of the 2750 that a tile of 128 takes.
 constexpr int64_t kChunkUnitCost = 256;
+constexpr int64_t kChunkNarrowCost = 384;      // that of one with both slots on the same rows, above it
 // Floats of a piece: output, maximum, sum of every row.
 constexpr size_t chunk_piece_floats(int padded_dim) { return static_cast<size_t>(chunk_rows(padded_dim)) * (padded_dim + 2); }
 constexpr size_t chunk_workspace_bytes(int dim)

@@ -66,9 +66,11 @@ __host__ __device__ __forceinline__ Sequence sequence_at(const ChunkArgs &a, int
 }
 
 // Costs of a sequence's units for one KV head: unit i costs lin + R (i + 1), in
-// keys times G (so that all sequences count alike); a narrow one by itself 7/8 of
-// that (half the products, but as many bytes: 16 sequences that decode beside three
-// chunks took 128 us with it, 134 with 1, 149 with 5/8, 170 with a half).
+// keys times G (so that all sequences count alike). A narrow one by itself costs 7/8 of
+// that (half the products, but as many bytes) with a larger fixed part, as both slots have to
+// be joined (4 new tokens of 32 sequences over an e4m3 cache: 188 us with none more, 166
+// with 384 keys' time; 16 sequences that decode beside three chunks: 117 us, with 768
+// 125; with a factor of 1 122).
 struct Costs {
     int64_t lin, head;
     int T, R;
@@ -80,6 +82,7 @@ struct Costs {
         T = static_cast<int>((rows + static_cast<uint32_t>(R) - 1) / static_cast<uint32_t>(R));
         lin = group * (static_cast<int64_t>(most(s.len - s.n, 0)) + kChunkUnitCost);
         narrow = two_slots && rows <= 128;
+        if (narrow) lin += group * kChunkNarrowCost;
         head = before(T);
     }
     __host__ __device__ __forceinline__ int64_t before(int i) const

@@ -41,7 +41,7 @@ extern "C" {
  * head_dim a multiple of 8 up to AWQ_ATTN_MAX_HEAD_DIM. Sizes that the 32-bit
  * rows and 64-bit costs of the split cannot hold are refused: with G = q_heads /
  * kv_heads, tokens * G has to be at most 2^31 - 256, and with the longest
- * context L (here: tokens) and u = G * (L + tokens + 256) + 512, both u * (L /
+ * context L (here: tokens) and u = G * (L + tokens + 640) + 512, both u * (L /
  * 128 + 1) and u * (tokens * G / 120 + 1) * kv_heads * batch at most 4 * 10^18.
  * Work is split over the rows, and over the keys where that alone does not fill
  * the card, by the lengths on the device; the parts are joined in the same
