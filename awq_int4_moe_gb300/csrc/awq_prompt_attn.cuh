@@ -1284,13 +1284,20 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             __syncwarp();
             if (lane == 0) done_with(ordinal);
         }
-        // ---- the cut units: each of the blocks that share one joins a part of it
-        for (int which = 0; which < 2; ++which) {
-            if (!(has_shared >> which & 1)) continue;
-            int16_t *const list = reinterpret_cast<int16_t *>(s_ml);         // [kChunkMaxCtas], then place, number, first
-            Unit *const kept = reinterpret_cast<Unit *>(smem + G::oMl + 1024);
-            meet();
-            if (warp == 0) {
+        // ---- the cut units: each of the blocks that share one joins a part of it. It is a
+        // chain of waits for L2: where the block has two, each warpgroup has one.
+        meet();                                                              // (all tiles are read: shared memory is free)
+        if (has_shared) {
+            const bool two = has_shared == 3;
+            const int at_once = two ? 128 : 256, me_tid = two ? tid & 127 : tid;
+            const int which = two ? w : has_shared >> 1;
+            int16_t *const list = reinterpret_cast<int16_t *>(smem + G::oMl + (two ? w * 1024 : 0));   // [kChunkMaxCtas], then place, number, first
+            Unit *const kept = reinterpret_cast<Unit *>(smem + G::oMl + (two ? w * 1024 : 0) + 512);
+            auto join_sync = [&]() {
+                if (two) named_barrier_sync(1 + w, 128);
+                else meet();
+            };
+            if (me_tid < 32) {
                 if (lane >> 4 == which) reinterpret_cast<uint32_t *>(kept)[lane & 15] = shared_unit;
                 __syncwarp();
                 int me, count;
@@ -1308,22 +1315,23 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     if (!ok) list[kChunkMaxCtas + 1] = 0;
                 }
             }
-            meet();
-            ok = ok && list[kChunkMaxCtas + 1] > 0;
-            if (!ok) continue;
+            join_sync();
             const Unit v = *kept;
-            const int me = list[kChunkMaxCtas], count = list[kChunkMaxCtas + 1], begun = list[kChunkMaxCtas + 2];
-            const int rows = v.rows, items = rows * (D / 8);
-            const int lo = static_cast<int>(static_cast<int64_t>(items) * me / count);
-            const int hi = static_cast<int>(static_cast<int64_t>(items) * (me + 1) / count);
+            // (after a time-out: no parts, and nothing to do but to meet)
+            const int me = list[kChunkMaxCtas], count = ok ? list[kChunkMaxCtas + 1] : 0, begun = list[kChunkMaxCtas + 2];
+            const int rows = count ? v.rows : 0, items = rows * (D / 8);
+            const int lo = count ? static_cast<int>(static_cast<int64_t>(items) * me / count) : 0;
+            const int hi = count ? static_cast<int>(static_cast<int64_t>(items) * (me + 1) / count) : 0;
             auto part = [&](int i, int r) {                                  // of the i-th block: row r's tile
                 return a.parts + (static_cast<int64_t>(list[i]) * 2 + (i == 0 ? 1 : 0)) * chunk_piece_floats(DP) +
                        (r >> 7) * static_cast<int64_t>(chunk_piece_floats(DP) / QT);
             };
-            // the parts' weights, a row a thread (the stages are free by now)
-            float *const weights = reinterpret_cast<float *>(stages);        // [part][256]
-            if (tid < rows) {
-                const int r = tid;
+            // the parts' weights, a row a thread: [part][256], the second unit's from the
+            // other end (all parts of both are no more than the blocks and one)
+            static_assert((kChunkMaxCtas + 1) * 256 * sizeof(float) <= G::oMl, "weights of the parts");
+            float *const weights = reinterpret_cast<float *>(smem + (two && w == 1 ? G::oMl - 1024 : 0));
+            const int next_part = two && w == 1 ? -256 : 256;
+            for (int r = me_tid; r < rows; r += at_once) {
                 float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
                 for (int i = 0; i < count; ++i) top = fmaxf(top, __ldcg(part(i, r) + 128 * DP + (r & 127)));
@@ -1332,21 +1340,21 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 for (int i = 0; i < count; ++i) {
                     const float *const ml = part(i, r) + 128 * DP + (r & 127);
                     const float w = ex2(__ldcg(ml) - ref);
-                    weights[i * 256 + r] = w;
+                    weights[i * next_part + r] = w;
                     sum += __ldcg(ml + 128) * w;
                 }
                 const float inv = sum == 0.f ? 0.f : a.cache.v.scale / sum;
-                for (int i = 0; i < count; ++i) weights[i * 256 + r] *= inv;
+                for (int i = 0; i < count; ++i) weights[i * next_part + r] *= inv;
                 if (me == 0 && a.lse) {
                     const uint32_t at = v.row0 + r, tok = at / static_cast<uint32_t>(a.group), g = at - tok * a.group;
                     a.lse[(static_cast<int64_t>(v.q0) + tok) * a.q_heads + static_cast<int64_t>(v.h) * a.group + g] =
                         sum == 0.f ? -INFINITY : (top + log2f(sum)) * kChunkLn2;
                 }
             }
-            meet();
+            join_sync();
             constexpr int IT = 4;                                            // items of a thread at a time
 #pragma unroll 1
-            for (int base = lo + tid; base < hi; base += IT * 256) {
+            for (int base = lo + me_tid; base < hi; base += IT * at_once) {
                 float f[IT][8];
 #pragma unroll
                 for (int k = 0; k < IT; ++k)
@@ -1357,15 +1365,15 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     float4 x[IT], y[IT];
 #pragma unroll
                     for (int k = 0; k < IT; ++k) {
-                        const int item = min(base + k * 256, hi - 1), chunk = item / rows, r = item - chunk * rows;
+                        const int item = min(base + k * at_once, hi - 1), chunk = item / rows, r = item - chunk * rows;
                         const float4 *const p = reinterpret_cast<const float4 *>(part(i, r)) + 2 * chunk * 128 + (r & 127);
                         x[k] = __ldcg(p);
                         y[k] = __ldcg(p + 128);
                     }
 #pragma unroll
                     for (int k = 0; k < IT; ++k) {
-                        const int item = min(base + k * 256, hi - 1), r = item % rows;
-                        const float by = weights[i * 256 + r];
+                        const int item = min(base + k * at_once, hi - 1), r = item % rows;
+                        const float by = weights[i * next_part + r];
                         const float z[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
 #pragma unroll
                         for (int e = 0; e < 8; ++e) f[k][e] += z[e] * by;
@@ -1373,7 +1381,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 }
 #pragma unroll
                 for (int k = 0; k < IT; ++k) {
-                    const int item = base + k * 256;
+                    const int item = base + k * at_once;
                     if (item >= hi) break;
                     const int chunk = item / rows, r = item - chunk * rows;
                     const uint32_t at = v.row0 + r, tok = at / static_cast<uint32_t>(a.group), g = at - tok * a.group;
@@ -1382,8 +1390,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 }
             }
             // the last block to leave makes the counters ready for the next call
-            meet();
-            if (tid == 0 && ok && atomic_add_acq_rel(a.counters + 2 * begun + 1, 1) == count - 1) {
+            join_sync();
+            if (me_tid == 0 && count && atomic_add_acq_rel(a.counters + 2 * begun + 1, 1) == count - 1) {
                 a.counters[2 * begun] = 0;
                 a.counters[2 * begun + 1] = 0;
             }
