@@ -44,6 +44,7 @@ awq_status chunk_call(ChunkArgs &a, int32_t dtype, float scale, void *workspace,
             }
         }
     }
+    a.narrow_cost = fp8 ? kChunkNarrowCost : 0;
     // rows of a KV head are counted in 32 bits, costs (and products of them) in 64
     const double G = a.group, rows = static_cast<double>(a.tokens) * G, R = a.unit_rows;
     if (rows > 0x7fffff00) return AWQ_ERR_UNSUPPORTED_SHAPE;

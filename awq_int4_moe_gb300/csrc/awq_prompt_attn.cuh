@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         for (int b = lo; b < hi; ++b) {
             const Sequence s = sequence_at(a, b);
             if (s.bad && blockIdx.x == 0) set_status(a.status, AWQ_ERR_BAD_INDEX);
-            mine += Costs(s, a.group, a.unit_rows, QT == 2).head * a.cache.num_heads;
+            mine += Costs(s, a, QT == 2).head * a.cache.num_heads;
         }
         int64_t incl = mine;
 #pragma unroll
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         if (x0 < x1 && x0 >= before && x0 < before + mine) {
             int b = lo;
             for (;; ++b) {
-                const int64_t c = Costs(sequence_at(a, b), a.group, a.unit_rows, QT == 2).head * a.cache.num_heads;
+                const int64_t c = Costs(sequence_at(a, b), a, QT == 2).head * a.cache.num_heads;
                 if (x0 < before + c) break;
                 before += c;
             }

@@ -25,6 +25,7 @@ struct ChunkArgs {
     int32_t page_shift;
     int32_t box;                   // keys of one copy: the largest power of two up to 128 that divides a page
     int32_t unit_rows;             // packed rows of a unit: of whole tokens where one has no more
+    int32_t narrow_cost;           // kChunkNarrowCost or 0
     int32_t q_box;                 // tokens of one copy of Q; 0: Q is copied row by row
     int32_t head_step[2], page_step[2];    // of K and V: 0 where the plane's stride is 0, else 1
     float factor;                  // |scale| * log2(e) * K's scale
@@ -49,7 +50,7 @@ constexpr int chunk_rows(int padded_dim) { return padded_dim <= 128 ? 256 : 128;
 // A unit's fixed time (Q, start, turnaround, stores) in tokens of its keys: some
 // 5000 cycles of the 2750 that a tile of 128 takes.
 constexpr int64_t kChunkUnitCost = 256;
-constexpr int64_t kChunkNarrowCost = 384;      // that of one with both slots on the same rows, above it
+constexpr int kChunkNarrowCost = 384;          // over e4m3 more for one with both slots on the same rows
 // Floats of a piece: output, maximum, sum of every row.
 constexpr size_t chunk_piece_floats(int padded_dim) { return static_cast<size_t>(chunk_rows(padded_dim)) * (padded_dim + 2); }
 constexpr size_t chunk_workspace_bytes(int dim)

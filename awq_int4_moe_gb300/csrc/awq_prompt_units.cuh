@@ -67,22 +67,22 @@ __host__ __device__ __forceinline__ Sequence sequence_at(const ChunkArgs &a, int
 
 // Costs of a sequence's units for one KV head: unit i costs lin + R (i + 1), in
 // keys times G (so that all sequences count alike). A narrow one by itself costs 7/8 of
-// that (half the products, but as many bytes) with a larger fixed part, as both slots have to
-// be joined (4 new tokens of 32 sequences over an e4m3 cache: 188 us with none more, 166
-// with 384 keys' time; 16 sequences that decode beside three chunks: 117 us, with 768
-// 125; with a factor of 1 122).
+// that (half the products, but as many bytes: 16 sequences that decode beside three
+// chunks 117 us, with a factor of 1 122), over e4m3 with a larger fixed part, as its
+// first tiles wait for their expansion (4 new tokens of 32 sequences 188 us with none
+// more, 166 with 384 keys' time, 165 with 768, and 16 sequences beside chunks then 125; over
+// 16 bits it changes nothing there and costs 40 short prompts 87 -> 91 us).
 struct Costs {
     int64_t lin, head;
     int T, R;
     bool narrow;
     __host__ __device__ __forceinline__ Costs() {}
-    __host__ __device__ __forceinline__ Costs(const Sequence &s, int group, int unit_rows, bool two_slots) : R(unit_rows)
+    __host__ __device__ __forceinline__ Costs(const Sequence &s, const ChunkArgs &a, bool two_slots) : R(a.unit_rows)
     {
-        const uint32_t rows = static_cast<uint32_t>(s.n) * static_cast<uint32_t>(group);     // (below 2^31: the host has checked)
+        const uint32_t rows = static_cast<uint32_t>(s.n) * static_cast<uint32_t>(a.group);     // (below 2^31: the host has checked)
         T = static_cast<int>((rows + static_cast<uint32_t>(R) - 1) / static_cast<uint32_t>(R));
-        lin = group * (static_cast<int64_t>(most(s.len - s.n, 0)) + kChunkUnitCost);
         narrow = two_slots && rows <= 128;
-        if (narrow) lin += group * kChunkNarrowCost;
+        lin = a.group * (static_cast<int64_t>(most(s.len - s.n, 0)) + kChunkUnitCost + (narrow ? a.narrow_cost : 0));
         head = before(T);
     }
     __host__ __device__ __forceinline__ int64_t before(int i) const
@@ -106,7 +106,7 @@ struct UnitWalk {
             at = x1;                                    // no share: no units
             return;
         }
-        const Costs c(sequence_at(a, b), a.group, a.unit_rows, TWO_SLOTS);
+        const Costs c(sequence_at(a, b), a, TWO_SLOTS);
         h = static_cast<int>(short_div(x0 - at, c.head));
         at += h * c.head;
         // the last unit that begins at or before x0
@@ -126,7 +126,7 @@ struct UnitWalk {
 #pragma unroll 1
         while (at < x1) {
             const Sequence s = sequence_at(a, b);
-            const Costs c(s, a.group, a.unit_rows, TWO_SLOTS);
+            const Costs c(s, a, TWO_SLOTS);
             if (t == c.T) {                             // (units remain, as costs do)
                 t = 0;
                 if (++h == a.cache.num_heads || c.T == 0) {

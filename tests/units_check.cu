@@ -35,7 +35,7 @@ template <bool TWO>
 void check(int id, const ChunkArgs &a, int grid)
 {
     int64_t total = 0;
-    for (int b = 0; b < a.batch; ++b) total += Costs(sequence_at(a, b), a.group, a.unit_rows, TWO).head * a.cache.num_heads;
+    for (int b = 0; b < a.batch; ++b) total += Costs(sequence_at(a, b), a, TWO).head * a.cache.num_heads;
     const int64_t per = share_of(total, grid);
     std::map<std::tuple<int, int, int>, Taken> seen;
     for (int c = 0; c < grid; ++c) {
@@ -44,7 +44,7 @@ void check(int id, const ChunkArgs &a, int grid)
         int64_t before = 0;
         if (x0 < x1)
             for (;; ++first) {
-                const int64_t cost = Costs(sequence_at(a, first), a.group, a.unit_rows, TWO).head * a.cache.num_heads;
+                const int64_t cost = Costs(sequence_at(a, first), a, TWO).head * a.cache.num_heads;
                 if (x0 < before + cost) break;
                 before += cost;
             }
@@ -121,6 +121,7 @@ int main()
         }
         a.tokens = cu.back();
         a.max_len = longest;
+        a.narrow_cost = id % 2 ? kChunkNarrowCost : 0;
         if (id % 50 == 7) {                      // bounds and lengths that are not what they may be
             cu[a.batch / 2] = between(-5, a.tokens + 5);
             lens[0] = between(0, 1) ? -3 : longest + 9;
