@@ -27,7 +27,8 @@
 // Tensor memory: S (and P over it, 16 bits) 2 x 128 columns, O 2 x 128 or 256.
 //
 // Warps: 0-7 softmax and output, a thread per row (nothing crosses lanes in a
-// step); 8 and 9 issue the MMAs of a slot each; the rest load. Units are found one
+// step); 8 and 9 issue the MMAs of a slot each; the rest load (and make V finite where
+// rows are masked). Units are found one
 // ahead of their use, by warp 9, or over e4m3 by warp 11. All meet at mbarriers, every
 // wait is bounded. Registers go where the scores are (208 or 200 a thread there): with 227 KB
 // of shared memory in use what spills comes back from L2.
@@ -51,12 +52,12 @@
 // chain scores, maximum, exponentials (128 a thread, 4 cycles a warp's
 // instruction) and product of a slot is not quite hidden by the other's. Then a unit's
 // turnaround (its last product, the stores, the next one's Q: 9000 cycles). Narrow
-// units: the bytes of K and V; over e4m3 their expansion (1650 cycles a tile, 32 KB
-// to shared memory). Small calls: launch, scan, and some ten dependent steps.
-// Device time: one prompt of 8192 tokens, 32 heads over 8 of 128, 414 us (1.33
-// PFLOP/s); 1024 tokens over 32768, 388 us; 13 ragged prompts up to 4096, 174 us; 4
-// prompts with heads of 256, 170 us; 4 new tokens for each of 32 sequences over an e4m3
-// cache, 201 us (2.7 TB/s of it); a prompt of 48, 12 us.
+// units: the bytes of K and V (84 % of the copy bandwidth); over e4m3 the warps that copy
+// and expand (some 1200 cycles a tile each). Small calls: launch, scan, and some ten dependent steps.
+// Device time: one prompt of 8192 tokens, 32 heads over 8 of 128, 405 us (1.36
+// PFLOP/s); 1024 tokens over 32768, 388 us; 13 ragged prompts up to 4096, 176 us; 4
+// prompts with heads of 256, 168 us; 4 new tokens for each of 32 sequences over an e4m3
+// cache, 158 us (3.5 TB/s of it); a prompt of 48, 11 us.
 // Tried, and slower: the scores read twice from tensor memory instead of kept in
 // registers, the first weights taken against the old maximum before the new one
 // is known (414 -> 456 us), one issuing warp for both slots (by a fifth),
@@ -89,7 +90,9 @@ constexpr int kWaitTries = 1 << 18;    // 1 to 2 s
 template <int DP, bool FP8>
 struct ChunkGeo {
     // e4m3: 10 copies codes, 11 finds the units, 12-15 expand the codes; else 10 and 11 copy
-    static constexpr int kThreads = FP8 ? 512 : 384, kFillWarp = FP8 ? 12 : 10, kFillWarps = FP8 ? 4 : 2;
+    // 64 columns each, or 10 copies and 11 makes tiles of V finite
+    static constexpr bool kGuardWarp = !FP8 && DP == 64;
+    static constexpr int kThreads = FP8 ? 512 : 384, kFillWarp = FP8 ? 12 : 10, kFillWarps = FP8 ? 4 : kGuardWarp ? 1 : 2;
     static constexpr int QT = DP <= 128 ? 2 : 1;            // row tiles of a unit
     static constexpr int R = 128 * QT;
     static constexpr int SC = DP < 128 ? DP : 128;          // columns of a stage
@@ -103,7 +106,8 @@ struct ChunkGeo {
     // after Q and the stages: maxima and sums that two slots exchange, rows' powers of two, barriers
     static constexpr int oStages = kQ, oRaw = oStages + kStages * kStage, oMl = oRaw + kRaw * kStage / 2, oExp = oMl + 2 * 128 * 8,
                          oUnits = oExp + 2 * 256, oBars = oUnits + kUnits * 64,
-                         kRawBars = FP8 ? kRaw : 1, kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 3 + 2 * kUnits + 2 * kRawBars,
+                         kRawBars = FP8 ? kRaw : kGuardWarp ? kStages : 1,
+                         kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 3 + 2 * kUnits + 2 * kRawBars,
                          oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
     static constexpr uint32_t kTmemO = 256;                 // first column of O; S at 0 and 128
     static_assert(kSmem <= 227 * 1024, "shared memory of a block");
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
     uint64_t *const drain = o_done + 2;
     uint64_t *const both = drain + 2;                                        // both softmax warpgroups
     uint64_t *const u_full = drain + 3, *const u_empty = u_full + kUnits;    // [kUnits]
-    uint64_t *const raw_full = u_empty + kUnits, *const raw_empty = raw_full + G::kRawBars;   // codes; one for guarded tiles
+    uint64_t *const raw_full = u_empty + kUnits, *const raw_empty = raw_full + G::kRawBars;   // codes; tiles to be made finite
     Unit *const s_unit = reinterpret_cast<Unit *>(smem + G::oUnits);
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + G::oMisc);
     int *const s_first = reinterpret_cast<int *>(smem + G::oMisc + 4);
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&full[i], FW);
+            mbar_init(&full[i], FP8 ? FW : 2);
             mbar_init(&empty[i], QT);            // the issuers
         }
         mbar_init(q_full, kScaledQ || !a.q_box ? 32 * FW : 1);
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         mbar_init(both, 8);
         for (int i = 0; i < G::kRawBars; ++i) {
-            mbar_init(&raw_full[i], FP8 ? 1 : 2);
+            mbar_init(&raw_full[i], FP8 || G::kGuardWarp ? 1 : 2);
             mbar_init(&raw_empty[i], FW);
         }
         for (int i = 0; i < kUnits; ++i) {
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         while (make_unit(walk, made) && ok) ++made;
     } else if (warp >= kLoaderWarp) {
         // ------------------------------------------------------- loader
-        const int lw = warp - G::kFillWarp;
+        const int lw = FW == 1 ? 0 : warp - G::kFillWarp;
         // ---- Q of a unit, 16 bytes a thread: RP rows of CH chunks a warp and turn, so a
         // thread's rows are as far apart as the warps reach and its token and head go on by additions.
         auto load_q = [&](const Unit &u, int ordinal) {
@@ -661,6 +665,31 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
 
         Ring to;                                             // the next stage to fill
         int ordinal = 0;
+        // 64 columns of a V tile in 16 bits, made finite from a key on (a multiple of 4 B);
+        // then the stage's arrival. B loads are in flight.
+        auto make_finite = [&](uint32_t tile, int from, uint64_t *bar) {
+            constexpr int B = G::kGuardWarp ? 4 : 8;
+#pragma unroll 1
+            for (int key = from; key < kChunkKeys; key += 4 * B) {
+                const uint32_t at = tile + key * 128 + lane * 16;
+                uint4 v[B];
+#pragma unroll
+                for (int k = 0; k < B; ++k) v[k] = lds_v4(at + k * 512);
+                uint32_t bad = 0;
+#pragma unroll
+                for (int k = 0; k < B; ++k) bad |= not_finite4<C>(v[k]);
+                if (bad) {
+                    s_bad[ordinal & 3] = ordinal;
+#pragma unroll
+                    for (int k = 0; k < B; ++k)
+                        sts_v4(at + k * 512, make_uint4(finite_pair<C>(v[k].x), finite_pair<C>(v[k].y), finite_pair<C>(v[k].z),
+                                                        finite_pair<C>(v[k].w)));
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
         if constexpr (FP8) {
             // One warp copies codes, up to kRaw stages ahead; four expand them, a row's 16
             // codes a thread.
@@ -789,7 +818,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     if (lane == 0) done_with(ordinal);
                 }
             }
-        } else {
+        } else if (!G::kGuardWarp || warp == kLoaderWarp) {
             uint32_t guard_phase = 0, filled = 0;
             int page = 0, place = -1;                        // of the lane's box of the next tile
             while (const Unit *const next = next_unit(++ordinal)) {
@@ -813,35 +842,18 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     for (int hh = 0; hh < HV; ++hh) {
                         // a warp copies 64 columns
                         const int d0 = hh * SC + lw * 64;
-                        const bool part = lw * 64 < SC && d0 < D;
+                        const bool part = G::kGuardWarp || d0 < D;
                         const uint32_t dst = smem_u32(stages) + to.i * G::kStage + lw * (kChunkKeys * 128);
+                        uint64_t *const bar = !guard ? &full[to.i] : G::kGuardWarp ? &raw_full[to.i] : raw_full;
                         wait(&empty[to.i], to.phase ^ 1);
-                        if (part) copy(u, is_v, key0, lane, pg, pl, in, d0, dst, 128, guard ? raw_full : &full[to.i]);
-                        else if (lane == 0) mbar_arrive(guard ? raw_full : &full[to.i]);
-                        if (guard) {
+                        if (part) copy(u, is_v, key0, lane, pg, pl, in, d0, dst, 128, bar);
+                        else if (lane == 0) mbar_arrive(bar);
+                        if (G::kGuardWarp) {
+                            if (lane == 0) mbar_arrive(&full[to.i]);     // (the other arrival is the bytes' or the next warp's)
+                        } else if (guard) {
                             wait(raw_full, guard_phase);
                             guard_phase ^= 1;
-                            if (part) {
-#pragma unroll 1
-                                for (int i = 0; i < kChunkKeys * 8 / 32; i += 8) {
-                                    uint4 v[8];
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k) v[k] = lds_v4(dst + lane * 16 + (i + k) * 512);
-                                    uint32_t bad = 0;
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k) bad |= not_finite4<C>(v[k]);
-                                    if (bad) {
-                                        s_bad[ordinal & 3] = ordinal;
-#pragma unroll
-                                        for (int k = 0; k < 8; ++k)
-                                            sts_v4(dst + lane * 16 + (i + k) * 512, make_uint4(finite_pair<C>(v[k].x), finite_pair<C>(v[k].y),
-                                                                                              finite_pair<C>(v[k].z), finite_pair<C>(v[k].w)));
-                                    }
-                                }
-                            }
-                            fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&full[to.i]);
+                            make_finite(dst, part ? 0 : kChunkKeys, &full[to.i]);
                         }
                         to.next(NST);
                         ++filled;
@@ -854,6 +866,27 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             if (!ok)
                 for (uint32_t i = filled > NST ? filled - NST : 0; i < filled; ++i)
                     mbar_wait_bounded(&full[i % NST], i / NST & 1, a.timeout_ns);
+        } else {
+            // Makes the guarded tiles of V finite: done by the warp that copies, each holds
+            // the next unit's Q and K back by 4000 cycles (40 short prompts with heads of 64
+            // 86 -> 79 us, 64 sequences that decode 157 -> 148). Larger heads keep both
+            // warps for the copies (1024 tokens over pages of 32 388 us, with one 404).
+            uint32_t base = 0, phases = 0;                   // the unit's first filling; a bit per stage
+            while (const Unit *const next = next_unit(++ordinal)) {
+                const Unit &u = *next;
+                const int n = u.k1 - u.k0, k0 = u.k0, all0 = u.all0, ahead = QT == 2 && u.rows > 128 ? 1 : 2;
+#pragma unroll 1
+                for (int j = max(0, all0 / kChunkKeys - k0); j < n; ++j) {
+                    const uint32_t st = (base + j + min(n, j + ahead)) % NST;
+                    wait(&raw_full[st], phases >> st & 1);
+                    phases ^= 1u << st;
+                    // its keys that some row does not see, from a multiple of 16 on
+                    make_finite(smem_u32(stages) + st * G::kStage, max(0, all0 - (k0 + j) * kChunkKeys) & ~15, &full[st]);
+                }
+                base += 2 * n;
+                __syncwarp();
+                if (lane == 0) done_with(ordinal);
+            }
         }
         cp_async_commit();
         cp_async_wait_group<0>();

@@ -24,8 +24,8 @@ extern "C" {
  *   s[i][j] = scale * (q[i] . k[j]),  j <= i
  *   out[i] = sum_j softmax(s[i])[j] v[j],  lse[i] = log(sum_j exp(s[i][j]))
  * scale is any finite number. What a row does not see does not reach it, NaN and
- * infinities among it; a value of v that is not finite makes its element of out
- * NaN in every row that sees it. A row whose scores are all -infinity has out =
+ * infinities among it; a value of v that is not finite leaves its element of out
+ * not finite in every row that sees it. A row whose scores are all -infinity has out =
  * 0 and lse = -infinity. Held in fewer than 32 bits: a weight, which enters the
  * product with v in the type of q (fp16: off by at most 2^-11 of it or 2^-32 of
  * the largest one; bf16: 2^-8 of it); the sum that it is divided by takes it in fp32.
