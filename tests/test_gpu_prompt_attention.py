@@ -417,3 +417,54 @@ def test_cache_past_32_bit_offsets():
     want, _, _ = c.call()
     got, lse, st = c.call(k_cache=big[0], v_cache=big[1], page_table=far[None].int())
     assert st == 0 and bool((got == want).all())
+
+
+@pytest.mark.parametrize("kind,cache", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_values_that_some_rows_do_not_see_in_cut_units(kind, cache, dim):
+    """Long contexts, cut between blocks, and one that is not: the last token's value
+    and all places behind it not finite. Only the last token's rows see that, the
+    others keep every bit."""
+    t = torch()
+    c = Case([9000, 20000, 130, 257], [3, 200, 130, 1], 8, 2, dim, kind, cache, page=16, seed=dim)
+    before, lse, st = c.call()
+    assert st == 0
+    c.check(before, lse)
+    bad = t.full((), math.nan, device="cuda").to(c.vc.dtype)
+    last = []
+    for b, n in enumerate(c.lens):
+        page, place = int(c.table[b, (n - 1) // 16]), (n - 1) % 16
+        c.vc[page, place, :, 5:9] = bad
+        c.vc[page, place + 1:] = bad
+        c.kc[page, place + 1:] = bad
+        last.append(c.cu[b + 1] - 1)
+    out, lse2, st = c.call()
+    assert st == 0 and t.equal(lse, lse2)
+    rows = t.zeros(c.rows, dtype=t.bool, device="cuda")
+    rows[last] = True
+    assert t.equal(out[~rows], before[~rows])
+    assert bool(out[rows][:, :, 5:9].isnan().all())
+    keep = t.ones(dim, dtype=t.bool, device="cuda")
+    keep[5:9] = False
+    assert t.equal(out[rows][:, :, keep], before[rows][:, :, keep])
+
+
+@pytest.mark.parametrize("cache", [None, "f16"])
+def test_rows_before_the_first_sequence_and_repeated_heads_of_q(cache):
+    """Bounds that begin past 0 leave the rows before them; a query that is the same
+    for all heads, by a stride of 0."""
+    t = torch()
+    c = Case([200, 31], None if cache is None else [40, 31], 4, 2, 128, "f16", cache, seed=3)
+    shift = 7
+    c.q = c.q[:, :1].expand(-1, 4, -1)
+    want, want_lse, st = c.call()
+    assert st == 0
+    c.check(want, want_lse)
+    pad = lambda x: t.cat([x.new_full((shift,) + x.shape[1:], math.nan), x])  # noqa: E731
+    c.q, c.rows, c.cu_t = pad(c.q), c.rows + shift, c.cu_t + shift
+    if cache is None:
+        c.k, c.v = pad(c.k), pad(c.v)
+    out, lse, st = c.call()
+    assert st == 0 and bool((out[:shift] == 9).all()) and bool((lse[:shift] == 9).all())
+    # (a stride of 0 takes the rows of q one by one, a copy of its own in boxes: the same numbers)
+    assert t.equal(out[shift:], want) and t.equal(lse[shift:], want_lse)
