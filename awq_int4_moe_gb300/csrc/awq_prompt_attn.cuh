@@ -43,7 +43,7 @@
 // Balance. Units are numbered sequence by sequence, head by head, tile by tile;
 // their costs (a unit's keys and a fixed part) have a closed form, and every
 // block takes an equal share of the sum, whatever units it belongs to. A unit
-// that is cut (in whole multiples of kPiece key tiles) leaves its parts in the
+// that is cut (between pairs of key tiles, into pieces of at least kPiece) leaves its parts in the
 // workspace; at the end the blocks that share it wait for the last one and each
 // join a part of its rows, in block order, so the same inputs give the same bits.
 //
@@ -52,11 +52,11 @@
 // chain scores, maximum, exponentials (128 a thread, 4 cycles a warp's
 // instruction) and product of a slot is not quite hidden by the other's. Then a unit's
 // turnaround (its last product, the stores, the next one's Q: 9000 cycles). Narrow
-// units: the bytes of K and V (84 % of the copy bandwidth); over e4m3 the warps that copy
+// units: the bytes of K and V (88 % of the copy bandwidth); over e4m3 the warps that copy
 // and expand (some 1200 cycles a tile each). Small calls: launch, scan, and some ten dependent steps.
 // Device time: one prompt of 8192 tokens, 32 heads over 8 of 128, 405 us (1.36
-// PFLOP/s); 1024 tokens over 32768, 388 us; 13 ragged prompts up to 4096, 176 us; 4
-// prompts with heads of 256, 168 us; 4 new tokens for each of 32 sequences over an e4m3
+// PFLOP/s); 1024 tokens over 32768, 388 us; 13 ragged prompts up to 4096, 174 us; 4
+// prompts with heads of 256, 151 us; 4 new tokens for each of 32 sequences over an e4m3
 // cache, 158 us (3.5 TB/s of it); a prompt of 48, 11 us.
 // Tried, and slower: the scores read twice from tensor memory instead of kept in
 // registers, the first weights taken against the old maximum before the new one
