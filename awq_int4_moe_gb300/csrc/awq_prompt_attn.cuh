@@ -57,7 +57,7 @@
 // Device time: one prompt of 8192 tokens, 32 heads over 8 of 128, 405 us (1.36
 // PFLOP/s); 1024 tokens over 32768, 388 us; 13 ragged prompts up to 4096, 174 us; 4
 // prompts with heads of 256, 151 us; 4 new tokens for each of 32 sequences over an e4m3
-// cache, 158 us (3.5 TB/s of it); a prompt of 48, 11 us.
+// cache, 150 us (3.6 TB/s of it); a prompt of 48, 11 us.
 // Tried, and slower: the scores read twice from tensor memory instead of kept in
 // registers, the first weights taken against the old maximum before the new one
 // is known (414 -> 456 us), one issuing warp for both slots (by a fifth),
@@ -639,18 +639,43 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             const int head = a.head_step[is_v] * u.h, step = a.page_step[is_v];
             const int bytes = box * row_bytes;
             int count = __popc(__ballot_sync(~0u, in));
-            if (boxes > 32) {                                // small and odd pages
+            auto expect = [&]() {
+                if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
+                __syncwarp();
+                if (in) tma_load_4d(dst + lane_box * bytes, map, bar, d0, place, head, step * page);
+            };
+            if (boxes <= 32) {
+                expect();
+                return;
+            }
+            // Pages of a token or two, and odd ones. All of the lane's boxes are asked for at
+            // once where registers allow it (4 new tokens of 32 sequences, pages of one token:
+            // e4m3 1384 -> 1027 us; 16-bit heads above 64 would lose 3 to 8 % on all pages).
+            if constexpr (FP8 || DP == 64) {
+                int pg[3], pl[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    pg[i] = 0;
+                    pl[i] = -1;
+                    if (32 * (i + 1) < boxes) find(u, key0 + (lane + 32 * (i + 1)) * box, pg[i], pl[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (!usable(pg[i], pl[i])) pl[i] = -1;
+                    count += __popc(__ballot_sync(~0u, pl[i] >= 0));
+                }
+                expect();
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (pl[i] >= 0) tma_load_4d(dst + (lane + 32 * (i + 1)) * bytes, map, bar, d0, pl[i], head, step * pg[i]);
+            } else {
 #pragma unroll 1
                 for (int i = lane + 32; i < boxes; i += 32) {
                     int pg, pl;
                     find(u, key0 + i * box, pg, pl);
                     count += __popc(__ballot_sync(~0u, usable(pg, pl)));
                 }
-            }
-            if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
-            __syncwarp();
-            if (in) tma_load_4d(dst + lane_box * bytes, map, bar, d0, place, head, step * page);
-            if (boxes > 32) {
+                expect();
 #pragma unroll 1
                 for (int i = lane + 32; i < boxes; i += 32) {
                     int pg, pl;
