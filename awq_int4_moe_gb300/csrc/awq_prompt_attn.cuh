@@ -1344,8 +1344,13 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         }
         // ---- the cut units: each of the blocks that share one joins a part of it. It is a
         // chain of waits for L2: where the block has two, each warpgroup has one.
-        meet();                                                              // (all tiles are read: shared memory is free)
+        meet();                                                              // (all tiles are read)
         if (has_shared) {
+            // Shared memory is free once the last Q has come, too: nothing above waits for
+            // that of a unit of which nothing is seen, the issuers do before they drain.
+            wait(&drain[0], 0);
+            if (QT == 2) wait(&drain[1], 0);
+            ok = __all_sync(~0u, ok);
             const bool two = has_shared == 3;
             const int at_once = two ? 128 : 256, me_tid = two ? tid & 127 : tid;
             const int which = two ? w : has_shared >> 1;
