@@ -99,8 +99,8 @@ struct ChunkGeo {
     static constexpr int HV = DP / SC;                      // stages of a key tile
     static constexpr int kStage = kChunkKeys * SC * 2;
     static constexpr int kStages = (FP8 ? 96 : 160) * 1024 / kStage;
-    // e4m3 stages on their way to fp16
-    static constexpr int kRaw = FP8 ? 64 * 1024 / (kStage / 2) : 0;
+    // e4m3 stages on their way to fp16, at most
+    static constexpr int kRaw = FP8 ? kChunkCodeBytes / (kStage / 2) : 0;
     static constexpr int kQSub = R * 128;                   // 64 columns of Q
     static constexpr int kQ = DP / 64 * kQSub;
     // after Q and the stages: maxima and sums that two slots exchange, rows' powers of two, barriers
@@ -637,12 +637,12 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                         int row_bytes, uint64_t *bar) {
             const CUtensorMap *const map = is_v ? &map_v : &map_k;
             const int head = a.head_step[is_v] * u.h, step = a.page_step[is_v];
-            const int bytes = box * row_bytes;
+            const int bytes = box * row_bytes, apart = FP8 ? box * code_row_bytes(row_bytes, box) : bytes;
             int count = __popc(__ballot_sync(~0u, in));
             auto expect = [&]() {
                 if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
                 __syncwarp();
-                if (in) tma_load_4d(dst + lane_box * bytes, map, bar, d0, place, head, step * page);
+                if (in) tma_load_4d(dst + lane_box * apart, map, bar, d0, place, head, step * page);
             };
             if (boxes <= 32) {
                 expect();
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 expect();
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
-                    if (pl[i] >= 0) tma_load_4d(dst + (lane + 32 * (i + 1)) * bytes, map, bar, d0, pl[i], head, step * pg[i]);
+                    if (pl[i] >= 0) tma_load_4d(dst + (lane + 32 * (i + 1)) * apart, map, bar, d0, pl[i], head, step * pg[i]);
             } else {
 #pragma unroll 1
                 for (int i = lane + 32; i < boxes; i += 32) {
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 for (int i = lane + 32; i < boxes; i += 32) {
                     int pg, pl;
                     find(u, key0 + i * box, pg, pl);
-                    if (usable(pg, pl)) tma_load_4d(dst + i * bytes, map, bar, d0, pl, head, step * pg);
+                    if (usable(pg, pl)) tma_load_4d(dst + i * apart, map, bar, d0, pl, head, step * pg);
                 }
             }
         };
@@ -720,6 +720,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             // codes a thread.
             constexpr int CH = SC / 16, RP = 32 / CH;
             const uint32_t raw0 = smem_u32(smem + G::oRaw);
+            const uint32_t code_row = code_row_bytes(SC, box), raw_stage = kChunkKeys * code_row;
+            const uint32_t raws = SC == 128 || code_row == SC ? G::kRaw : G::kRaw / 2;
             Ring raw;
             if (warp == kLoaderWarp) {
                 // A lane has a box of one of the next tiles, and the one as many tiles on: a
@@ -763,8 +765,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
 #pragma unroll
                         for (int hh = 0; hh < HV; ++hh) {
                             wait(&raw_empty[raw.i], raw.phase ^ 1);
-                            copy(u, is_v, key0, lane_box, page, place, in, hh * SC, raw0 + raw.i * (G::kStage / 2), SC, &raw_full[raw.i]);
-                            raw.next(G::kRaw);
+                            copy(u, is_v, key0, lane_box, page, place, in, hh * SC, raw0 + raw.i * raw_stage, SC, &raw_full[raw.i]);
+                            raw.next(raws);
                             ++copied;
                         }
                     }
@@ -772,8 +774,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     if (lane == 0) done_with(ordinal);
                 }
                 if (!ok)                                     // as below
-                    for (uint32_t i = copied > G::kRaw ? copied - G::kRaw : 0; i < copied; ++i)
-                        mbar_wait_bounded(&raw_full[i % G::kRaw], i / G::kRaw & 1, a.timeout_ns);
+                    for (uint32_t i = copied > raws ? copied - raws : 0; i < copied; ++i)
+                        mbar_wait_bounded(&raw_full[i % raws], i / raws & 1, a.timeout_ns);
             } else {
                 // Lanes of the second 64 columns take the row beside theirs, whose swizzle has
                 // the other parity, so that neither load nor store hits a bank twice. RP rows
@@ -792,7 +794,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
 #pragma unroll 1
                         for (int hh = 0; hh < HV; ++hh) {
                             const uint32_t tile = smem_u32(stages) + to.i * G::kStage;
-                            const uint32_t from = raw0 + raw.i * (G::kStage / 2) + row * SC + ch * 16;
+                            const uint32_t from = raw0 + raw.i * raw_stage + row * code_row + ch * 16, step = RP * code_row;
                             wait_two(&empty[to.i], to.phase ^ 1, &raw_full[raw.i], raw.phase);
                             // (unrolled where rows alternate between two offsets)
                             auto place_of = [&](int i) { return tile + (RP == 4 && i & 1 ? at1 + (i - 1) * (RP * 128) : at0 + i * (RP * 128)); };
@@ -806,7 +808,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
 #pragma unroll 1
                                 for (int i = 0; i < 32 / RP; ++i) {
                                     uint4 lo, hi;
-                                    expand(lds_v4(from + i * 512), lo, hi);
+                                    expand(lds_v4(from + i * step), lo, hi);
                                     if (not_finite4<C>(lo) | not_finite4<C>(hi)) {
                                         s_bad[ordinal & 3] = ordinal;
                                         lo = make_uint4(finite_pair<C>(lo.x), finite_pair<C>(lo.y), finite_pair<C>(lo.z), finite_pair<C>(lo.w));
@@ -819,12 +821,12 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                                 constexpr int B = 4;                 // loads in flight
                                 uint4 v[B];
 #pragma unroll
-                                for (int i = 0; i < B; ++i) v[i] = lds_v4(from + i * 512);
+                                for (int i = 0; i < B; ++i) v[i] = lds_v4(from + i * step);
 #pragma unroll
                                 for (int i = 0; i < 32 / RP; ++i) {
                                     uint4 lo, hi;
                                     expand(v[i % B], lo, hi);
-                                    if (i + B < 32 / RP) v[i % B] = lds_v4(from + (i + B) * 512);
+                                    if (i + B < 32 / RP) v[i % B] = lds_v4(from + (i + B) * step);
                                     sts_v4(place_of(i), lo);
                                     sts_v4(place_of(i) ^ 16, hi);
                                 }
@@ -836,7 +838,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                                 mbar_arrive(&full[to.i]);
                             }
                             to.next(NST);
-                            raw.next(G::kRaw);
+                            raw.next(raws);
                         }
                     }
                     __syncwarp();

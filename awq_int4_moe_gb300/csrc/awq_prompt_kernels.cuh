@@ -51,6 +51,11 @@ constexpr int chunk_rows(int padded_dim) { return padded_dim <= 128 ? 256 : 128;
 // 5000 cycles of the 2750 that a tile of 128 takes.
 constexpr int64_t kChunkUnitCost = 256;
 constexpr int kChunkNarrowCost = 384;          // over e4m3 more for one with both slots on the same rows
+// e4m3 codes on their way to fp16: their shared memory, and the bytes from one row of a
+// tile to the next. A TMA copy begins on a 128-byte boundary there, so rows of 64 that are
+// copied one by one (pages of an odd size) lie 128 apart, and half as many tiles fit.
+constexpr int kChunkCodeBytes = 64 * 1024;
+__host__ __device__ constexpr int code_row_bytes(int columns, int box) { return columns * box < 128 ? 128 : columns; }
 // Floats of a piece: output, maximum, sum of every row.
 constexpr size_t chunk_piece_floats(int padded_dim) { return static_cast<size_t>(chunk_rows(padded_dim)) * (padded_dim + 2); }
 constexpr size_t chunk_workspace_bytes(int dim)
