@@ -417,10 +417,9 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
     int64_t x0, x1, per_cta;
     {
         int64_t *const scan = reinterpret_cast<int64_t *>(stages);           // [16], before any tile
-        const int per = (a.batch + kThreads - 1) / kThreads;
-        const int lo = min(a.batch, tid * per), hi = min(a.batch, lo + per);
+        const Span span = sequences_of(a.batch, tid, kThreads);
         int64_t mine = 0;
-        for (int b = lo; b < hi; ++b) {
+        for (int b = span.lo; b < span.hi; ++b) {
             const Sequence s = sequence_at(a, b);
             if (s.bad && blockIdx.x == 0) set_status(a.status, AWQ_ERR_BAD_INDEX);
             mine += Costs(s, a, QT == 2).head * a.cache.num_heads;
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         x0 = min(total, per_cta * blockIdx.x);
         x1 = min(total, x0 + per_cta);
         if (x0 < x1 && x0 >= before && x0 < before + mine) {
-            int b = lo;
+            int b = span.lo;
             for (;; ++b) {
                 const int64_t c = Costs(sequence_at(a, b), a, QT == 2).head * a.cache.num_heads;
                 if (x0 < before + c) break;

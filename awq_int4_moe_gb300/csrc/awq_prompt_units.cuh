@@ -69,6 +69,20 @@ __host__ __device__ __forceinline__ Sequence sequence_at(const ChunkArgs &a, int
     return s;
 }
 
+// The sequences whose costs one of `threads` threads adds up: lo .. hi - 1 (in 32 bits
+// for every batch that has 32).
+struct Span {
+    int lo, hi;
+};
+__host__ __device__ __forceinline__ Span sequences_of(int batch, int thread, int threads)
+{
+    const int64_t per = batch / threads + (batch % threads != 0), lo = thread * per;
+    Span s;
+    s.lo = static_cast<int>(lo < batch ? lo : batch);
+    s.hi = batch - s.lo > per ? static_cast<int>(s.lo + per) : batch;
+    return s;
+}
+
 // Costs of a sequence's units for one KV head: unit i costs lin + R (i + 1), in
 // keys times G (so that all sequences count alike). A narrow one by itself costs 7/8 of
 // that (half the products, but as many bytes: 16 sequences that decode beside three

@@ -30,12 +30,28 @@ void copies()
         }
 }
 
+// Each sequence of a batch is one thread's, up to the largest batch.
+void sequences()
+{
+    for (int threads : {384, 512})
+        for (int batch : {1, 2, 383, 384, 385, 511, 512, 513, 100000, 0x7fffffff - 1000, 0x7fffffff - 383, 0x7fffffff - 1, 0x7fffffff}) {
+            int at = 0;
+            for (int t = 0; t < threads; ++t) {
+                const Span s = sequences_of(batch, t, threads);
+                if (s.lo != at || s.hi < s.lo || s.hi > batch) fail("a thread's sequences", batch, t);
+                at = s.hi;
+            }
+            if (at != batch) fail("sequences of no thread", batch, at);
+        }
+}
+
 }  // namespace
 
 int main(int argc, char **argv)
 {
     const char *const name = argc > 1 ? argv[1] : "";
     if (!std::strcmp(name, "copies")) copies();
+    else if (!std::strcmp(name, "sequences")) sequences();
     else fail("no such check", 0, 0);
     std::puts("ok");
     return 0;

@@ -28,3 +28,7 @@ def check(tmp_path_factory):
 
 def test_copies_begin_on_boundaries(check):
     check("copies")
+
+
+def test_the_largest_batches_are_dealt_to_the_threads(check):
+    check("sequences")
