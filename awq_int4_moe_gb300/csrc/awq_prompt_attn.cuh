@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
     // ---- the sum of all costs, and the first unit of the block's share
     int64_t x0, x1, per_cta;
     {
-        int64_t *const scan = reinterpret_cast<int64_t *>(stages);           // [16], before any tile
+        int64_t *const scan = reinterpret_cast<int64_t *>(s_ml);             // [16], where no copy goes
         const Span span = sequences_of(a.batch, tid, kThreads);
         int64_t mine = 0;
         for (int b = span.lo; b < span.hi; ++b) {
