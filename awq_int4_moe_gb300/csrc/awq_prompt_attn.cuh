@@ -79,9 +79,9 @@ constexpr float kChunkLazy = 8.f;      // a score raises the maximum when it pas
 // fp16 weights are taken against 2^-7 of the maximum: they stay below 2^15 and
 // keep 31 bits below the maximum's own before they vanish.
 constexpr float kChunkRaiseF16 = 7.f;
-// Below every factor that turns a score into a base-2 logarithm: with a factor
-// of 0 a masked score of -infinity would be NaN.
-constexpr float kChunkMinFactor = 1.17549435e-38f;
+// Least factor that turns a score into a base-2 logarithm: with 0 a masked score of
+// -infinity would be NaN. The smallest fp32 makes 2^-21 of the largest score.
+constexpr float kChunkMinFactor = 1.40129846e-45f;
 constexpr float kChunkLn2 = 0.6931471805599453f;
 constexpr int kMmaWarp = 8, kLoaderWarp = 10;
 constexpr int kUnits = 3;              // units in shared memory
