@@ -64,6 +64,7 @@
 // rolled loops over the MMAs, outputs transposed by shuffles before their stores.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -1137,7 +1138,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     factor = a.factor;
                     if constexpr (kScaledQ) factor *= __uint_as_float(static_cast<uint32_t>(
                         max(1, s_exp[(ordinal & 1) * 256 + (wide ? w * 128 : 0) + row] - 112 - 14 + 127)) << 23);
-                    factor = fmaxf(factor, kChunkMinFactor);
+                    // (finite: a score of 0 stays 0)
+                    factor = fminf(fmaxf(factor, kChunkMinFactor), FLT_MAX);
                 }
                 float s[128];
 #pragma unroll
