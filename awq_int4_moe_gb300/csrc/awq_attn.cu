@@ -58,9 +58,10 @@ constexpr float kLazy = 8.f;           // a score raises the maximum when it pas
 // keep 31 bits below the maximum's own before they vanish (with 24, thousands
 // of tokens of a weight of 2^-25 would vanish beside a single large one).
 constexpr float kRaiseF16 = 7.f;
-// Below every factor that turns a score into a base-2 logarithm: with a factor
-// of 0 (a scale of 0) a masked score of -infinity would be NaN.
-constexpr float kMinFactor = 1.17549435e-38f;
+// Least factor that turns a score into a base-2 logarithm: with 0 (a scale of 0) a
+// masked score of -infinity would be NaN. The smallest fp32 makes 2^-21 of the
+// largest score.
+constexpr float kMinFactor = 1.40129846e-45f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
