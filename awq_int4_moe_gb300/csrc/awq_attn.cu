@@ -43,6 +43,7 @@
 // up to 16000, 64 / 8 heads, e4m3: 173 us, 5.9 TB/s; the fixed part (lengths,
 // table, first copies, merge, join) is about 9 us of each.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "awq_decoder_kernels.cuh"
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(Geo<FP8, DP, NT>::kThreads, 1) attn_kernel(con
                         qf[nt][ks][i] = pack2<C>(x.x * down, x.y * down);
                     }
             }
-            f = fmaxf(f, kMinFactor);
+            f = fminf(fmaxf(f, kMinFactor), FLT_MAX);      // (finite: a score of 0 stays 0)
             fac[nt][0] = __shfl_sync(~0u, f, 8 * t4);
             fac[nt][1] = __shfl_sync(~0u, f, 8 * t4 + 4);
         }

@@ -36,3 +36,14 @@ def test_large_products_with_a_small_scale(dim, scale):
     c.q[..., 0] = 2.0 ** 63
     c.kc.copy_(c.kc.sign() * 2.0 ** 63)
     c.check(*decode(c))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_large_queries_and_a_large_scale_over_keys_of_zero(dim):
+    """bf16 queries of 2^120 over an e4m3 cache: their power of two times the scale is
+    past fp32's range, the scores are 0."""
+    c = Case([300, 9], [1, 1], 4, 2, dim, "bf16", "e4m3", seed=dim)
+    c.scale = 2.0 ** 30
+    c.q.fill_(2.0 ** 120)
+    c.kc.copy_(c.kc.float().zero_())
+    c.check(*decode(c))
