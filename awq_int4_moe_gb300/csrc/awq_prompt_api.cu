@@ -12,7 +12,7 @@ namespace awq {
 
 namespace {
 
-constexpr uint64_t kChunkTimeoutNs = 2000000000ull;    // 2 s per device wait
+constexpr uint64_t kChunkTimeoutNs = 1000000000ull;    // 1 s and a block's own time per wait for another block
 
 // What both attention calls have in common, behind their own checks: `a` has
 // q, out, the planes, their index arrays, sizes and max_len.

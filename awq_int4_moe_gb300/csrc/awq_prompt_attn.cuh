@@ -86,7 +86,7 @@ constexpr float kChunkMinFactor = 1.40129846e-45f;
 constexpr float kChunkLn2 = 0.6931471805599453f;
 constexpr int kMmaWarp = 8, kLoaderWarp = 10;
 constexpr int kUnits = 3;              // units in shared memory
-constexpr int kWaitTries = 1 << 18;    // 1 to 2 s
+constexpr int kWaitTries = 1 << 18;    // of 4 to 33 us, as measured: 1 to 9 s
 
 template <int DP, bool FP8>
 struct ChunkGeo {
@@ -108,7 +108,7 @@ struct ChunkGeo {
     static constexpr int oStages = kQ, oRaw = oStages + kStages * kStage, oMl = oRaw + kRaw * kStage / 2, oExp = oMl + 2 * 128 * 8,
                          oUnits = oExp + 2 * 256, oBars = oUnits + kUnits * 64,
                          kRawBars = FP8 ? kRaw : kGuardWarp ? kStages : 1,
-                         kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 3 + 2 * kUnits + 2 * kRawBars,
+                         kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 5 + 2 * kUnits + 2 * kRawBars,
                          oMisc = oBars + kBars * 8, kSmem = oMisc + 40;
     static constexpr uint32_t kTmemO = 256;                 // first column of O; S at 0 and 128
     static_assert(kSmem <= 227 * 1024, "shared memory of a block");
@@ -368,13 +368,15 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
     uint64_t *const o_done = p_full + 2;         // [2]
     uint64_t *const drain = o_done + 2;
     uint64_t *const both = drain + 2;                                        // both softmax warpgroups
-    uint64_t *const u_full = drain + 3, *const u_empty = u_full + kUnits;    // [kUnits]
+    uint64_t *const one = drain + 3;                                         // [2]: each by itself
+    uint64_t *const u_full = drain + 5, *const u_empty = u_full + kUnits;    // [kUnits]
     uint64_t *const raw_full = u_empty + kUnits, *const raw_empty = raw_full + G::kRawBars;   // codes; tiles to be made finite
     Unit *const s_unit = reinterpret_cast<Unit *>(smem + G::oUnits);
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem + G::oMisc);
     int *const s_first = reinterpret_cast<int *>(smem + G::oMisc + 4);
     int64_t *const s_first_at = reinterpret_cast<int64_t *>(smem + G::oMisc + 8);
     int *const s_bad = reinterpret_cast<int *>(smem + G::oMisc + 16);        // [4]
+    uint64_t *const s_start = reinterpret_cast<uint64_t *>(smem + G::oMisc + 32);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
     const int D = a.cache.head_dim;
@@ -397,6 +399,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         mbar_init(both, 8);
+        for (int i = 0; i < 2; ++i) mbar_init(&one[i], 4);
         for (int i = 0; i < G::kRawBars; ++i) {
             mbar_init(&raw_full[i], FP8 || G::kGuardWarp ? 1 : 2);
             mbar_init(&raw_empty[i], FW);
@@ -413,6 +416,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
     if (warp == kMmaWarp) tc_alloc(tmem_slot, 512);
     grid_dependency_wait();
     grid_launch_dependents();
+    if (tid == kThreads - 1) *s_start = global_timer_ns();
 
     // ---- the sum of all costs, and the first unit of the block's share
     int64_t x0, x1, per_cta;
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         __syncthreads();
     }
     const uint32_t tmem = *tmem_slot;
-    // Waits give up after kWaitTries suspensions of some microseconds each; what a
+    // Waits give up after kWaitTries suspensions; what a
     // role does after that is harmless and ends soon, as it waits no more. The status
     // is set once, at the end.
     bool ok = true;
@@ -1359,9 +1363,17 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
             const int which = two ? w : has_shared >> 1;
             int16_t *const list = reinterpret_cast<int16_t *>(smem + G::oMl + (two ? w * 1024 : 0));   // [kChunkMaxCtas], then place, number, first
             Unit *const kept = reinterpret_cast<Unit *>(smem + G::oMl + (two ? w * 1024 : 0) + 512);
+            // Those that join a unit meet; they wait longer than the one that waits for the
+            // other blocks, which may be later by some part of what this block took itself.
+            auto limit = [&]() { return a.timeout_ns + (global_timer_ns() - *s_start); };
+            uint64_t *const joining = two ? &one[w] : both;
+            uint32_t joined = two ? 0 : met;
             auto join_sync = [&]() {
-                if (two) named_barrier_sync(1 + w, 128);
-                else meet();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(joining);
+                if (ok && !mbar_try_wait(joining, joined) && !mbar_wait_bounded(joining, joined, 2 * limit())) ok = false;
+                joined ^= 1;
+                ok = __all_sync(~0u, ok);
             };
             if (me_tid < 32) {
                 if (lane >> 4 == which) reinterpret_cast<uint32_t *>(kept)[lane & 15] = shared_unit;
@@ -1372,13 +1384,13 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     list[kChunkMaxCtas] = static_cast<int16_t>(me);
                     list[kChunkMaxCtas + 1] = static_cast<int16_t>(count);
                     list[kChunkMaxCtas + 2] = static_cast<int16_t>(begun);
-                    const uint64_t t0 = global_timer_ns();
-                    while (ok && ld_acquire_gpu(a.counters + 2 * begun) < count)
-                        if (global_timer_ns() - t0 > a.timeout_ns) {
-                            set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
-                            ok = false;
-                        }
-                    if (!ok) list[kChunkMaxCtas + 1] = 0;
+                    bool late = false;                   // (not `ok`: this warp still meets the others)
+                    if (ok && ld_acquire_gpu(a.counters + 2 * begun) < count) {
+                        const uint64_t t0 = global_timer_ns(), most = limit();
+                        while (!late && ld_acquire_gpu(a.counters + 2 * begun) < count) late = global_timer_ns() - t0 > most;
+                    }
+                    if (late) set_status(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+                    if (!ok || late) list[kChunkMaxCtas + 1] = 0;
                 }
             }
             join_sync();

@@ -30,7 +30,7 @@ struct ChunkArgs {
     int32_t head_step[2], page_step[2];    // of K and V: 0 where the plane's stride is 0, else 1
     float factor;                  // |scale| * log2(e) * K's scale
     int32_t negative;              // the scale is below 0
-    uint64_t timeout_ns;
+    uint64_t timeout_ns;           // of a block's wait for others, beyond the time that it took itself
 };
 
 struct HeadNormArgs {
