@@ -919,6 +919,8 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 if (lane == 0) done_with(ordinal);
             }
         }
+        // (and the last Q that was asked for: of the unit before the one that did not come)
+        if (!ok && warp == G::kFillWarp && ordinal > 1) mbar_wait_bounded(q_full, ordinal & 1, a.timeout_ns);
         cp_async_commit();
         cp_async_wait_group<0>();
     } else if (warp >= kMmaWarp) {
