@@ -48,8 +48,9 @@ awq_status chunk_call(ChunkArgs &a, int32_t dtype, float scale, void *workspace,
     // rows of a KV head are counted in 32 bits, costs (and products of them) in 64
     const double G = a.group, rows = static_cast<double>(a.tokens) * G, R = a.unit_rows;
     if (rows > 0x7fffff00) return AWQ_ERR_UNSUPPORTED_SHAPE;
-    const double most = 4.6e18, unit = G * (static_cast<double>(a.max_len) + kChunkUnitCost + kChunkNarrowCost + a.tokens) + 2 * R;
-    if (unit * (a.max_len / 128 + 1) > most || unit * (rows / R + 1) * a.cache.num_heads * a.batch > most)
+    const double unit = G * (static_cast<double>(a.max_len) + kChunkUnitCost + kChunkNarrowCost + a.tokens) + 2 * R;
+    // (a cost times tiles; the sum of all costs, units of as few as 65 rows, and a block's share more)
+    if (unit * (a.max_len / 128 + 1) > 4.6e18 || unit * (rows / R + 1) * a.cache.num_heads * a.batch > 8.5e18)
         return AWQ_ERR_UNSUPPORTED_SHAPE;
     if (ws_bytes < chunk_workspace_bytes(dim)) return AWQ_ERR_WORKSPACE_TOO_SMALL;
     // copies are boxes of keys that lie in one page wherever they begin
