@@ -84,6 +84,8 @@ inline awq_status rope_args(RopeArgs &a, int &vec, const awq_heads *q, const awq
     r = check_cache(cache, dtype, 1024);
     if (r) return r;
     if (rotary_dim < 0 || rotary_dim > cache->head_dim || rotary_dim % 2) return AWQ_ERR_UNSUPPORTED_SHAPE;
+    // (a token's rows, and the turns of threads past them, are counted in 32 bits)
+    if (static_cast<int64_t>(q_heads) + 2 * static_cast<int64_t>(cache->num_heads) > 0x7fffffff - 2047) return AWQ_ERR_UNSUPPORTED_SHAPE;
     if (tokens == 0) return AWQ_OK;
     for (const awq_heads *h : {q, q_out, k, v}) {
         r = check_heads(h);

@@ -139,7 +139,8 @@ typedef struct {
  * positions i32[tokens]; cos_sin f32[max_positions][rotary_dim], dense,
  * 16-byte aligned; slots i64[tokens]; q, q_out [tokens][q_heads][head_dim],
  * k, v [tokens][cache->num_heads][head_dim]. tokens >= 0 (0 launches
- * nothing); q_heads >= 1; head_dim 1..1024; rotary_dim even, 0..head_dim.
+ * nothing); q_heads >= 1, with twice the cache's num_heads at most 2^31 - 2048;
+ * head_dim 1..1024; rotary_dim even, 0..head_dim.
  */
 AWQ_API awq_status awq_rope_append(const awq_heads *q, const awq_heads *q_out, const awq_heads *k,
                                    const awq_heads *v, const int32_t *positions, const float *cos_sin,

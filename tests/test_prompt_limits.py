@@ -2,7 +2,8 @@
 GPU: a size within them gets as far as the check of the workspace."""
 import pytest
 
-from test_prompt_boundary import SHAPE, SMALL, chunk, prompt
+from test_decoder_boundary import rope
+from test_prompt_boundary import OK, SHAPE, SMALL, chunk, norm, prompt
 import test_prompt_boundary as tb
 
 
@@ -43,3 +44,12 @@ def test_sizes_within_the_limits_of_a_cache_are_taken():
     over = dict(tokens=tokens, batch=batch, q_heads=16, pages=pages, stride=pages, cache=tb.cache(heads=2), ws_bytes=1000)
     assert chunk(**over) == SMALL
     assert chunk(**{**over, "batch": 8 * batch}) == SHAPE
+
+
+@pytest.mark.parametrize("append", [norm, rope])
+def test_rows_of_a_token_that_32_bits_do_not_count(append):
+    most = 2 ** 31 - 2048 - 2 * 2
+    assert append(q_heads=most + 1) == SHAPE
+    assert append(q_heads=2 ** 31 - 1) == SHAPE
+    assert append(q_heads=8, cache=tb.cache(heads=2 ** 30)) == SHAPE
+    assert append(q_heads=most, tokens=0) == OK
