@@ -43,7 +43,7 @@
 // Balance. Units are numbered sequence by sequence, head by head, tile by tile;
 // their costs (a unit's keys and a fixed part) have a closed form, and every
 // block takes an equal share of the sum, whatever units it belongs to. A unit
-// that is cut (between pairs of key tiles, into pieces of at least kPiece) leaves its parts in the
+// that is cut (between pairs of key tiles, not within kPiece of its ends) leaves its parts in the
 // workspace; at the end the blocks that share it wait for the last one and each
 // join a part of its rows, in block order, so the same inputs give the same bits.
 //

@@ -6,12 +6,14 @@
 
 namespace awq {
 
-// A cut leaves no piece of fewer key tiles than this, for a piece costs its turnaround, its
-// bytes in the workspace and a join: a share that would begin or end there has the
-// whole or nothing of it. With 4 / 6 / 8, 13 ragged prompts take 181 / 174 / 175 us, 16
-// sequences that decode beside three chunks 111 / 109 / 111, 64 that decode with heads of 64
-// 140 / 143 / 148, 8 of 8 new tokens with heads of 256 36 / 39 / 42. Pairs of tiles, so
-// that two slots have the same number (in eights, 4 prompts with heads of 256 took 167 us, not 151).
+// No cut lies within this many key tiles of a unit's ends, for a piece costs its turnaround,
+// its bytes in the workspace and a join: a share that would begin or end there has
+// the whole or nothing of it. Pieces between two cuts are what the blocks' shares make them, two
+// tiles or more (5 new tokens over 2000, 20 heads over 4: pieces of 6, 2, 2 and 6). With 4 / 6 / 8,
+// 13 ragged prompts take 181 / 174 / 175 us, 16 sequences that decode beside three
+// chunks 111 / 109 / 111, 64 that decode with heads of 64 140 / 143 / 148, 8 of 8 new tokens with
+// heads of 256 36 / 39 / 42. Pairs of tiles, so that two slots have the same number (in
+// eights, 4 prompts with heads of 256 took 167 us, not 151).
 constexpr int kPiece = 6, kCutStep = 2;
 
 __host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }

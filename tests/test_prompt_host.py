@@ -32,3 +32,7 @@ def test_copies_begin_on_boundaries(check):
 
 def test_the_largest_batches_are_dealt_to_the_threads(check):
     check("sequences")
+
+
+def test_pieces_of_cut_units(check):
+    check("pieces")
