@@ -148,10 +148,6 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b)
 }
 
 // 32 columns of the warp's 32 lanes; complete after tc_wait_ld32().
-#define AWQ_R32(r, i)                                                                                                            \
-    r[i], r[i + 1], r[i + 2], r[i + 3], r[i + 4], r[i + 5], r[i + 6], r[i + 7], r[i + 8], r[i + 9], r[i + 10], r[i + 11],          \
-        r[i + 12], r[i + 13], r[i + 14], r[i + 15], r[i + 16], r[i + 17], r[i + 18], r[i + 19], r[i + 20], r[i + 21], r[i + 22],   \
-        r[i + 23], r[i + 24], r[i + 25], r[i + 26], r[i + 27], r[i + 28], r[i + 29], r[i + 30], r[i + 31]
 __device__ __forceinline__ void tc_ld32_async(uint32_t taddr, float *r)
 {
     asm volatile(
@@ -174,17 +170,6 @@ __device__ __forceinline__ void tc_wait_ld32(float *r)
                    "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
                  :
                  : "memory");
-}
-__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t *r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-        "r"(r[31])
-        : "memory");
 }
 
 // Shared memory matrix descriptor of V as the B operand, MN-major: rows of 64
