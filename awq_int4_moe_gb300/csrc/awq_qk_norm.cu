@@ -21,8 +21,8 @@
 // access). A row of more than 32 items is read twice, its second time from L1.
 //
 // Bound by the bytes for many tokens (a prompt of 8191: 189 MB, 68 % of the copy
-// bandwidth; what is missing is the latency of a warp's first rows), by the launch and dependent
-// loads for few.
+// bandwidth; what is missing is the latency of a warp's first rows and loads on their way: a
+// multiprocessor holds 32 of its blocks of one warp), by the launch and dependent loads for few.
 #include <algorithm>
 #include <type_traits>
 

@@ -23,7 +23,7 @@ extern "C" {
  * sees its rows 0 .. i:
  *   s[i][j] = scale * (q[i] . k[j]),  j <= i
  *   out[i] = sum_j softmax(s[i])[j] v[j],  lse[i] = log(sum_j exp(s[i][j]))
- * scale is any finite number. What a row does not see does not reach it, NaN and
+ * scale is any finite number; scores past fp32's range count as infinite. What a row does not see does not reach it, NaN and
  * infinities among it; a value of v that is not finite leaves its element of out
  * not finite in every row that sees it. A row whose scores are all -infinity has out =
  * 0 and lse = -infinity. Held in fewer than 32 bits: a weight, which enters the
@@ -49,7 +49,8 @@ extern "C" {
  * workspace: at least awq_prompt_attention_workspace_bytes() of device scratch,
  * 256-byte aligned, zero-filled once before its first use; every call leaves it
  * ready for the next one on the same device (but for one that ended in
- * AWQ_ERR_DEVICE_TIMEOUT: then zero it again). It must not be used by two calls
+ * AWQ_ERR_DEVICE_TIMEOUT, which a block sets that has waited for the others a second longer
+ * than it worked itself: then zero it again). It must not be used by two calls
  * that can run at the same time, nor by calls other than this one and
  * awq_chunk_attention.
  */
@@ -67,7 +68,8 @@ AWQ_API size_t awq_prompt_attention_workspace_bytes(int32_t head_dim);
 /*
  * awq_chunk_attention -- attention of a chunk of new tokens per sequence over
  * the paged cache: the next part of a long prompt, drafted tokens to be
- * verified, single tokens, or a batch that mixes them.
+ * verified, single tokens, or a batch that mixes them. (For a batch of single tokens alone
+ * awq_paged_attention is faster and rounds a weight less: it multiplies it as two terms.)
  * Sequence b has n = cu_seqlens[b + 1] - cu_seqlens[b] new tokens, the rows
  * from cu_seqlens[b] on of q and out, and L = seq_lens[b] tokens in the cache,
  * the new ones among them (appended before the call). Its new token i is at
@@ -77,8 +79,9 @@ AWQ_API size_t awq_prompt_attention_workspace_bytes(int32_t head_dim);
  * as fp16 (exact), a weight over an e4m3 cache as fp16, and a bf16 query over
  * it as fp16 with its row's power of two taken out (off by at most 2^-24 of its
  * row's largest element).
- * Pages past a sequence's last token are not read, nor are the places after it.
- * A length outside [0, max_pages * page_size], a page outside [0, num_pages)
+ * Pages past a sequence's last token are not read, and what the places after it hold does
+ * not reach the output.
+ * A length outside [0, max_pages * page_size] or above 2^31 - 256, a page outside [0, num_pages)
  * that is needed, and cu_seqlens as in awq_prompt_attention set
  * AWQ_ERR_BAD_INDEX; that sequence's output is then undefined.
  * page_table i32[batch][max_pages], row stride table_stride; seq_lens
