@@ -680,8 +680,10 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
         Ring to;                                             // the next stage to fill
         int ordinal = 0;
         // 64 columns of a V tile in 16 bits, made finite from a key on (a multiple of 4 B);
-        // then the stage's arrival. B loads are in flight.
-        auto make_finite = [&](uint32_t tile, int from, uint64_t *bar) {
+        // then the stage's arrival. B loads are in flight. The unit is marked for
+        // not_finite_seen() only where one lies before the unit's last key: past it are the rest of
+        // a page and what another kernel left in the stage, which no row sees.
+        auto make_finite = [&](uint32_t tile, int from, int keys, uint64_t *bar) {
             constexpr int B = G::kGuardWarp ? 4 : 8;
 #pragma unroll 1
             for (int key = from; key < kChunkKeys; key += 4 * B) {
@@ -692,12 +694,28 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                 uint32_t bad = 0;
 #pragma unroll
                 for (int k = 0; k < B; ++k) bad |= not_finite4<C>(v[k]);
+                auto seen = [&](int k) { return key + 4 * k + (lane >> 3) < keys; };
+                auto put = [&](int k, uint4 x) {
+                    sts_v4(at + k * 512, make_uint4(finite_pair<C>(x.x), finite_pair<C>(x.y), finite_pair<C>(x.z), finite_pair<C>(x.w)));
+                };
+                // (hardly ever run, but its registers and length count: rolled, 4 prompts with heads of
+                // 256 take 145 us, not 156; unrolled, 13 ragged prompts with heads of 128 171, not 175)
                 if (bad) {
-                    s_bad[ordinal & 3] = ordinal;
+                    if constexpr (DP > 128) {
+#pragma unroll 1
+                        for (int k = 0; k < B; ++k) {
+                            const uint4 x = lds_v4(at + k * 512);
+                            if (not_finite4<C>(x) && seen(k)) s_bad[ordinal & 3] = ordinal;
+                            put(k, x);
+                        }
+                    } else {
+                        bool mark = false;
 #pragma unroll
-                    for (int k = 0; k < B; ++k)
-                        sts_v4(at + k * 512, make_uint4(finite_pair<C>(v[k].x), finite_pair<C>(v[k].y), finite_pair<C>(v[k].z),
-                                                        finite_pair<C>(v[k].w)));
+                        for (int k = 0; k < B; ++k) mark |= not_finite4<C>(v[k]) && seen(k);
+                        if (mark) s_bad[ordinal & 3] = ordinal;
+#pragma unroll
+                        for (int k = 0; k < B; ++k) put(k, v[k]);
+                    }
                 }
             }
             fence_proxy_async();
@@ -776,9 +794,11 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     const Unit u = *next;
                     load_q(u, ordinal);
                     Tiles t(u);
+                    // the first tile that is guarded, and the unit's keys in the last one
+                    const int guarded_from = u.all0 / kChunkKeys - u.k0, last_keys = u.keys - (u.k1 - 1) * kChunkKeys;
 #pragma unroll 1
                     while (t.more()) {
-                        const bool guard = guarded(u, t.is_v(), (u.k0 + t.tile()) * kChunkKeys);
+                        const bool guard = t.is_v() && t.v >= guarded_from;
                         t.next();
 #pragma unroll 1
                         for (int hh = 0; hh < HV; ++hh) {
@@ -799,7 +819,10 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                                     uint4 lo, hi;
                                     expand(lds_v4(from + i * step), lo, hi);
                                     if (not_finite4<C>(lo) | not_finite4<C>(hi)) {
-                                        s_bad[ordinal & 3] = ordinal;
+                                        // (marked as in make_finite(); t.v is V's tile after this one, and the
+                                        // row comes from its address: registers are short)
+                                        if (t.v < t.n || static_cast<int>((from + i * step - raw0) / code_row % kChunkKeys) < last_keys)
+                                            s_bad[ordinal & 3] = ordinal;
                                         lo = make_uint4(finite_pair<C>(lo.x), finite_pair<C>(lo.y), finite_pair<C>(lo.z), finite_pair<C>(lo.w));
                                         hi = make_uint4(finite_pair<C>(hi.x), finite_pair<C>(hi.y), finite_pair<C>(hi.z), finite_pair<C>(hi.w));
                                     }
@@ -869,7 +892,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                         } else if (guard) {
                             wait(raw_full, guard_phase);
                             guard_phase ^= 1;
-                            make_finite(dst, part ? 0 : kChunkKeys, &full[to.i]);
+                            make_finite(dst, part ? 0 : kChunkKeys, u.keys - key0, &full[to.i]);
                         }
                         to.next(NST);
                         ++filled;
@@ -897,7 +920,7 @@ __global__ void __launch_bounds__(ChunkGeo<DP, FP8>::kThreads, 1)
                     wait(&raw_full[st], phases >> st & 1);
                     phases ^= 1u << st;
                     // its keys that some row does not see, from a multiple of 16 on
-                    make_finite(smem_u32(stages) + st * G::kStage, max(0, all0 - (k0 + j) * kChunkKeys) & ~15, &full[st]);
+                    make_finite(smem_u32(stages) + st * G::kStage, max(0, all0 - (k0 + j) * kChunkKeys) & ~15, u.keys - (k0 + j) * kChunkKeys, &full[st]);
                 }
                 base += 2 * n;
                 __syncwarp();
