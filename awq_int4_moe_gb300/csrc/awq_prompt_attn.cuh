@@ -54,9 +54,9 @@
 // turnaround (its last product, the stores, the next one's Q: 9000 cycles). Narrow
 // units: the bytes of K and V (87 % of the copy bandwidth); over e4m3 the warps that copy
 // and expand (some 1200 cycles a tile each), beside softmax warps that take rows of padding too. Small calls: launch, scan, and some ten dependent steps.
-// Device time: one prompt of 8192 tokens, 32 heads over 8 of 128, 405 us (1.36
-// PFLOP/s); 1024 tokens over 32768, 386 us; 13 ragged prompts up to 1999, 172 us; 4
-// prompts with heads of 256, 150 us; 4 new tokens for each of 32 sequences over an e4m3
+// Device time: one prompt of 8192 tokens, 32 heads over 8 of 128, 410 us (1.34
+// PFLOP/s); 1024 tokens over 32768, 391 us; 13 ragged prompts up to 1999, 171 us; 4
+// prompts with heads of 256, 143 us; 4 new tokens for each of 32 sequences over an e4m3
 // cache, 150 us (3.6 TB/s of it); a prompt of 48, 11 us.
 // Tried, and slower: the scores read twice from tensor memory instead of kept in
 // registers, the first weights taken against the old maximum before the new one

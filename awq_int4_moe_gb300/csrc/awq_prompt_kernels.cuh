@@ -49,9 +49,9 @@ constexpr int kChunkKeys = 128;                                       // tokens 
 constexpr int chunk_rows(int padded_dim) { return padded_dim <= 128 ? 256 : 128; }
 // A unit's fixed part of its cost (Q, turnaround, stores), in tokens of its keys: as two
 // key tiles of 2750 cycles each. The turnaround itself is 9000; what of it counts was found by
-// timing. With 128 / 256 / 384 / 512, 13 ragged prompts take 190 / 172 / 187 / 186 us, 4 with
-// heads of 256 181 / 150 / 146 / 150, one of 8192 tokens 406 / 409 / 409 / 418, 40 short ones with heads of 64
-// 77 / 78 / 77 / 74, 4 new tokens of 32 sequences over e4m3 151 / 150 / 145 / 143.
+// timing. With 128 / 256 / 384 / 512, 13 ragged prompts take 190 / 171 / 187 / 184 us, 4 with
+// heads of 256 173 / 143 / 146 / 150, one of 8192 tokens 408 / 411 / 412 / 422, 40 short ones with heads of 64
+// 77 / 78 / 76 / 74, 4 new tokens of 32 sequences over e4m3 151 / 150 / 145 / 143.
 constexpr int64_t kChunkUnitCost = 256;
 constexpr int kChunkNarrowCost = 384;          // over e4m3 more for one with both slots on the same rows
 // e4m3 codes on their way to fp16: their shared memory, and the bytes from one row of a

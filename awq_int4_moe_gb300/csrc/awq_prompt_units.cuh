@@ -10,10 +10,10 @@ namespace awq {
 // its bytes in the workspace and a join: a share that would begin or end there has
 // the whole or nothing of it. Pieces between two cuts are what the blocks' shares make them, two
 // tiles or more (5 new tokens over 2000, 20 heads over 4: pieces of 6, 2, 2 and 6). With 4 / 6 / 8,
-// 13 ragged prompts take 181 / 172 / 171 us, 16 sequences that decode beside three
-// chunks 111 / 107 / 107, 64 of up to 3000 that decode with heads of 64 83 / 85 / 91 over fp16 and 138 / 79 / 81 over
+// 13 ragged prompts take 179 / 171 / 171 us, 16 sequences that decode beside three
+// chunks 110 / 107 / 108, 64 of up to 3000 that decode with heads of 64 83 / 85 / 90 over fp16 and 76 / 79 / 80 over
 // e4m3, 8 of 8 new tokens over 4000 with heads of 256 37 / 42 / 46. Pairs of tiles, so that two slots have
-// the same number (in eights, 4 prompts with heads of 256 take 158 us, not 150).
+// the same number (in eights, 4 prompts with heads of 256 take 153 us, not 143).
 constexpr int kPiece = 6, kCutStep = 2;
 
 __host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
@@ -88,10 +88,10 @@ __host__ __device__ __forceinline__ Span sequences_of(int batch, int thread, int
 // Costs of a sequence's units for one KV head: unit i costs lin + R (i + 1), in
 // keys times G (so that all sequences count alike). A narrow one by itself costs 7/8 of
 // that (half the products, but as many bytes: 16 sequences that decode beside three
-// chunks 107 us, with a factor of 1 112; it changes nothing else measured), over e4m3 with a larger fixed
+// chunks 107 us, with a factor of 1 113; nothing else measured changes by more than 1 %), over e4m3 with a larger fixed
 // part, as its first tiles wait for their expansion. With none / 384 / 768 keys' time more, 4 new tokens of 32
-// sequences take 171 / 150 / 143 us, 16 beside chunks 105 / 107 / 111, 64 that decode with heads of 64
-// 75 / 79 / 81; over 16 bits 384 cost those 85 -> 91 us.
+// sequences take 172 / 150 / 143 us, 16 beside chunks 106 / 107 / 110, 64 that decode with heads of 64
+// 74 / 79 / 81; over 16 bits 384 cost those 85 -> 90 us.
 struct Costs {
     int64_t lin, head;
     int T, R;

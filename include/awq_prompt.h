@@ -107,7 +107,7 @@ AWQ_API awq_status awq_chunk_attention(const awq_heads *q, const awq_kv_cache *c
  * in fp32; y is rotated (and copied past rotary_dim) without being rounded in
  * between. v is appended as it is. The squares are added in fp32: a head whose
  * sum passes its range (finite bf16 values can) has y = 0, and squares below its
- * range count as 0.
+ * range count as 0. A weight of k divided by its e4m3 plane's scale has to stay in that range, too.
  * q_weight, k_weight: 16-bit [head_dim] of the activations' type, 2-byte
  * aligned; eps >= 0 and finite. All else as in awq_rope_append.
  */
