@@ -24,11 +24,12 @@ def test_parts_that_never_come(dim, cache, lens):
     import awq_int4_moe_gb300 as awq
     c = Case(lens, [1] * len(lens), 4, 2, dim, "f16", cache, 64, seed=dim)
     ws = torch.zeros(awq.prompt_attention_workspace_bytes(dim), dtype=torch.uint8, device="cuda")
+    assert c.call(workspace=ws)[2] == 0                                 # (loads the kernel)
     ws.view(torch.int32)[0:320:2] = -1000
     torch.cuda.synchronize()
     t0 = time.monotonic()
     assert c.call(workspace=ws)[2] == awq.ERR_DEVICE_TIMEOUT
-    assert 0.9 < time.monotonic() - t0 < 3
+    assert 0.9 < time.monotonic() - t0 < 6
     ws.zero_()
     for _ in range(2):
         out, lse, st = c.call(workspace=ws)
