@@ -30,7 +30,8 @@
 // step); 8 and 9 issue the MMAs of a slot each; the rest load (and make V finite where
 // rows are masked). Units are found one
 // ahead of their use, by warp 9, or over e4m3 by warp 11. All meet at mbarriers, every
-// wait is bounded (2^18 tries within a block, a time for other blocks). Registers go where the scores are (208 or 200 a thread there): with 227 KB
+// wait is bounded (2^18 tries within a block, a time for other blocks). Registers go
+// where the scores are (208 or 200 a thread there): with 227 KB
 // of shared memory in use what spills comes back from L2.
 //
 // Copies are TMA boxes into 128-byte swizzled stages of 128 keys x 128 columns: of K
@@ -53,7 +54,8 @@
 // instruction) and product of a slot is not quite hidden by the other's. Then a unit's
 // turnaround (its last product, the stores, the next one's Q: 9000 cycles). Narrow
 // units: the bytes of K and V (87 % of the copy bandwidth); over e4m3 the warps that copy
-// and expand (some 1200 cycles a tile each), beside softmax warps that take rows of padding too. Small calls: launch, scan, and some ten dependent steps.
+// and expand (some 1200 cycles a tile each), beside softmax warps that take rows of
+// padding too. Small calls: launch, scan, and some ten dependent steps.
 // Device time: one prompt of 8192 tokens, 32 heads over 8 of 128, 410 us (1.34
 // PFLOP/s); 1024 tokens over 32768, 391 us; 13 ragged prompts up to 1999, 171 us; 4
 // prompts with heads of 256, 143 us; 4 new tokens for each of 32 sequences over an e4m3

@@ -23,7 +23,8 @@ extern "C" {
  * sees its rows 0 .. i:
  *   s[i][j] = scale * (q[i] . k[j]),  j <= i
  *   out[i] = sum_j softmax(s[i])[j] v[j],  lse[i] = log(sum_j exp(s[i][j]))
- * scale is any finite number; scores past fp32's range count as infinite. What a row does not see does not reach it, NaN and
+ * scale is any finite number; scores past fp32's range count as infinite.
+ * What a row does not see does not reach it, NaN and
  * infinities among it; a value of v that is not finite leaves its element of out
  * not finite in every row that sees it. A row whose scores are all -infinity has out =
  * 0 and lse = -infinity. Held in fewer than 32 bits: a weight, which enters the
